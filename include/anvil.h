@@ -263,6 +263,116 @@ int anvil_bank_update_dev(const void* grad, int grad_dtype, float* velocity,
                           const float* eff_lr, int64_t g, int64_t m, int64_t n, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Training operators around a bank: the layers whose gradients the bank step takes.
+ *
+ * Conventions on top of those above:
+ *   - Matrices of activations are [rows][width] with a pitch (ld*, in elements, >= width; any
+ *     value for a single row; at most 2^22) between rows; weights are contiguous.  Any widths,
+ *     pitches and element-aligned pointers are taken (rows < 2^31, widths <= 2^22, one weight
+ *     matrix <= 2^30 elements); the linear layers run fastest when widths and pitches are
+ *     multiples of 8 and pointers 16-byte aligned.  An output may not share memory with another
+ *     argument (ANVIL_ERR_ALIAS); column ranges of one buffer at one pitch do not.
+ *   - Calls allocate nothing, never synchronise and may be captured into a HIP graph (the first
+ *     call of each kind outside capture: it sets kernel attributes once).  Where a call takes a
+ *     workspace, it needs the bytes its *_workspace function gives, 256-byte aligned; 0 bytes
+ *     means none is needed (it may be NULL).  Its contents need not be kept between calls.
+ *   - Sums are fp32; 16-bit outputs are rounded once, to nearest even.  Results do not depend on
+ *     timing: no atomics.
+ * ------------------------------------------------------------------------------------------ */
+enum anvil_dtype { ANVIL_F32 = 0, ANVIL_BF16 = 1, ANVIL_F16 = 2 };
+
+/* act(z): z; max(z, 0); max(z, 0)^2; z Phi(z) with the normal distribution function Phi (the erf
+ * form); z / (1 + exp(-z)).  NaN passes through. */
+enum anvil_act {
+  ANVIL_ACT_NONE = 0,
+  ANVIL_ACT_RELU = 1,
+  ANVIL_ACT_RELU2 = 2,
+  ANVIL_ACT_GELU = 3,
+  ANVIL_ACT_SILU = 4
+};
+
+/* Layer norm over the columns: mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ * y = (x - mean) rstd weight + bias.
+ *   x, y         dtype [rows][cols] at pitches ldx, ldy
+ *   weight, bias [cols] of param_dtype (ANVIL_F32 or dtype), each may be NULL (1 and 0)
+ *   mean, rstd   fp32 [rows], for the backward pass; each may be NULL */
+int anvil_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias,
+                     int param_dtype, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                     int dtype, int64_t rows, int64_t cols, void* stream);
+
+/* Its backward pass, with h = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean_c(g) - h mean_c(g h)),  dweight = sum over rows of dy h,
+ *   dbias = sum over rows of dy.
+ *   dweight, dbias  fp32 [cols], each may be NULL; zeros when there are no rows
+ *   workspace       needed when either is given */
+int anvil_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          const void* weight, int param_dtype, const float* mean,
+                          const float* rstd, void* dx, int64_t lddx, float* dweight, float* dbias,
+                          int dtype, int64_t rows, int64_t cols, void* workspace,
+                          size_t workspace_bytes, void* stream);
+size_t anvil_layer_norm_grad_workspace(int64_t rows, int64_t cols);
+
+/* Linear layer: z = x w^T + bias (w_kn = 0: w [n][k]) or x w + bias (w_kn = 1: w [k][n]);
+ * y = act(z) + residual.
+ *   dtype      ANVIL_BF16 or ANVIL_F16: x, w, residual, y, preact
+ *   bias       [n] of bias_dtype (ANVIL_F32 or dtype), or NULL
+ *   residual   [rows][n] or NULL
+ *   preact     receives z [rows][n] (rounded to dtype; y is formed from the unrounded z), or NULL */
+int anvil_linear(const void* x, int64_t ldx, const void* w, int w_kn, const void* bias,
+                 int bias_dtype, int act, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                 void* preact, int64_t ldz, int dtype, int64_t rows, int64_t n, int64_t k,
+                 void* stream);
+
+/* Gradient of its input, dx = (dz w) * act'(preact) + add (dz w^T for w_kn = 1).
+ *   preact     [rows][k]: the preactivation that x = act(preact) came from, so that dx is the dz of
+ *              the layer before; not read (and may be NULL) for ANVIL_ACT_NONE
+ *   add        [rows][k] or NULL: the gradient that reaches x another way (a residual) */
+int anvil_linear_grad_input(const void* dz, int64_t lddz, const void* w, int w_kn,
+                            const void* preact, int64_t ldz, int act, const void* add,
+                            int64_t ldadd, void* dx, int64_t lddx, int dtype, int64_t rows,
+                            int64_t n, int64_t k, void* stream);
+
+/* Gradient of its weight and bias: dw = dz^T x [n][k] (w_kn = 0) or x^T dz [k][n] (w_kn = 1), of
+ * dw_dtype (ANVIL_F32 or dtype): a bank's gradient.  dbias = sum over rows of dz, fp32 [n], or
+ * NULL.  Both are zeros when there are no rows. */
+int anvil_linear_grad_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, int w_kn,
+                             void* dw, int dw_dtype, float* dbias, int dtype, int64_t rows,
+                             int64_t n, int64_t k, void* workspace, size_t workspace_bytes,
+                             void* stream);
+/* Workspace of the weight gradient; experts = 1 for anvil_linear_grad_weight. */
+size_t anvil_linear_grad_weight_workspace(int w_kn, int64_t rows, int64_t n, int64_t k,
+                                          int64_t experts);
+
+/* dz = dy * act'(preact), elementwise over [rows][n] (dtype ANVIL_BF16 or ANVIL_F16). */
+int anvil_activation_grad(const void* dy, int64_t lddy, const void* preact, int64_t ldz, int act,
+                          void* dz, int64_t lddz, int dtype, int64_t rows, int64_t n,
+                          void* stream);
+
+/* The same three products for a stack of experts over ragged groups of rows: w is [experts][n][k]
+ * (or [experts][k][n]), bias [experts][n], dw and dbias likewise, and rows offsets[e] ..
+ * offsets[e + 1] - 1 belong to expert e.
+ *   offsets    DEVICE integers [experts + 1] of offset_bits (32 or 64), read when the kernels run
+ *              (the host never sees them).  They should not decrease and lie in 0 .. rows; the
+ *              kernels take their running maximum clamped to that range, so that other values
+ *              give other groups but no access out of range.
+ * Rows before offsets[0] or from offsets[experts] on belong to no expert: y, preact and dx get
+ * zeros there (without residual or add), and dw does not see them.  An expert without rows gets
+ * zeros in dw and dbias.  experts <= 65535. */
+int anvil_expert_linear(const void* x, int64_t ldx, const void* w, int w_kn, const void* offsets,
+                        int offset_bits, int64_t experts, const void* bias, int bias_dtype, int act,
+                        const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact,
+                        int64_t ldz, int dtype, int64_t rows, int64_t n, int64_t k, void* stream);
+int anvil_expert_grad_input(const void* dz, int64_t lddz, const void* w, int w_kn,
+                            const void* offsets, int offset_bits, int64_t experts,
+                            const void* preact, int64_t ldz, int act, const void* add,
+                            int64_t ldadd, void* dx, int64_t lddx, int dtype, int64_t rows,
+                            int64_t n, int64_t k, void* stream);
+int anvil_expert_grad_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, int w_kn,
+                             const void* offsets, int offset_bits, int64_t experts, void* dw,
+                             int dw_dtype, float* dbias, int dtype, int64_t rows, int64_t n,
+                             int64_t k, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

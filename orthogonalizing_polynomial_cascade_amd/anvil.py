@@ -57,6 +57,25 @@ SIGNATURES = {
                                   _vp]),
     "anvil_equalize": (_i, [_vp, _vp, _d, _vp, _i64, _i64, _i64, _vp]),
     "anvil_decay_update": (_i, [_vp, _vp, _vp, _f, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "anvil_layer_norm": (_i, [_vp, _i64, _vp, _vp, _i, _f, _vp, _i64, _vp, _vp, _i, _i64, _i64,
+                              _vp]),
+    "anvil_layer_norm_grad": (_i, [_vp, _i64, _vp, _i64, _vp, _i, _vp, _vp, _vp, _i64, _vp, _vp,
+                                   _i, _i64, _i64, _vp, _sz, _vp]),
+    "anvil_layer_norm_grad_workspace": (_sz, [_i64, _i64]),
+    "anvil_linear": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _i,
+                          _i64, _i64, _i64, _vp]),
+    "anvil_linear_grad_input": (_i, [_vp, _i64, _vp, _i, _vp, _i64, _i, _vp, _i64, _vp, _i64, _i,
+                                     _i64, _i64, _i64, _vp]),
+    "anvil_linear_grad_weight": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _i, _i64, _i64,
+                                      _i64, _vp, _sz, _vp]),
+    "anvil_linear_grad_weight_workspace": (_sz, [_i, _i64, _i64, _i64, _i64]),
+    "anvil_activation_grad": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i64, _i, _i64, _i64, _vp]),
+    "anvil_expert_linear": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _i, _i, _vp, _i64, _vp,
+                                 _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp]),
+    "anvil_expert_grad_input": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _i64, _i, _vp, _i64,
+                                     _vp, _i64, _i, _i64, _i64, _i64, _vp]),
+    "anvil_expert_grad_weight": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i, _i64, _vp, _i, _vp, _i,
+                                      _i64, _i64, _i64, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -430,3 +449,292 @@ def rail_scalars(step: int):
     fast rail only before step 514, blend weight 0.4385 on the fast rail from step 514 on; fast
     beta 0.85 and Nesterov momentum 0.95 throughout (the pre-engage beta scheduler is not given)."""
     return 0.95, 0.85, (1.0 if step < 514 else 0.4385)
+
+
+# ---------------------------------------------------------------------------------------------
+# Training operators around a bank.  Activations are [rows, width] tensors whose rows may lie any
+# pitch apart (the last dimension contiguous); weights, biases and offsets are contiguous.
+# ---------------------------------------------------------------------------------------------
+
+ANVIL_F32, ANVIL_BF16, ANVIL_F16 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}
+_dtypes = {}
+
+
+def _dtype_code(t, name, allowed=None):
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: ANVIL_F32, torch.bfloat16: ANVIL_BF16,
+                        torch.float16: ANVIL_F16})
+    code = _dtypes.get(t.dtype)
+    if code is None or (allowed is not None and code not in allowed):
+        raise TypeError(f"{name} has an unsupported dtype ({t.dtype})")
+    return code
+
+
+def _on_gpu(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU (got {t.device})")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.set_device)")
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """Checks a [rows, width] operand and returns its row pitch in elements."""
+    _on_gpu(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, width] (got {t.dim()} dimensions)")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    width, (step, last) = t.shape[1], t.stride()
+    if last != 1 and width > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.shape[0] > 1 and step < width:
+        raise ValueError(f"{name}: its rows overlap (pitch {step}, width {width})")
+    return max(step, width)
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`: memory of another stream than the current one is kept
+    from reuse until that stream is done with it."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        if s != torch.cuda.current_stream():
+            t.record_stream(s)
+    return t
+
+
+def _act(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)} (got {name!r})")
+    return ACTIVATIONS[name]
+
+
+def _scratch(workspace, need, device, stream):
+    """(pointer, bytes) of the workspace: the caller's, or one of `need` bytes."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _empty((need,), torch.uint8, device, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    return _ptr(workspace), workspace.numel(), workspace
+
+
+def anvil_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
+    """Layer norm of each row of x (bf16, fp16 or fp32 [rows, cols]); weight and bias [cols] are
+    fp32 or of x's dtype.  Returns (y, mean, rstd), the last two fp32 [rows] for the backward
+    pass."""
+    import torch
+    ldx = _rows(x, "x")
+    code = _dtype_code(x, "x")
+    rows, cols = x.shape
+    param = code
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            param = _dtype_code(t, name, (ANVIL_F32, code))
+            _need(t, name, t.dtype, (cols,))
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one dtype")
+    if out is None:
+        out = _empty((rows, cols), x.dtype, x.device, stream)
+    ldy = _rows(out, "out", x.dtype, (rows, cols))
+    mean = _empty((rows,), torch.float32, x.device, stream)
+    rstd = _empty((rows,), torch.float32, x.device, stream)
+    _check("anvil_layer_norm", load().anvil_layer_norm(
+        _ptr(x), ldx, _ptr(weight), _ptr(bias), param, eps, _ptr(out), ldy, _ptr(mean), _ptr(rstd),
+        code, rows, cols, _stream(stream)))
+    return out, mean, rstd
+
+
+def anvil_layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, stream=None):
+    """Backward pass of anvil_layer_norm: returns (dx, dweight, dbias), the last two fp32 [cols].
+    Without a weight (None) it was 1; dweight and dbias are returned all the same."""
+    import torch
+    ldx = _rows(x, "x")
+    code = _dtype_code(x, "x")
+    rows, cols = x.shape
+    lddy = _rows(dy, "dy", x.dtype, (rows, cols))
+    param = code
+    if weight is not None:
+        param = _dtype_code(weight, "weight", (ANVIL_F32, code))
+        _need(weight, "weight", weight.dtype, (cols,))
+    _need(mean, "mean", torch.float32, (rows,))
+    _need(rstd, "rstd", torch.float32, (rows,))
+    if out is None:
+        out = _empty((rows, cols), x.dtype, x.device, stream)
+    lddx = _rows(out, "out", x.dtype, (rows, cols))
+    sums = _empty((2, cols), torch.float32, x.device, stream)
+    dweight, dbias = sums[0], sums[1]
+    lib = load()
+    ws, wsb, keep = _scratch(workspace, lib.anvil_layer_norm_grad_workspace(rows, cols), x.device,
+                             stream)
+    _check("anvil_layer_norm_grad", lib.anvil_layer_norm_grad(
+        _ptr(dy), lddy, _ptr(x), ldx, _ptr(weight), param, _ptr(mean), _ptr(rstd), _ptr(out), lddx,
+        _ptr(dweight), _ptr(dbias), code, rows, cols, ws, wsb, _stream(stream)))
+    return out, dweight, dbias
+
+
+def _weight(w, x, w_kn, experts):
+    """(n, k) of a weight matrix or stack of x's dtype."""
+    _need(w, "w", x.dtype)
+    if w.dim() != (2 if experts is None else 3):
+        raise ValueError("w must be [n, k], or [experts, n, k] for experts")
+    if experts is not None and w.shape[0] != experts:
+        raise ValueError(f"w holds {w.shape[0]} experts, offsets {experts}")
+    n, k = w.shape[-2:]
+    return (k, n) if w_kn else (n, k)
+
+
+def _offsets(offsets):
+    """(pointer, bits, experts) of the row offsets."""
+    import torch
+    _on_gpu(offsets, "offsets")
+    if offsets.dtype not in (torch.int32, torch.int64):
+        raise TypeError("offsets must be int32 or int64")
+    if offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous [experts + 1] tensor")
+    return _ptr(offsets), 32 if offsets.dtype == torch.int32 else 64, offsets.numel() - 1
+
+
+def _linear(fn, x, w, offsets, bias, residual, act, w_kn, keep_preact, preact, out, stream):
+    ldx = _rows(x, "x")
+    code = _dtype_code(x, "x", (ANVIL_BF16, ANVIL_F16))
+    group = () if offsets is None else _offsets(offsets)
+    experts = group[2] if group else None
+    n, k = _weight(w, x, w_kn, experts)
+    rows = x.shape[0]
+    if x.shape[1] != k:
+        raise ValueError(f"x has width {x.shape[1]}, w takes {k}")
+    bias_code = code
+    if bias is not None:
+        bias_code = _dtype_code(bias, "bias", (ANVIL_F32, code))
+        _need(bias, "bias", bias.dtype, (n,) if experts is None else (experts, n))
+    ldr = _rows(residual, "residual", x.dtype, (rows, n)) if residual is not None else 0
+    if out is None:
+        out = _empty((rows, n), x.dtype, x.device, stream)
+    ldy = _rows(out, "out", x.dtype, (rows, n))
+    if preact is None and keep_preact:
+        preact = _empty((rows, n), x.dtype, x.device, stream)
+    ldz = _rows(preact, "preact", x.dtype, (rows, n)) if preact is not None else 0
+    _check(fn, getattr(load(), fn)(
+        _ptr(x), ldx, _ptr(w), int(w_kn), *group, _ptr(bias), bias_code, _act(act), _ptr(residual),
+        ldr, _ptr(out), ldy, _ptr(preact), ldz, code, rows, n, k, _stream(stream)))
+    return out, preact
+
+
+def _grad_input(fn, dz, w, offsets, preact, act, add, w_kn, out, stream):
+    lddz = _rows(dz, "dz")
+    code = _dtype_code(dz, "dz", (ANVIL_BF16, ANVIL_F16))
+    group = () if offsets is None else _offsets(offsets)
+    n, k = _weight(w, dz, w_kn, group[2] if group else None)
+    rows = dz.shape[0]
+    if dz.shape[1] != n:
+        raise ValueError(f"dz has width {dz.shape[1]}, w gives {n}")
+    ldz = _rows(preact, "preact", dz.dtype, (rows, k)) if preact is not None else 0
+    ldadd = _rows(add, "add", dz.dtype, (rows, k)) if add is not None else 0
+    if out is None:
+        out = _empty((rows, k), dz.dtype, dz.device, stream)
+    lddx = _rows(out, "out", dz.dtype, (rows, k))
+    _check(fn, getattr(load(), fn)(
+        _ptr(dz), lddz, _ptr(w), int(w_kn), *group, _ptr(preact), ldz, _act(act), _ptr(add), ldadd,
+        _ptr(out), lddx, code, rows, n, k, _stream(stream)))
+    return out
+
+
+def _grad_weight(fn, dz, x, offsets, w_kn, out, out_dtype, want_bias, workspace, stream):
+    import torch
+    lddz = _rows(dz, "dz")
+    code = _dtype_code(dz, "dz", (ANVIL_BF16, ANVIL_F16))
+    rows, n = dz.shape
+    ldx = _rows(x, "x", dz.dtype)
+    k = x.shape[1]
+    if x.shape[0] != rows:
+        raise ValueError(f"x has {x.shape[0]} rows, dz {rows}")
+    group = () if offsets is None else _offsets(offsets)
+    stack = (group[2],) if group else ()
+    shape = stack + ((k, n) if w_kn else (n, k))
+    if out is None:
+        out = _empty(shape, out_dtype or torch.float32, dz.device, stream)
+    out_code = _dtype_code(out, "out", (ANVIL_F32, code))
+    _need(out, "out", out.dtype, shape)
+    dbias = _empty(stack + (n,), torch.float32, dz.device, stream) if want_bias else None
+    lib = load()
+    need = lib.anvil_linear_grad_weight_workspace(int(w_kn), rows, n, k, stack[0] if stack else 1)
+    ws, wsb, keep = _scratch(workspace, need, dz.device, stream)
+    _check(fn, getattr(lib, fn)(
+        _ptr(dz), lddz, _ptr(x), ldx, int(w_kn), *group, _ptr(out), out_code, _ptr(dbias), code,
+        rows, n, k, ws, wsb, _stream(stream)))
+    return out, dbias
+
+
+def anvil_linear(x, w, bias=None, residual=None, act="none", w_kn=False, keep_preact=False,
+                 preact=None, out=None, stream=None):
+    """Linear layer y = act(x w^T + bias) + residual with w [n, k] (w_kn: x w, w [k, n]); x bf16 or
+    fp16 [rows, k], act one of ACTIVATIONS, bias fp32 or of x's dtype.  Returns (y, z), z the
+    preactivation x w^T + bias where keep_preact asks for it or `preact` receives it, else None."""
+    return _linear("anvil_linear", x, w, None, bias, residual, act, w_kn, keep_preact, preact, out,
+                   stream)
+
+
+def anvil_linear_grad_input(dz, w, preact=None, act="none", add=None, w_kn=False, out=None,
+                            stream=None):
+    """dx = (dz w) * act'(preact) + add: the gradient of a linear layer's input x = act(preact)
+    with respect to preact; add is a gradient that reaches it another way (a residual)."""
+    return _grad_input("anvil_linear_grad_input", dz, w, None, preact, act, add, w_kn, out, stream)
+
+
+def anvil_linear_grad_weight(dz, x, w_kn=False, out=None, out_dtype=None, want_bias=True,
+                             workspace=None, stream=None):
+    """(dw, dbias): dw = dz^T x [n, k] (w_kn: x^T dz [k, n]), fp32 or dz's dtype, and the fp32 sum of
+    dz over the rows (None without want_bias)."""
+    return _grad_weight("anvil_linear_grad_weight", dz, x, None, w_kn, out, out_dtype, want_bias,
+                        workspace, stream)
+
+
+def anvil_activation_grad(dy, preact, act, out=None, stream=None):
+    """dz = dy * act'(preact), elementwise on [rows, n]."""
+    lddy = _rows(dy, "dy")
+    code = _dtype_code(dy, "dy", (ANVIL_BF16, ANVIL_F16))
+    rows, n = dy.shape
+    ldz = _rows(preact, "preact", dy.dtype, (rows, n))
+    if out is None:
+        out = _empty((rows, n), dy.dtype, dy.device, stream)
+    lddz = _rows(out, "out", dy.dtype, (rows, n))
+    _check("anvil_activation_grad", load().anvil_activation_grad(
+        _ptr(dy), lddy, _ptr(preact), ldz, _act(act), _ptr(out), lddz, code, rows, n,
+        _stream(stream)))
+    return out
+
+
+def anvil_expert_linear(x, w, offsets, bias=None, residual=None, act="none", w_kn=False,
+                        keep_preact=False, preact=None, out=None, stream=None):
+    """anvil_linear for a stack of experts: rows offsets[e] .. offsets[e + 1] - 1 of x go through
+    w[e] (w [experts, n, k], bias [experts, n], offsets int32 or int64 [experts + 1] on the GPU).
+    Rows outside every expert's range give zeros."""
+    return _linear("anvil_expert_linear", x, w, offsets, bias, residual, act, w_kn, keep_preact,
+                   preact, out, stream)
+
+
+def anvil_expert_grad_input(dz, w, offsets, preact=None, act="none", add=None, w_kn=False, out=None,
+                            stream=None):
+    """anvil_linear_grad_input over the experts' groups of rows."""
+    return _grad_input("anvil_expert_grad_input", dz, w, offsets, preact, act, add, w_kn, out,
+                       stream)
+
+
+def anvil_expert_grad_weight(dz, x, offsets, w_kn=False, out=None, out_dtype=None, want_bias=True,
+                             workspace=None, stream=None):
+    """anvil_linear_grad_weight over the experts' groups of rows: dw [experts, n, k], the gradient
+    stack of the experts' bank, and dbias [experts, n]."""
+    return _grad_weight("anvil_expert_grad_weight", dz, x, offsets, w_kn, out, out_dtype, want_bias,
+                        workspace, stream)

@@ -1,0 +1,45 @@
+// Activations of the linear layers and their derivatives, in fp32.  Comparisons are written so that
+// NaN passes through (a maximum against zero would drop it).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace anvil {
+
+enum Act { kActNone = 0, kActRelu = 1, kActRelu2 = 2, kActGelu = 3, kActSilu = 4 };
+
+__device__ __forceinline__ float relu(float z) { return z < 0.0f ? 0.0f : z; }
+
+// Standard normal distribution function.
+__device__ __forceinline__ float normal_cdf(float z) {
+  return 0.5f * erfcf(-0.70710678118654752f * z);
+}
+
+__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float act_value(int act, float z) {
+  switch (act) {
+    case kActRelu: return relu(z);
+    case kActRelu2: { const float r = relu(z); return r * r; }
+    case kActGelu: return z * normal_cdf(z);
+    case kActSilu: return z * logistic(z);
+    default: return z;
+  }
+}
+
+// d act / dz; 0 at z = 0 for the two rectifiers.
+__device__ __forceinline__ float act_slope(int act, float z) {
+  switch (act) {
+    case kActRelu: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    case kActRelu2: return 2.0f * relu(z);
+    case kActGelu:
+      return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), normal_cdf(z));
+    case kActSilu: {
+      const float s = logistic(z);
+      return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace anvil

@@ -9,7 +9,18 @@
 #include <utility>
 
 #include "../../include/anvil.h"
+#include "api_common.h"
 #include "launchers.h"
+
+namespace {
+thread_local int t_last_hip = 0;
+}
+
+int anvil::hip_status(hipError_t e) {
+  if (e == hipSuccess) return ANVIL_OK;
+  t_last_hip = static_cast<int>(e);
+  return ANVIL_ERR_HIP;
+}
 
 namespace {
 
@@ -38,20 +49,9 @@ constexpr int kMaxMaps = 16;
 // Banks with more rows than this use the split (two-rounding) apply (anvil.py).
 constexpr int64_t kSplitMinRows = 1024;
 
-thread_local int t_last_hip = 0;
-
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return ANVIL_OK;
-  t_last_hip = static_cast<int>(e);
-  return ANVIL_ERR_HIP;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
+using anvil::aligned;
+using anvil::hip_status;
+using anvil::overlap;
 
 // Shape checks shared by every entry point.  Returns ANVIL_OK with *empty set for a zero-size
 // stack.

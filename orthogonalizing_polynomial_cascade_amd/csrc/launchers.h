@@ -62,4 +62,90 @@ hipError_t launch_equalize(uint16_t* u, float* lane_energy, double beta2, float*
 hipError_t launch_decay(uint16_t* param, uint16_t* mantissa, const uint16_t* u, float wd,
                         const float* lr, const float* gate, const Shape& sh, hipStream_t stream);
 
+// ---- training operators (norm.hip, linear.hip; checked by train_api.hip) ----
+
+enum ElemType { kF32 = 0, kBf16 = 1, kF16 = 2 };
+
+// Layer norm of `rows` rows; in the backward pass y / ldy are dx / lddx.
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* weight;
+  const void* bias;
+  bool param_f32;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  int type;
+  int64_t rows;
+  int cols;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+// Partial rows (of 2 * cols fp32) that launch_norm_grad leaves in `partial`.
+int norm_grad_blocks(int64_t rows, int cols);
+hipError_t launch_norm_grad(const NormArgs& a, const void* dy, int64_t lddy, float* dweight,
+                            float* dbias, float* partial, hipStream_t stream);
+
+// Rows in groups: group e owns rows [offsets[e], offsets[e + 1]) (device integers of 4 or 8
+// bytes), and matrix e of a stack.  Without offsets all rows belong to one matrix.
+struct Groups {
+  const void* offsets;   // or null
+  bool wide;             // 64-bit offsets
+  int count;
+};
+
+// out[r][c] = epilogue(sum_d a[r][d] * b(c, d)), b of the row's group.
+//   forward   z = sum + bias;  keep = z;  out = act(z) + add
+//   gradient  out = sum * act'(aux) + add
+struct RowsProduct {
+  const void* a;
+  int64_t lda;
+  const void* b;
+  bool b_kmajor;         // b stored [d][c] instead of [c][d]
+  int64_t rows;
+  int cols, depth;
+  Groups groups;
+  bool f16;
+  bool gradient;
+  int act;
+  const void* bias;      // [groups][cols] or null
+  bool bias_f32;
+  const void* aux;       // gradient: preactivation, or null
+  int64_t ldaux;
+  const void* add;       // or null
+  int64_t ldadd;
+  void* keep;            // or null
+  int64_t ldkeep;
+  void* out;
+  int64_t ldout;
+};
+hipError_t launch_rows_product(const RowsProduct& a, hipStream_t stream);
+
+// dw[e][i][j] = sum over the rows r of group e of p[r][i] * q[r][j], and the column sums of
+// whichever of the two is dz.
+struct WeightProduct {
+  const void* p;
+  int64_t ldp;
+  const void* q;
+  int64_t ldq;
+  int64_t rows;
+  int pi, qj;
+  bool dz_is_q;
+  Groups groups;
+  bool f16;
+  void* dw;
+  bool dw_f32;
+  float* db;             // [groups][width of dz] or null
+};
+// Fp32 words of workspace for the product (0: none needed).
+size_t weight_product_words(const WeightProduct& a);
+hipError_t launch_weight_product(const WeightProduct& a, float* ws, hipStream_t stream);
+
+// dz = dy * act'(z), elementwise.
+hipError_t launch_activation_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
+                                  void* dz, int64_t lddz, bool f16, int64_t rows, int cols,
+                                  hipStream_t stream);
+
 }  // namespace anvil

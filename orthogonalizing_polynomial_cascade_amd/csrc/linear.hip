@@ -1,0 +1,412 @@
+// The linear layers that a bank's matrices belong to: products of activations with a weight matrix
+// (or a stack of them, one per expert) with their epilogue, and the two gradient products.
+//
+//   rows product    out[r][c] = epilogue(sum_d a[r][d] b(c, d))      forward and input gradient
+//   weight product  dw[i][j]  = sum_r p[r][i] q[r][j]                weight gradient (a bank's grad)
+//
+// Both are  C[i][j] = sum_k P(i, k) Q(j, k)  with fp32 accumulation on the matrix cores and one
+// rounding at the end; an operand is "K-contiguous" (k runs along its rows in memory) or "K-major"
+// (k runs down its rows).
+//
+// Groups (experts): rows are sorted by expert and the kernels read the row offsets themselves.  The
+// offsets are taken as a running maximum clamped to [0, rows], so that every row has at most one
+// owner and no access leaves the buffers whatever they hold; a row without an owner (before the
+// first offset or past the last) gets an output row of zeros.
+#include <algorithm>
+#include <atomic>
+
+#include "activation.h"
+#include "device_common.h"
+#include "launchers.h"
+#include "mfma_slab.h"
+#include "scalar_types.h"
+
+namespace anvil {
+
+namespace {
+
+constexpr int64_t kMaxGrid = 1 << 22;   // a launch counts its work-items in 32 bits
+
+template <typename T>
+struct Mfma;
+template <>
+struct Mfma<bf16> {
+  typedef bf16x8_t vec;
+  __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mfma<f16> {
+  typedef f16 vec __attribute__((ext_vector_type(8)));
+  __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// Offset j of the groups, clamped to [0, rows] (not yet a running maximum).
+__device__ __forceinline__ int64_t raw_offset(const Groups& g, int j, int64_t rows) {
+  int64_t v = g.wide ? static_cast<const int64_t*>(g.offsets)[j]
+                     : (int64_t)static_cast<const int32_t*>(g.offsets)[j];
+  return v < 0 ? 0 : (v > rows ? rows : v);
+}
+
+__device__ __forceinline__ int64_t wave_max(int64_t v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const int64_t u = __shfl_xor(v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
+// Rows [*begin, *end) of group e: every wave looks at the offsets up to e + 1.
+__device__ __forceinline__ void group_rows(const Groups& g, int64_t rows, int e, int64_t* begin,
+                                           int64_t* end) {
+  if (!g.offsets) {
+    *begin = 0;
+    *end = rows;
+    return;
+  }
+  int64_t lo = 0;
+  for (int j = threadIdx.x & 63; j <= e; j += 64) {
+    const int64_t v = raw_offset(g, j, rows);
+    lo = v > lo ? v : lo;
+  }
+  lo = wave_max(lo);
+  const int64_t hi = raw_offset(g, e + 1, rows);
+  *begin = lo;
+  *end = hi > lo ? hi : lo;
+}
+
+// The rows in tiles of TILE, group by group; rows without an owner form two groups of their own,
+// before the first and after the last.  Finds tile t: its first row and the end of its group's
+// rows, and its group (-1: no owner).  Returns false past the last tile.
+template <int TILE>
+__device__ __forceinline__ bool row_tile(const Groups& g, int64_t rows, int64_t t, int64_t* row0,
+                                         int64_t* end, int* group) {
+  if (!g.offsets) {
+    *row0 = t * TILE;
+    *end = rows;
+    *group = 0;
+    return *row0 < rows;
+  }
+  // segment s = 0 .. count + 1 spans bound(s) .. bound(s + 1): bound(0) = 0, bound(s) = the running
+  // maximum of the offsets up to s - 1, bound(count + 2) = rows
+  const int lane = threadIdx.x & 63;
+  int64_t start = 0;      // bound at the chunk's first segment
+  int64_t done = 0;       // tiles of the segments before the chunk
+  for (int s0 = 0; s0 < g.count + 2; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t hi = s <= g.count ? raw_offset(g, s, rows) : rows;   // bound(s + 1), to be a maximum
+    hi = hi > start ? hi : start;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(hi, o);
+      if (lane >= o && u > hi) hi = u;
+    }
+    int64_t lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = start;
+    const int64_t mine = (hi - lo + TILE - 1) / TILE;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
+    }
+    const uint64_t past = __ballot(done + upto > t);
+    if (past) {
+      const int who = __ffsll((unsigned long long)past) - 1;
+      const int64_t first = done + __shfl(upto - mine, who);   // tiles before the segment
+      *row0 = __shfl(lo, who) + (t - first) * TILE;
+      *end = __shfl(hi, who);
+      const int seg = s0 + who;
+      *group = seg == 0 || seg > g.count ? -1 : seg - 1;
+      return true;
+    }
+    done += __shfl(upto, 63);
+    start = __shfl(hi, 63);
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------------------------------------
+// The kernels for any width, pitch and alignment: 64x64 tiles, four waves of one 32x32 fragment,
+// operands through registers into LDS.
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kAnyTile = 64;
+constexpr int kAnyDepth = 32;
+constexpr int kAnyPitch = kAnyDepth + 8;   // elements per LDS row: 16-byte slots, spread banks
+
+// One operand of the tile: 64 rows by 32 k, eight elements of one lane.  K-contiguous: element
+// (i, k) at base[i * ld + k]; K-major: at base[k * ld + i].
+template <typename T, bool KMAJOR>
+struct AnySlab {
+  T v[8];
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t i0, int64_t ni,
+                                       int64_t k0, int64_t nk) {
+    const int t = threadIdx.x;
+    const int64_t major = KMAJOR ? k0 + t / 8 : i0 + t / 4;           // the strided index
+    const int64_t minor = KMAJOR ? i0 + (t % 8) * 8 : k0 + (t % 4) * 8;
+    const int64_t nmaj = KMAJOR ? nk : ni, nmin = KMAJOR ? ni : nk;
+    const T* p = base + major * ld + minor;
+    if (major < nmaj && minor + 8 <= nmin) {
+      __builtin_memcpy(v, p, sizeof(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = major < nmaj && minor + e < nmin ? p[e] : from_f32<T>(0.0f);
+    }
+  }
+  __device__ __forceinline__ void store(T (*lds)[kAnyPitch]) const {
+    const int t = threadIdx.x;
+    if constexpr (KMAJOR) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[(t % 8) * 8 + e][t / 8] = v[e];
+    } else {
+      __builtin_memcpy(&lds[t / 4][(t % 4) * 8], v, sizeof(v));
+    }
+  }
+};
+
+// acc (one fragment per wave, C transposed: register r of lane l is row l%32, column
+// 8(r/4) + 4(l/32) + r%4) of the tile's k range [k0, k1).  With `sum`, the wave also adds up its
+// P (sum_p) or Q fragment over k into `sums` (every register of lane l: row or column l%32).
+template <typename T, bool PT, bool QT>
+__device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t i0, int64_t ni,
+                                               const T* Q, int64_t ldq, int64_t j0, int64_t nj,
+                                               int64_t k0, int64_t k1, f32x16_t& acc, bool sum,
+                                               bool sum_p, f32x16_t& sums) {
+  __shared__ __attribute__((aligned(16))) T lp[kAnyTile][kAnyPitch];
+  __shared__ __attribute__((aligned(16))) T lq[kAnyTile][kAnyPitch];
+  typedef typename Mfma<T>::vec vec;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  vec one;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) one[e] = from_f32<T>(1.0f);
+  AnySlab<T, PT> sp;
+  AnySlab<T, QT> sq;
+  if (k0 < k1) {
+    sp.load(P, ldp, i0, ni, k0, k1);
+    sq.load(Q, ldq, j0, nj, k0, k1);
+  }
+  for (int64_t k = k0; k < k1; k += kAnyDepth) {
+    __syncthreads();   // the previous slab's reads are done
+    sp.store(lp);
+    sq.store(lq);
+    __syncthreads();
+    if (k + kAnyDepth < k1) {
+      sp.load(P, ldp, i0, ni, k + kAnyDepth, k1);
+      sq.load(Q, ldq, j0, nj, k + kAnyDepth, k1);
+    }
+#pragma unroll
+    for (int ks = 0; ks < kAnyDepth / 16; ++ks) {
+      const int kk = ks * 16 + 8 * (lane >> 5);
+      const vec fp = *reinterpret_cast<const vec*>(&lp[(wave >> 1) * 32 + (lane & 31)][kk]);
+      const vec fq = *reinterpret_cast<const vec*>(&lq[(wave & 1) * 32 + (lane & 31)][kk]);
+      acc = Mfma<T>::run(fq, fp, acc);
+      if (sum) sums = Mfma<T>::run(one, sum_p ? fp : fq, sums);
+    }
+  }
+}
+
+template <typename T, bool QT>
+__global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int64_t tiles_m, int tiles_n) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t tile = blockIdx.x; tile < tiles_m * tiles_n; tile += gridDim.x) {
+    int64_t row0, end;
+    int group;
+    if (!row_tile<kAnyTile>(p.groups, p.rows, tile / tiles_n, &row0, &end, &group)) return;
+    const int64_t j0 = (tile % tiles_n) * kAnyTile;
+    const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
+    f32x16_t acc = {}, none = {};
+    any_accumulate<T, false, QT>(static_cast<const T*>(p.a), p.lda, row0, end, b,
+                                 QT ? p.cols : p.depth, j0, p.cols, 0, group < 0 ? 0 : p.depth,
+                                 acc, false, false, none);
+    const int64_t r = row0 + (wave >> 1) * 32 + (lane & 31);
+    if (r >= end) continue;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t c = j0 + (wave & 1) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+      if (c >= p.cols) continue;
+      float z = acc[i];
+      if (group < 0) {
+        if (p.keep) static_cast<T*>(p.keep)[r * p.ldkeep + c] = from_f32<T>(0.0f);
+        static_cast<T*>(p.out)[r * p.ldout + c] = from_f32<T>(0.0f);
+        continue;
+      }
+      if (p.gradient) {
+        if (p.aux) z *= act_slope(p.act, to_f32(static_cast<const T*>(p.aux)[r * p.ldaux + c]));
+      } else {
+        if (p.bias) {
+          const int64_t bi = (int64_t)group * p.cols + c;
+          z += p.bias_f32 ? static_cast<const float*>(p.bias)[bi]
+                          : to_f32(static_cast<const T*>(p.bias)[bi]);
+        }
+        if (p.keep) static_cast<T*>(p.keep)[r * p.ldkeep + c] = from_f32<T>(z);
+        z = act_value(p.act, z);
+      }
+      if (p.add) z += to_f32(static_cast<const T*>(p.add)[r * p.ldadd + c]);
+      static_cast<T*>(p.out)[r * p.ldout + c] = from_f32<T>(z);
+    }
+  }
+}
+
+// Weight product, tile by tile of [groups][splits][tiles]: split s of a group takes the s-th part
+// of its rows (a multiple of kAnyDepth).  With one split the tile goes to dw and db; with more, as
+// fp32 to plane s of the workspace, [splits][groups * pi * qj] and then [splits][groups * width].
+template <typename T>
+__global__ __launch_bounds__(256) void any_weight_kernel(WeightProduct p, float* ws, int splits,
+                                                         int tiles_i, int tiles_j) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t tiles = (int64_t)tiles_i * tiles_j;
+  const int groups = p.groups.count;
+  const int width = p.dz_is_q ? p.qj : p.pi;
+  const int64_t plane = (int64_t)groups * p.pi * p.qj;
+  for (int64_t w = blockIdx.x; w < tiles * splits * groups; w += gridDim.x) {
+    const int64_t t = w % tiles;
+    const int s = (int)(w / tiles % splits);
+    const int e = (int)(w / tiles / splits);
+    const int64_t i0 = t / tiles_j * kAnyTile, j0 = t % tiles_j * kAnyTile;
+    int64_t begin, end;
+    group_rows(p.groups, p.rows, e, &begin, &end);
+    const int64_t part =
+        ((end - begin + splits - 1) / splits + kAnyDepth - 1) / kAnyDepth * kAnyDepth;
+    const int64_t k0 = std::min(begin + s * part, end), k1 = std::min(k0 + part, end);
+    const bool sum = p.db && (p.dz_is_q ? i0 == 0 && wave < 2 : j0 == 0 && (wave & 1) == 0);
+    f32x16_t acc = {}, sums = {};
+    any_accumulate<T, true, true>(static_cast<const T*>(p.p), p.ldp, i0, p.pi,
+                                  static_cast<const T*>(p.q), p.ldq, j0, p.qj, k0, k1, acc, sum,
+                                  !p.dz_is_q, sums);
+    if (sum && lane < 32) {
+      const int64_t c = p.dz_is_q ? j0 + (wave & 1) * 32 + lane : i0 + (wave >> 1) * 32 + lane;
+      if (c < width) {
+        float* db = splits > 1 ? ws + splits * plane + (int64_t)s * groups * width : p.db;
+        db[(int64_t)e * width + c] = sums[0];
+      }
+    }
+    const int64_t i = i0 + (wave >> 1) * 32 + (lane & 31);
+    if (i >= p.pi) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t j = j0 + (wave & 1) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+      if (j >= p.qj) continue;
+      const int64_t at = ((int64_t)e * p.pi + i) * p.qj + j;
+      if (splits > 1) ws[s * plane + at] = acc[r];
+      else if (p.dw_f32) static_cast<float*>(p.dw)[at] = acc[r];
+      else static_cast<T*>(p.dw)[at] = from_f32<T>(acc[r]);
+    }
+  }
+}
+
+// Adds the splits' planes in order: n words of `out` from planes n words apart.
+template <typename O>
+__global__ __launch_bounds__(256) void join_kernel(const float* ws, int splits, int64_t n, O* out) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float s = ws[i];
+    for (int k = 1; k < splits; ++k) s += ws[k * n + i];
+    out[i] = from_f32<O>(s);
+  }
+}
+
+int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, kMaxGrid)); }
+
+template <typename T>
+hipError_t launch_rows_t(const RowsProduct& a, hipStream_t stream) {
+  const int64_t tiles_m = ceil64(a.rows, kAnyTile) + (a.groups.offsets ? a.groups.count + 1 : 0);
+  const int tiles_n = (int)ceil64(a.cols, kAnyTile);
+  if (a.b_kmajor)
+    any_rows_kernel<T, true><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_m, tiles_n);
+  else
+    any_rows_kernel<T, false><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+// Splits of each group's rows: enough workgroups for two rounds of four a CU while a split keeps
+// at least 512 rows on average.
+int weight_splits(const WeightProduct& a) {
+  const int64_t tiles = ceil64(a.pi, kAnyTile) * ceil64(a.qj, kAnyTile) * a.groups.count;
+  const int64_t want = std::max<int64_t>(1, 2048 / tiles);
+  const int64_t most = std::max<int64_t>(1, a.rows / a.groups.count / 512);
+  return (int)std::min<int64_t>(std::min(want, most), 64);
+}
+
+template <typename T>
+hipError_t launch_weight_t(const WeightProduct& a, float* ws, hipStream_t stream) {
+  const int tiles_i = (int)ceil64(a.pi, kAnyTile), tiles_j = (int)ceil64(a.qj, kAnyTile);
+  const int splits = weight_splits(a);
+  const int64_t work = (int64_t)tiles_i * tiles_j * splits * a.groups.count;
+  any_weight_kernel<T><<<grid_for(work), 256, 0, stream>>>(a, ws, splits, tiles_i, tiles_j);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t n = (int64_t)a.groups.count * a.pi * a.qj;
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil64(n, 256), 4096);
+  if (a.dw_f32) join_kernel<float><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<float*>(a.dw));
+  else join_kernel<T><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<T*>(a.dw));
+  e = hipGetLastError();
+  if (e != hipSuccess || !a.db) return e;
+  const int64_t nb = (int64_t)a.groups.count * (a.dz_is_q ? a.qj : a.pi);
+  join_kernel<float><<<(unsigned)std::min<int64_t>(ceil64(nb, 256), 4096), 256, 0, stream>>>(
+      ws + splits * n, splits, nb, a.db);
+  return hipGetLastError();
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void activation_grad_kernel(const T* dy, int64_t lddy, const T* z,
+                                                              int64_t ldz, int act, T* dz,
+                                                              int64_t lddz, int64_t rows, int cols) {
+  const int pieces = (cols + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pieces;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / pieces;
+    const int c = (int)(i % pieces) * 8;
+    if (c + 8 <= cols) {
+      float d[8], v[8];
+      load_vec<T, 8>(dy + r * lddy + c, d);
+      load_vec<T, 8>(z + r * ldz + c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] *= act_slope(act, v[e]);
+      store_vec<T, 8>(dz + r * lddz + c, d);
+    } else {
+      for (int e = c; e < cols; ++e)
+        dz[r * lddz + e] =
+            from_f32<T>(to_f32(dy[r * lddy + e]) * act_slope(act, to_f32(z[r * ldz + e])));
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rows_product(const RowsProduct& a, hipStream_t stream) {
+  return a.f16 ? launch_rows_t<f16>(a, stream) : launch_rows_t<bf16>(a, stream);
+}
+
+size_t weight_product_words(const WeightProduct& a) {
+  const int splits = weight_splits(a);
+  if (splits == 1) return 0;
+  return (size_t)splits * a.groups.count *
+         ((size_t)a.pi * a.qj + (a.dz_is_q ? (size_t)a.qj : (size_t)a.pi));
+}
+
+hipError_t launch_weight_product(const WeightProduct& a, float* ws, hipStream_t stream) {
+  return a.f16 ? launch_weight_t<f16>(a, ws, stream) : launch_weight_t<bf16>(a, ws, stream);
+}
+
+hipError_t launch_activation_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
+                                  void* dz, int64_t lddz, bool f16_type, int64_t rows, int cols,
+                                  hipStream_t stream) {
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil64(rows * ((cols + 7) / 8), 256), 16384);
+  if (f16_type)
+    activation_grad_kernel<f16><<<grid, 256, 0, stream>>>(
+        static_cast<const f16*>(dy), lddy, static_cast<const f16*>(z), ldz, act,
+        static_cast<f16*>(dz), lddz, rows, cols);
+  else
+    activation_grad_kernel<bf16><<<grid, 256, 0, stream>>>(
+        static_cast<const bf16*>(dy), lddy, static_cast<const bf16*>(z), ldz, act,
+        static_cast<bf16*>(dz), lddz, rows, cols);
+  return hipGetLastError();
+}
+
+}  // namespace anvil
