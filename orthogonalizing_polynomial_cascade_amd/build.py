@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libanvil.so")
 SOURCES = ["momentum.hip", "gemm.hip", "normalize.hip", "update.hip", "api.hip", "norm.hip",
-           "linear.hip", "train_api.hip"]
+           "linear.hip", "linear_tiles.hip", "train_api.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,123 @@
+// Shared by the linear layers' kernels: the matrix instruction of each element type and the groups
+// of rows.
+#pragma once
+
+#include "device_common.h"
+#include "launchers.h"
+#include "scalar_types.h"
+
+namespace anvil {
+
+template <typename T>
+struct Mfma;
+template <>
+struct Mfma<bf16> {
+  typedef bf16x8_t vec;
+  __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mfma<f16> {
+  typedef f16 vec __attribute__((ext_vector_type(8)));
+  __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// Offset j of the groups, clamped to [0, rows] (not yet a running maximum).
+__device__ __forceinline__ int64_t raw_offset(const Groups& g, int j, int64_t rows) {
+  int64_t v = g.wide ? static_cast<const int64_t*>(g.offsets)[j]
+                     : (int64_t)static_cast<const int32_t*>(g.offsets)[j];
+  return v < 0 ? 0 : (v > rows ? rows : v);
+}
+
+__device__ __forceinline__ int64_t wave_max(int64_t v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const int64_t u = __shfl_xor(v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
+// Rows [*begin, *end) of group e: every wave looks at the offsets up to e + 1.
+__device__ __forceinline__ void group_rows(const Groups& g, int64_t rows, int e, int64_t* begin,
+                                           int64_t* end) {
+  if (!g.offsets) {
+    *begin = 0;
+    *end = rows;
+    return;
+  }
+  int64_t lo = 0;
+  for (int j = threadIdx.x & 63; j <= e; j += 64) {
+    const int64_t v = raw_offset(g, j, rows);
+    lo = v > lo ? v : lo;
+  }
+  lo = wave_max(lo);
+  const int64_t hi = raw_offset(g, e + 1, rows);
+  *begin = lo;
+  *end = hi > lo ? hi : lo;
+}
+
+// The rows in tiles of TILE, group by group; rows without an owner form two groups of their own,
+// before the first and after the last.  Finds tile t: its first row and the end of its group's
+// rows, and its group (-1: no owner).  Returns false past the last tile.
+template <int TILE>
+__device__ __forceinline__ bool row_tile(const Groups& g, int64_t rows, int64_t t, int64_t* row0,
+                                         int64_t* end, int* group) {
+  if (!g.offsets) {
+    *row0 = t * TILE;
+    *end = rows;
+    *group = 0;
+    return *row0 < rows;
+  }
+  // segment s = 0 .. count + 1 spans bound(s) .. bound(s + 1): bound(0) = 0, bound(s) = the running
+  // maximum of the offsets up to s - 1, bound(count + 2) = rows
+  const int lane = threadIdx.x & 63;
+  int64_t start = 0;      // bound at the chunk's first segment
+  int64_t done = 0;       // tiles of the segments before the chunk
+  for (int s0 = 0; s0 < g.count + 2; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t hi = s <= g.count ? raw_offset(g, s, rows) : rows;   // bound(s + 1), to be a maximum
+    hi = hi > start ? hi : start;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(hi, o);
+      if (lane >= o && u > hi) hi = u;
+    }
+    int64_t lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = start;
+    const int64_t mine = (hi - lo + TILE - 1) / TILE;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
+    }
+    const uint64_t past = __ballot(done + upto > t);
+    if (past) {
+      const int who = __ffsll((unsigned long long)past) - 1;
+      const int64_t first = done + __shfl(upto - mine, who);   // tiles before the segment
+      *row0 = __shfl(lo, who) + (t - first) * TILE;
+      *end = __shfl(hi, who);
+      const int seg = s0 + who;
+      *group = seg == 0 || seg > g.count ? -1 : seg - 1;
+      return true;
+    }
+    done += __shfl(upto, 63);
+    start = __shfl(hi, 63);
+  }
+  return false;
+}
+
+// linear_tiles.hip: the tiled kernels, for widths and pitches that are multiples of 8 and pointers
+// of 16-byte alignment (tiles_take_*), with their launches.
+bool tiles_take_rows(const RowsProduct& a);
+hipError_t launch_rows_tiles(const RowsProduct& a, hipStream_t stream);
+bool tiles_take_weight(const WeightProduct& a);
+hipError_t launch_weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream_t stream);
+// Splits of each group's rows that the tiled weight product makes (by sizes alone).
+int weight_tile_splits(const WeightProduct& a);
+
+}  // namespace anvil

@@ -1,0 +1,574 @@
+// The linear layers' products on LDS tiles (see linear.hip for what they compute): widths and pitches
+// that are multiples of 8, 16-byte aligned pointers.
+//
+// Pipeline (gfx950):
+//  * Slabs of BK = 64 k of both operands travel from memory straight into LDS (16 bytes a lane, no
+//    registers in between) into two buffers.  Rows past the tile's group, columns past the width
+//    and k past the depth get an offset outside the buffer's range, which loads zeros.
+//  * A wave reads the fragments of one 16-deep k-step while the matrix cores work on the step
+//    before it.  At the last step of a slab the waves meet: the next slab has landed (it was
+//    requested a whole slab earlier), its first fragments are read and the slab after it is
+//    requested into the buffer just finished, all ahead of that step's multiplies.
+//  * K-contiguous operands are one ds_read_b128 per fragment and lane, K-major ones two transposing
+//    reads; both layouts are swizzled against bank conflicts (mfma_slab.h).
+//  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row;
+//    one exchange between the wave's halves makes them eight, and the rows leave as 16-byte stores
+//    with bias, activation, derivative and residual applied in the registers.
+//  * KS > 1: KS sets of waves share a tile, each with its own part of the depth and its own buffers,
+//    and the first set adds the others' sums in order: for calls with fewer tiles than CUs.
+#include <algorithm>
+#include <atomic>
+
+#include "activation.h"
+#include "device_common.h"
+#include "launchers.h"
+#include "linear_common.h"
+#include "mfma_slab.h"
+#include "scalar_types.h"
+
+namespace anvil {
+
+namespace {
+
+constexpr int kBK = 64;
+
+// The copies of one operand's slabs.  `base` is the address of the next slab's origin (row 0 of the
+// tile, its first k), uniform over the wave and advanced slab by slab, so that offsets within it
+// stay small however long the depth is; `off` are the lane's byte offsets from it.
+template <bool KMAJOR, int ROWS, int NW>
+struct SlabStream {
+  static constexpr int kInsts = ROWS * kBK / 512 / NW;
+  static_assert(ROWS * kBK / 512 % NW == 0 && kInsts >= 1, "instructions split over the waves");
+  uint32_t off[kInsts];
+  uint64_t base, step;
+
+  __device__ static __forceinline__ void piece(int i, int wave, int lane, int* row, int* c) {
+    const int u = wave + i * NW;
+    if constexpr (!KMAJOR) {
+      constexpr int kSlots = kBK / 8;
+      *row = (64 / kSlots) * u + lane / kSlots;
+      *c = (lane % kSlots) ^ KContig<ROWS, kBK>::swz(*row);
+    } else {
+      constexpr int kSlots = ROWS / 8;
+      *row = u * (512 / ROWS) + lane / kSlots;
+      *c = (lane % kSlots) ^ KMajor<ROWS>::swz(*row);
+    }
+  }
+
+  // origin: the element of tile row 0 at the first k; rows: valid rows from there
+  __device__ __forceinline__ SlabStream(const uint16_t* origin, int64_t ld, int64_t rows, int wave,
+                                        int lane) {
+    base = reinterpret_cast<uint64_t>(origin);
+    step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
+#pragma unroll
+    for (int i = 0; i < kInsts; ++i) {
+      int row, c;
+      piece(i, wave, lane, &row, &c);
+      if constexpr (!KMAJOR) {
+        off[i] = row < rows ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u : kOOB;
+      } else {
+        off[i] = c * 8 < rows ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u : kOOB;
+      }
+    }
+  }
+
+  // Requests the slab at `base` into LDS address dst; left: depth from its first k on.
+  __device__ __forceinline__ void issue(uint32_t dst, int64_t left, int wave) {
+    const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
+    if (left >= kBK) {
+#pragma unroll
+      for (int i = 0; i < kInsts; ++i)
+        dma16(rsrc, dst + (uint32_t)(wave + i * NW) * 1024u, off[i]);
+    } else {
+      const int lane = __lane_id();
+#pragma unroll
+      for (int i = 0; i < kInsts; ++i) {
+        int row, c;
+        piece(i, wave, lane, &row, &c);
+        dma16(rsrc, dst + (uint32_t)(wave + i * NW) * 1024u,
+              (KMAJOR ? row : c * 8) < left ? off[i] : kOOB);
+      }
+    }
+    base += step;
+  }
+};
+
+template <int BM, int BN, int WM, int WN, int KS>
+struct Tile {
+  static constexpr int kWaves = WM * WN;             // of one set
+  static constexpr int kThreads = kWaves * KS * 64;
+  static constexpr int kWTM = BM / WM, kWTN = BN / WN;
+  static constexpr int kFM = kWTM / 32, kFN = kWTN / 32;
+  static constexpr int kStage = (BM + BN) * kBK * 2;
+  static constexpr int kQ = BM * kBK * 2;            // Q's part of a stage
+  static constexpr int kRing = 2 * kStage;
+  static constexpr int kLds = KS * kRing;
+  static_assert(kWTM % 32 == 0 && kWTN % 32 == 0, "whole fragments");
+  static_assert(KS == 1 || kWaves * kFM * kFN * 4096 <= kRing, "a set's sums fit its buffers");
+};
+
+// acc += the wave's block of sum over `depth` k of P(i, k) Q(j, k); `sum`: 0 none, 1 also the sums
+// over k of the wave's P fragment `wn`, 2 of its Q fragment `wm` into `sums`.
+template <typename T, bool PT, bool QT, int BM, int BN, int WM, int WN, int KS, bool SUMS>
+__device__ __forceinline__ void accumulate(
+    const uint16_t* P, int64_t ldp, int64_t rows_p, const uint16_t* Q, int64_t ldq, int64_t rows_q,
+    int64_t depth, char* smem, int wave, int kg,
+    f32x16_t (&acc)[Tile<BM, BN, WM, WN, KS>::kFM][Tile<BM, BN, WM, WN, KS>::kFN], int sum,
+    f32x16_t& sums) {
+  using C = Tile<BM, BN, WM, WN, KS>;
+  typedef typename Mfma<T>::vec vec;
+  const int lane = threadIdx.x & 63;
+  const int wm = wave / WN, wn = wave % WN;
+  constexpr int kSteps = kBK / 16;
+  // with KS sets every set runs the same number of slabs; slabs past the depth are zeros
+  const int64_t slabs = (depth + kBK - 1) / kBK;
+  const int KT = (int)(KS > 1 ? (slabs + KS - 1) / KS : slabs);
+  if (KT == 0) return;
+  const int64_t k0 = KS > 1 ? (int64_t)kg * KT * kBK : 0;
+  int64_t left = depth - k0;     // of the next slab to request
+
+  SlabStream<PT, BM, C::kWaves> sp(P + k0 * (PT ? ldp : 1), ldp, rows_p, wave, lane);
+  SlabStream<QT, BN, C::kWaves> sq(Q + k0 * (QT ? ldq : 1), ldq, rows_q, wave, lane);
+  const uint32_t lds = lds_addr(smem);
+  auto request = [&](int stage) {
+    sp.issue(lds + (uint32_t)(stage * C::kStage), left, wave);
+    sq.issue(lds + (uint32_t)(stage * C::kStage + C::kQ), left, wave);
+    left -= kBK;
+  };
+
+  vec fa[2][C::kFM], fb[2][C::kFN];
+  auto read = [&](int stage, int ks, int buf) {
+    const char* tp = smem + stage * C::kStage;
+    const char* tq = tp + C::kQ;
+#pragma unroll
+    for (int f = 0; f < C::kFM; ++f)
+      fa[buf][f] = __builtin_bit_cast(
+          vec, (read_frag<PT, BM, kBK>(tp, wm * C::kWTM + f * 32, ks, lane)));
+#pragma unroll
+    for (int f = 0; f < C::kFN; ++f)
+      fb[buf][f] = __builtin_bit_cast(
+          vec, (read_frag<QT, BN, kBK>(tq, wn * C::kWTN + f * 32, ks, lane)));
+  };
+  vec one;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) one[e] = from_f32<T>(1.0f);
+
+  request(0);
+  wait_vmcnt<0>();
+  __syncthreads();
+  if (KT > 1) request(1);
+  read(0, 0, 0);
+  for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      if (ks + 1 < kSteps) {
+        read(kt & 1, ks + 1, (ks + 1) & 1);
+      } else if (kt + 1 < KT) {
+        // this wave's reads of slab kt are done and its part of slab kt + 1 has landed; past the
+        // barrier that holds for every wave
+        wait_lds();
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (kt + 2 < KT) request(kt & 1);
+        read((kt + 1) & 1, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // the reads stay ahead of the multiplies
+#pragma unroll
+      for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < C::kFN; ++fn)
+          acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
+      if constexpr (SUMS) {
+        if (sum == 1) {
+#pragma unroll
+          for (int f = 0; f < C::kFM; ++f)
+            if (f == wn) sums = Mfma<T>::run(one, fa[ks & 1][f], sums);
+        } else if (sum == 2) {
+#pragma unroll
+          for (int f = 0; f < C::kFN; ++f)
+            if (f == wm) sums = Mfma<T>::run(one, fb[ks & 1][f], sums);
+        }
+      }
+    }
+  }
+  if constexpr (KS > 1) {
+    // each set's sums go through its own buffers; the first set adds them in order
+    __syncthreads();
+    char* mine = smem + wave * (C::kFM * C::kFN * 4096) + lane * 16;
+    if (kg > 0) {
+#pragma unroll
+      for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < C::kFN; ++fn)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4_t*>(mine + ((fm * C::kFN + fn) * 4 + q) * 1024) =
+                f32x4_t{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2],
+                        acc[fm][fn][4 * q + 3]};
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int s = 1; s < KS; ++s)
+#pragma unroll
+        for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+          for (int fn = 0; fn < C::kFN; ++fn)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4_t v = *reinterpret_cast<const f32x4_t*>(
+                  mine + s * C::kRing + ((fm * C::kFN + fn) * 4 + q) * 1024);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[fm][fn][4 * q + e] += v[e];
+            }
+    }
+  }
+}
+
+// Two packed 16-bit values of type T.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(a)) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(b)) << 16);
+}
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float* a, float* b) {
+  *a = to_f32(__builtin_bit_cast(T, (uint16_t)(w & 0xFFFFu)));
+  *b = to_f32(__builtin_bit_cast(T, (uint16_t)(w >> 16)));
+}
+
+// The accumulator holds, per lane, columns 8q + 4(lane / 32) + 0..3 of its row for q = 0..3.  For
+// the pair q = 2h, 2h + 1 the exchange leaves the lane with the eight columns 16h + 8(lane / 32)
+// .. + 7 (v[0..3] from the lower half's lanes, v[4..7] from the upper's), as packed dwords.
+template <typename T>
+__device__ __forceinline__ u32x4_t to_row_piece(const float v[8]) {
+  const auto s0 = __builtin_amdgcn_permlane32_swap(pack2<T>(v[0], v[1]), pack2<T>(v[4], v[5]), false, false);
+  const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<T>(v[2], v[3]), pack2<T>(v[6], v[7]), false, false);
+  return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+}
+// The inverse: a 16-byte piece of the row to the values that belong to the accumulator's entries.
+template <typename T>
+__device__ __forceinline__ void from_row_piece(u32x4_t w, float v[8]) {
+  const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  unpack2<T>(s0[0], &v[0], &v[1]);
+  unpack2<T>(s1[0], &v[2], &v[3]);
+  unpack2<T>(s0[1], &v[4], &v[5]);
+  unpack2<T>(s1[1], &v[6], &v[7]);
+}
+
+// Tiles of one launch in an order that lets the workgroups that run together on an XCD share their
+// operands: consecutive ids go down kBand row tiles before they step to the next column tile.
+constexpr int kBand = 4;
+__device__ __forceinline__ void banded(int t, int tiles_m, int tiles_n, int* ti, int* tj) {
+  const int band = t / (kBand * tiles_n);
+  const int rest = t - band * kBand * tiles_n;
+  const int high = min(kBand, tiles_m - band * kBand);
+  *ti = band * kBand + rest % high;
+  *tj = rest / high;
+}
+
+template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
+__global__ __launch_bounds__(WM * WN * KS * 64)
+__attribute__((amdgpu_waves_per_eu(OCC)))
+void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
+  using C = Tile<BM, BN, WM, WN, KS>;
+  extern __shared__ __attribute__((aligned(1024))) char smem_all[];
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int kg = wave_all / C::kWaves;
+  const int wave = wave_all % C::kWaves;
+
+  int ti, tj;
+  banded(xcd_remap(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, &ti, &tj);
+  int64_t row0, end;
+  int group;
+  if (!row_tile<BM>(p.groups, p.rows, ti, &row0, &end, &group)) return;
+  const int j0 = tj * BN;
+  const int64_t matrix = (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
+  const uint16_t* Q = static_cast<const uint16_t*>(p.b) + matrix +
+                      (QT ? (int64_t)j0 : (int64_t)j0 * p.depth);
+
+  f32x16_t acc[C::kFM][C::kFN];
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+  f32x16_t none;
+  accumulate<T, false, QT, BM, BN, WM, WN, KS, false>(
+      static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, Q,
+      QT ? p.cols : p.depth, p.cols - j0, group < 0 ? 0 : p.depth, smem_all + kg * C::kRing, wave,
+      kg, acc, 0, none);
+  if (KS > 1 && kg > 0) return;
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int half = lane >> 5;
+  const int c0 = j0 + wn * C::kWTN;
+#pragma unroll
+  for (int fn = 0; fn < C::kFN; ++fn)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the lane's accumulator entries are columns ca .. ca + 3 and ca + 8 .. ca + 11, its piece of
+      // the row columns cp .. cp + 7
+      const int ca = c0 + fn * 32 + 16 * h + 4 * half;
+      const int cp = c0 + fn * 32 + 16 * h + 8 * half;
+      float bias[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
+      if (p.bias && group >= 0) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int c = ca + 8 * q;
+          if (c >= p.cols) continue;
+          const int64_t at = (int64_t)group * p.cols + c;
+          if (p.bias_f32) load_vec<float, 4>(static_cast<const float*>(p.bias) + at, bias + 4 * q);
+          else load_vec<T, 4>(static_cast<const T*>(p.bias) + at, bias + 4 * q);
+        }
+      }
+#pragma unroll
+      for (int fm = 0; fm < C::kFM; ++fm) {
+        const int64_t r = row0 + wm * C::kWTM + fm * 32 + (lane & 31);
+        const bool inside = r < end && cp < p.cols;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[fm][fn][8 * h + e];
+        if (p.gradient) {
+          if (p.aux) {
+            u32x4_t w{};
+            if (inside)
+              w = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.aux) + r * p.ldaux + cp);
+            float z[8];
+            from_row_piece<T>(w, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= act_slope(p.act, z[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += bias[e];
+          if (p.keep) {
+            const u32x4_t w = to_row_piece<T>(v);
+            if (inside)
+              *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.keep) + r * p.ldkeep + cp) = w;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = act_value(p.act, v[e]);
+        }
+        if (p.add && group >= 0) {
+          u32x4_t w{};
+          if (inside)
+            w = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.add) + r * p.ldadd + cp);
+          float a[8];
+          from_row_piece<T>(w, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += a[e];
+        }
+        u32x4_t w = to_row_piece<T>(v);
+        if (group < 0) w = u32x4_t{};
+        if (inside) *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.out) + r * p.ldout + cp) = w;
+      }
+    }
+}
+
+// Workgroups in the order [groups][splits][tiles]; split s of a group takes the s-th part of its
+// rows (whole slabs).  Where a group's rows are split, its sums go as fp32 to plane s of the
+// workspace: [splits][groups * pi * qj], then [splits][groups * width of dz].
+template <typename T, int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(WM * WN * 64)
+__attribute__((amdgpu_waves_per_eu(OCC)))
+void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int tiles_j) {
+  using C = Tile<BM, BN, WM, WN, 1>;
+  static_assert(C::kFM <= WN && C::kFN <= WM, "each wave sums one fragment at most");
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int tiles = tiles_i * tiles_j;
+  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int s = id / tiles % splits;
+  const int e = id / tiles / splits;
+  int ti, tj;
+  banded(id % tiles, tiles_i, tiles_j, &ti, &tj);
+  const int i0 = ti * BM, j0 = tj * BN;
+  int64_t begin, end;
+  group_rows(p.groups, p.rows, e, &begin, &end);
+  const int64_t part = ((end - begin + kBK - 1) / kBK + splits - 1) / splits * kBK;
+  const int64_t k0 = min(begin + s * part, end), k1 = min(k0 + part, end);
+
+  f32x16_t acc[C::kFM][C::kFN];
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+  f32x16_t sums{};
+  const int sum = !p.db ? 0 : p.dz_is_q ? (ti == 0 ? 2 : 0) : (tj == 0 ? 1 : 0);
+  accumulate<T, true, true, BM, BN, WM, WN, 1, true>(
+      static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.pi - i0,
+      static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.qj - j0, k1 - k0, smem, wave, 0,
+      acc, sum, sums);
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int half = lane >> 5;
+  const int width = p.dz_is_q ? p.qj : p.pi;
+  const int64_t plane = (int64_t)p.groups.count * p.pi * p.qj;
+  if (sum && lane < 32 && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
+    const int c = (sum == 1 ? i0 + wm * C::kWTM + wn * 32 : j0 + wn * C::kWTN + wm * 32) + lane;
+    float* db = splits > 1 ? ws + splits * plane + (int64_t)s * p.groups.count * width : p.db;
+    if (c < width) db[(int64_t)e * width + c] = sums[0];
+  }
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm) {
+    const int i = i0 + wm * C::kWTM + fm * 32 + (lane & 31);
+    const int64_t row = ((int64_t)e * p.pi + i) * p.qj;
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) {
+      const int c0 = j0 + wn * C::kWTN + fn * 32;
+      if (splits > 1 || p.dw_f32) {
+        float* out = splits > 1 ? ws + s * plane : static_cast<float*>(p.dw);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = c0 + 8 * q + 4 * half;
+          if (i < p.pi && c < p.qj)
+            *reinterpret_cast<f32x4_t*>(out + row + c) =
+                f32x4_t{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2],
+                        acc[fm][fn][4 * q + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = acc[fm][fn][8 * h + k];
+          const u32x4_t w = to_row_piece<T>(v);
+          const int c = c0 + 16 * h + 8 * half;
+          if (i < p.pi && c < p.qj)
+            *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.dw) + row + c) = w;
+        }
+      }
+    }
+  }
+}
+
+int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups of one launch, which counts its work-items (at most 1024 a workgroup) in 32 bits;
+// larger calls take the kernels of linear.hip, whose workgroups walk over tiles.
+constexpr int64_t kMaxGrid = (int64_t(1) << 22) - 1;
+
+// Launches a kernel of more than 64 KB of LDS (its limit raised once per device).
+template <typename K, typename... A>
+hipError_t launch_lds(K kern, std::atomic<uint64_t>& configured, int64_t grid, int threads, int lds,
+                      hipStream_t stream, A... args) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit == 0 || !(configured.load(std::memory_order_acquire) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  kern<<<dim3((unsigned)grid), threads, lds, stream>>>(args...);
+  return hipGetLastError();
+}
+
+// Tile shapes of the rows product: 32x32 with eight sets of one wave, 64x64 with four sets of four,
+// 128x128 of four waves (two workgroups a CU), 256x256 of eight.
+enum RowsTile { kRows32, kRows64, kRows128, kRows256 };
+constexpr int kRowsSide[] = {32, 64, 128, 256};
+
+int64_t row_tiles(const RowsProduct& a, int side) {
+  return ceil64(a.rows, side) + (a.groups.offsets ? a.groups.count + 1 : 0);
+}
+
+RowsTile rows_tile(const RowsProduct& a) {
+  const int64_t stack = a.groups.offsets ? std::max(1, a.groups.count) : 1;
+  const int64_t height = ceil64(a.rows, stack);   // rows of a typical group
+  if (height <= 32) return kRows32;
+  if (stack * ceil64(height, 256) * ceil64(a.cols, 256) >= 200) return kRows256;
+  if (stack * ceil64(height, 128) * ceil64(a.cols, 128) >= 256) return kRows128;
+  return kRows64;
+}
+
+template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
+hipError_t rows_tiles(const RowsProduct& a, hipStream_t stream) {
+  using C = Tile<BM, BN, WM, WN, KS>;
+  static std::atomic<uint64_t> configured{0};
+  const int64_t tiles_m = row_tiles(a, BM), tiles_n = ceil64(a.cols, BN);
+  return launch_lds(rows_tile_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured, tiles_m * tiles_n,
+                    C::kThreads, C::kLds, stream, a, (int)tiles_m, (int)tiles_n);
+}
+
+template <typename T, bool QT>
+hipError_t rows_variant(const RowsProduct& a, hipStream_t stream) {
+  switch (rows_tile(a)) {
+    case kRows32: return rows_tiles<T, QT, 32, 32, 1, 1, 8, 2>(a, stream);
+    case kRows64: return rows_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
+    case kRows128: return rows_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
+    default: return rows_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
+  }
+}
+
+bool multiple8(int64_t v) { return v % 8 == 0; }
+bool wide_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool big_weight_tiles(const WeightProduct& a) {
+  return ceil64(a.pi, 256) * ceil64(a.qj, 256) * a.groups.count >= 24 && a.rows / a.groups.count >= 512;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int OCC>
+hipError_t weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
+  using C = Tile<BM, BN, WM, WN, 1>;
+  static std::atomic<uint64_t> configured{0};
+  const int64_t tiles_i = ceil64(a.pi, BM), tiles_j = ceil64(a.qj, BN);
+  return launch_lds(weight_tile_kernel<T, BM, BN, WM, WN, OCC>, configured,
+                    tiles_i * tiles_j * splits * a.groups.count, C::kThreads, C::kLds, stream, a, ws,
+                    splits, (int)tiles_i, (int)tiles_j);
+}
+
+template <typename T>
+hipError_t weight_variant(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
+  if (big_weight_tiles(a)) return weight_tiles<T, 256, 256, 2, 4, 2>(a, ws, splits, stream);
+  return weight_tiles<T, 128, 128, 2, 2, 2>(a, ws, splits, stream);
+}
+
+}  // namespace
+
+bool tiles_take_rows(const RowsProduct& a) {
+  const int side = kRowsSide[rows_tile(a)];
+  if (row_tiles(a, side) * ceil64(a.cols, side) > kMaxGrid) return false;
+  return a.depth > 0 && multiple8(a.depth) && multiple8(a.cols) && multiple8(a.lda) &&
+         multiple8(a.ldout) && wide_aligned(a.a) && wide_aligned(a.b) && wide_aligned(a.out) &&
+         (!a.aux || (multiple8(a.ldaux) && wide_aligned(a.aux))) &&
+         (!a.add || (multiple8(a.ldadd) && wide_aligned(a.add))) &&
+         (!a.keep || (multiple8(a.ldkeep) && wide_aligned(a.keep)));
+}
+
+hipError_t launch_rows_tiles(const RowsProduct& a, hipStream_t stream) {
+  if (a.f16)
+    return a.b_kmajor ? rows_variant<f16, true>(a, stream) : rows_variant<f16, false>(a, stream);
+  return a.b_kmajor ? rows_variant<bf16, true>(a, stream) : rows_variant<bf16, false>(a, stream);
+}
+
+bool tiles_take_weight(const WeightProduct& a) {
+  const int side = big_weight_tiles(a) ? 256 : 128;
+  if (ceil64(a.pi, side) * ceil64(a.qj, side) * a.groups.count * weight_tile_splits(a) > kMaxGrid)
+    return false;
+  return multiple8(a.pi) && multiple8(a.qj) && multiple8(a.ldp) && multiple8(a.ldq) &&
+         wide_aligned(a.p) && wide_aligned(a.q) && wide_aligned(a.dw);
+}
+
+int weight_tile_splits(const WeightProduct& a) {
+  const bool big = big_weight_tiles(a);
+  const int side = big ? 256 : 128;
+  const int64_t slots = big ? 256 : 512;
+  const int64_t tiles = ceil64(a.pi, side) * ceil64(a.qj, side) * a.groups.count;
+  const int64_t most = std::max<int64_t>(1, a.rows / a.groups.count / 512);
+  return (int)std::max<int64_t>(1, std::min({slots / tiles, most, int64_t(64)}));
+}
+
+hipError_t launch_weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
+  return a.f16 ? weight_variant<f16>(a, ws, splits, stream)
+               : weight_variant<bf16>(a, ws, splits, stream);
+}
+
+}  // namespace anvil

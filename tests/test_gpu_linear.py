@@ -87,6 +87,24 @@ def test_linear_shapes(gpu_lib, rows, n, k, w_kn, kind):
     _check_backward(gpu_lib, dz, x, w, _mat(rows, k, t, seed + 5), add, act, w_kn, t)
 
 
+# enough tiles for the larger tile shapes, with ragged last rows, columns and depths
+@pytest.mark.parametrize("rows,n,k", [(2100, 2000, 72), (5000, 2600, 136), (4100, 3336, 64), (700, 1288, 1032)])
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_linear_large_tiles(gpu_lib, rows, n, k, w_kn, kind):
+    t = TYPES[kind]
+    x, dz = _mat(rows, k, t, 1), _mat(rows, n, t, 4, 0.1)
+    w = _stack(1, n, k, t, 2, w_kn)[0]
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(3)).cuda()
+    _check_forward(gpu_lib, x, w, bias, _mat(rows, n, t, 5), "relu2", w_kn, True, t)
+    _check_backward(gpu_lib, dz, x, w, _mat(rows, k, t, 6), None, "silu", w_kn, t)
+    # the wide input gradient: the same tiles with the roles of n and k exchanged
+    w2 = _stack(1, k, n, t, 7, w_kn)[0]
+    dx = gpu_lib.anvil_linear_grad_input(x, w2, preact=dz, act="gelu", w_kn=w_kn, out=_nan(rows, n, t=t))
+    want, err = H.grad_input(x.cpu(), w2.cpu(), dz.cpu(), "gelu", None, w_kn)
+    H.assert_within(dx, want, err + H.half_step(want, t), "dx")
+
+
 @pytest.mark.parametrize("act", H.ACTS)
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("rows", [3, 300])
@@ -285,6 +303,14 @@ def test_expert_groups(gpu_lib, groups, w_kn, n, k):
 def test_expert_large_groups(gpu_lib, w_kn):
     """Groups longer than a tile and a split, one of them most of the rows, one empty."""
     _expert_case(gpu_lib, 6000, [0, 4096, 4100, 4100, 5999], 264, 520, w_kn, torch.bfloat16, "relu2", False)
+
+
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("n,k", [(2304, 136), (1032, 1288)])
+def test_expert_large_tiles(gpu_lib, w_kn, n, k):
+    """Enough tiles for the largest tile shapes, groups that end inside them."""
+    _expert_case(gpu_lib, 4900, [0, 700, 700, 1399, 1800, 2900, 3333, 4000, 4900], n, k, w_kn, torch.bfloat16,
+                 "silu", True)
 
 
 def test_expert_without_experts(gpu_lib):
