@@ -11,9 +11,9 @@
 //    requested into the buffer just finished, all ahead of that step's multiplies.
 //  * K-contiguous operands are one ds_read_b128 per fragment and lane, K-major ones two transposing
 //    reads; both layouts are swizzled against bank conflicts (mfma_slab.h).
-//  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row;
-//    one exchange between the wave's halves makes them eight, and the rows leave as 16-byte stores
-//    with bias, activation, derivative and residual applied in the registers.
+//  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row.
+//    The rows leave through LDS (the buffer that is free by then), eight columns a lane, whole lines
+//    an access, with bias, activation, derivative and residual applied on the way.
 //  * KS > 1: KS sets of waves share a tile, each with its own part of the depth and its own buffers,
 //    and the first set adds the others' sums in order: for calls with fewer tiles than CUs.
 #include <algorithm>
@@ -104,6 +104,7 @@ struct Tile {
   static constexpr int kRing = 2 * kStage;
   static constexpr int kLds = KS * kRing;
   static_assert(kWTM % 32 == 0 && kWTN % 32 == 0, "whole fragments");
+  static_assert(kWaves * 32 * kWTN * 4 <= kStage, "the outgoing rows fit one buffer");
   static_assert(KS == 1 || kWaves * kFM * kFN * 4096 <= kRing, "a set's sums fit its buffers");
 };
 
@@ -225,36 +226,75 @@ __device__ __forceinline__ void accumulate(
   }
 }
 
-// Two packed 16-bit values of type T.
+// Eight 16-bit values of type T as they lie in memory, to fp32 and back.
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(a)) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(b)) << 16);
+__device__ __forceinline__ void unpack8(u32x4_t w, float v[8]) {
+  T t[8];
+  __builtin_memcpy(t, &w, 16);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32(t[e]);
 }
 template <typename T>
-__device__ __forceinline__ void unpack2(uint32_t w, float* a, float* b) {
-  *a = to_f32(__builtin_bit_cast(T, (uint16_t)(w & 0xFFFFu)));
-  *b = to_f32(__builtin_bit_cast(T, (uint16_t)(w >> 16)));
+__device__ __forceinline__ u32x4_t pack8(const float v[8]) {
+  T t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = from_f32<T>(v[e]);
+  u32x4_t w;
+  __builtin_memcpy(&w, t, 16);
+  return w;
 }
 
-// The accumulator holds, per lane, columns 8q + 4(lane / 32) + 0..3 of its row for q = 0..3.  For
-// the pair q = 2h, 2h + 1 the exchange leaves the lane with the eight columns 16h + 8(lane / 32)
-// .. + 7 (v[0..3] from the lower half's lanes, v[4..7] from the upper's), as packed dwords.
-template <typename T>
-__device__ __forceinline__ u32x4_t to_row_piece(const float v[8]) {
-  const auto s0 = __builtin_amdgcn_permlane32_swap(pack2<T>(v[0], v[1]), pack2<T>(v[4], v[5]), false, false);
-  const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<T>(v[2], v[3]), pack2<T>(v[6], v[7]), false, false);
-  return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
-}
-// The inverse: a 16-byte piece of the row to the values that belong to the accumulator's entries.
-template <typename T>
-__device__ __forceinline__ void from_row_piece(u32x4_t w, float v[8]) {
-  const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-  const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  unpack2<T>(s0[0], &v[0], &v[1]);
-  unpack2<T>(s1[0], &v[2], &v[3]);
-  unpack2<T>(s0[1], &v[4], &v[5]);
-  unpack2<T>(s1[1], &v[6], &v[7]);
+// A wave's 32 rows of its block on their way out: the accumulators (a lane holds runs of four columns
+// of one row) go to LDS as fp32 and come back with eight consecutive columns a lane, lanes
+// side by side along the rows, so that every access to memory is whole 128-byte lines.  (Stored
+// from the accumulators' layout, 32 bytes of 32 rows an instruction, the lines left L2 half
+// written: 392 us against 232 for the 32768 x 2816 product of depth 768 with two outputs.)  Slots
+// of 16 bytes are swizzled by row: both sides are free of bank conflicts.
+template <int WTN>
+struct OutStage {
+  static constexpr int kLanes = WTN / 8;        // lanes of a row
+  static constexpr int kRows = 64 / kLanes;     // rows of one pass
+  static constexpr int kPasses = 32 / kRows;
+  static constexpr int kBytes = 32 * WTN * 4;
+  static constexpr int kPer256 = 64 / WTN;      // rows in the 256 bytes that the banks span
+  static_assert(WTN == 32 || WTN == 64, "rows of 128 or 256 bytes");
+  __device__ static __forceinline__ char* at(char* base, int row, int slot) {
+    return base + row * (WTN * 4) + ((slot ^ ((row / kPer256) & (WTN / 4 - 1))) << 4);
+  }
+  template <int FN>
+  __device__ static __forceinline__ void put(char* base, const f32x16_t (&acc)[FN], int lane) {
+    // the previous rows have been read: LDS accesses of one wave complete in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(at(base, lane & 31, fn * 8 + 2 * q + (lane >> 5))) =
+            f32x4_t{acc[fn][4 * q], acc[fn][4 * q + 1], acc[fn][4 * q + 2], acc[fn][4 * q + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Row (of 32) and first column (of WTN) of the lane's piece in a pass.
+  __device__ static __forceinline__ int row(int pass, int lane) { return pass * kRows + lane / kLanes; }
+  __device__ static __forceinline__ int col(int lane) { return lane % kLanes * 8; }
+  __device__ static __forceinline__ void get(char* base, int pass, int lane, float v[8]) {
+    const int r = row(pass, lane), slot = lane % kLanes * 2;
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(at(base, r, slot));
+    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(at(base, r, slot + 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = lo[e];
+      v[4 + e] = hi[e];
+    }
+  }
+};
+
+// LDS offset of the buffer that no wave reads any more after `depth` k of a tile: the one before the
+// last slab's (its readers have all met a barrier since).
+template <typename C>
+__device__ __forceinline__ int out_stage(int64_t depth) {
+  return (int)(((depth + kBK - 1) / kBK) & 1) * C::kStage;
 }
 
 // Tiles of one launch in an order that lets the workgroups that run together on an XCD share their
@@ -295,78 +335,77 @@ void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   f32x16_t none;
+  const int64_t depth = group < 0 ? 0 : p.depth;
   accumulate<T, false, QT, BM, BN, WM, WN, KS, false>(
       static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, Q,
-      QT ? p.cols : p.depth, p.cols - j0, group < 0 ? 0 : p.depth, smem_all + kg * C::kRing, wave,
+      QT ? p.cols : p.depth, p.cols - j0, depth, smem_all + kg * C::kRing, wave,
       kg, acc, 0, none);
   if (KS > 1 && kg > 0) return;
 
+  using S = OutStage<C::kWTN>;
   const int wm = wave / WN, wn = wave % WN;
-  const int half = lane >> 5;
-  const int c0 = j0 + wn * C::kWTN;
+  char* stage = smem_all + out_stage<C>(depth) + wave * S::kBytes;
+  const int c = j0 + wn * C::kWTN + S::col(lane);
+  const bool inside_c = c < p.cols;
+  float bias[8];
 #pragma unroll
-  for (int fn = 0; fn < C::kFN; ++fn)
+  for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
+  if (p.bias && group >= 0 && inside_c) {
+    const int64_t at = (int64_t)group * p.cols + c;
+    if (p.bias_f32) load_vec<float, 8>(static_cast<const float*>(p.bias) + at, bias);
+    else load_vec<T, 8>(static_cast<const T*>(p.bias) + at, bias);
+  }
+  // One copy of the epilogue's code for all rows (the loops are kept as loops): unrolled over the
+  // block, with every activation in it, it was larger than the instruction cache and took longer
+  // than twelve slabs' multiplies.
+#pragma unroll 1
+  for (int fm = 0; fm < C::kFM; ++fm) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // the lane's accumulator entries are columns ca .. ca + 3 and ca + 8 .. ca + 11, its piece of
-      // the row columns cp .. cp + 7
-      const int ca = c0 + fn * 32 + 16 * h + 4 * half;
-      const int cp = c0 + fn * 32 + 16 * h + 8 * half;
-      float bias[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
-      if (p.bias && group >= 0) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int c = ca + 8 * q;
-          if (c >= p.cols) continue;
-          const int64_t at = (int64_t)group * p.cols + c;
-          if (p.bias_f32) load_vec<float, 4>(static_cast<const float*>(p.bias) + at, bias + 4 * q);
-          else load_vec<T, 4>(static_cast<const T*>(p.bias) + at, bias + 4 * q);
+    for (int f = 0; f < C::kFM; ++f)
+      if (f == fm) S::put(stage, acc[f], lane);
+    const int64_t r0 = row0 + wm * C::kWTM + fm * 32 + S::row(0, lane);
+    // the lane's pieces of the operands, one pass ahead
+    u32x4_t aux{}, add{};
+    auto fetch = [&](int i) {
+      const int64_t r = r0 + i * S::kRows;
+      if (!inside_c || r >= end) return;
+      if (p.aux) aux = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.aux) + r * p.ldaux + c);
+      if (p.add) add = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.add) + r * p.ldadd + c);
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int i = 0; i < S::kPasses; ++i) {
+      const int64_t r = r0 + i * S::kRows;
+      const bool inside = inside_c && r < end;
+      const u32x4_t aux_now = aux, add_now = add;
+      if (i + 1 < S::kPasses) fetch(i + 1);
+      float v[8];
+      S::get(stage, i, lane, v);
+      if (p.gradient) {
+        if (p.aux) {
+          float z[8];
+          unpack8<T>(aux_now, z);
+          scale_by_slope<8>(p.act, z, v);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += bias[e];
+        if (p.keep && inside)
+          *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.keep) + r * p.ldkeep + c) =
+              group < 0 ? u32x4_t{} : pack8<T>(v);
+        activate<8>(p.act, v);
       }
+      if (p.add) {
+        float a[8];
+        unpack8<T>(add_now, a);
 #pragma unroll
-      for (int fm = 0; fm < C::kFM; ++fm) {
-        const int64_t r = row0 + wm * C::kWTM + fm * 32 + (lane & 31);
-        const bool inside = r < end && cp < p.cols;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = acc[fm][fn][8 * h + e];
-        if (p.gradient) {
-          if (p.aux) {
-            u32x4_t w{};
-            if (inside)
-              w = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.aux) + r * p.ldaux + cp);
-            float z[8];
-            from_row_piece<T>(w, z);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= act_slope(p.act, z[e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += bias[e];
-          if (p.keep) {
-            const u32x4_t w = to_row_piece<T>(v);
-            if (inside)
-              *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.keep) + r * p.ldkeep + cp) = w;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = act_value(p.act, v[e]);
-        }
-        if (p.add && group >= 0) {
-          u32x4_t w{};
-          if (inside)
-            w = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.add) + r * p.ldadd + cp);
-          float a[8];
-          from_row_piece<T>(w, a);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += a[e];
-        }
-        u32x4_t w = to_row_piece<T>(v);
-        if (group < 0) w = u32x4_t{};
-        if (inside) *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.out) + r * p.ldout + cp) = w;
+        for (int e = 0; e < 8; ++e) v[e] += a[e];
       }
+      if (inside)
+        *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.out) + r * p.ldout + c) =
+            group < 0 ? u32x4_t{} : pack8<T>(v);
     }
+  }
 }
 
 // Workgroups in the order [groups][splits][tiles]; split s of a group takes the s-th part of its
@@ -406,7 +445,6 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
       acc, sum, sums);
 
   const int wm = wave / WN, wn = wave % WN;
-  const int half = lane >> 5;
   const int width = p.dz_is_q ? p.qj : p.pi;
   const int64_t plane = (int64_t)p.groups.count * p.pi * p.qj;
   if (sum && lane < 32 && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
@@ -414,35 +452,22 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
     float* db = splits > 1 ? ws + splits * plane + (int64_t)s * p.groups.count * width : p.db;
     if (c < width) db[(int64_t)e * width + c] = sums[0];
   }
+  using S = OutStage<C::kWTN>;
+  char* stage = smem + out_stage<C>(k1 - k0) + wave * S::kBytes;
+  const int c = j0 + wn * C::kWTN + S::col(lane);
 #pragma unroll
   for (int fm = 0; fm < C::kFM; ++fm) {
-    const int i = i0 + wm * C::kWTM + fm * 32 + (lane & 31);
-    const int64_t row = ((int64_t)e * p.pi + i) * p.qj;
+    S::put(stage, acc[fm], lane);
 #pragma unroll
-    for (int fn = 0; fn < C::kFN; ++fn) {
-      const int c0 = j0 + wn * C::kWTN + fn * 32;
-      if (splits > 1 || p.dw_f32) {
-        float* out = splits > 1 ? ws + s * plane : static_cast<float*>(p.dw);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = c0 + 8 * q + 4 * half;
-          if (i < p.pi && c < p.qj)
-            *reinterpret_cast<f32x4_t*>(out + row + c) =
-                f32x4_t{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2],
-                        acc[fm][fn][4 * q + 3]};
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = acc[fm][fn][8 * h + k];
-          const u32x4_t w = to_row_piece<T>(v);
-          const int c = c0 + 16 * h + 8 * half;
-          if (i < p.pi && c < p.qj)
-            *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.dw) + row + c) = w;
-        }
-      }
+    for (int k = 0; k < S::kPasses; ++k) {
+      const int i = i0 + wm * C::kWTM + fm * 32 + S::row(k, lane);
+      float v[8];
+      S::get(stage, k, lane, v);
+      if (i >= p.pi || c >= p.qj) continue;
+      const int64_t at = ((int64_t)e * p.pi + i) * p.qj + c;
+      if (splits > 1) store_vec<float, 8>(ws + s * plane + at, v);
+      else if (p.dw_f32) store_vec<float, 8>(static_cast<float*>(p.dw) + at, v);
+      else *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.dw) + at) = pack8<T>(v);
     }
   }
 }
