@@ -67,19 +67,17 @@ struct AnySlab {
 
 // acc (one fragment per wave, C transposed: register r of lane l is row l%32, column
 // 8(r/4) + 4(l/32) + r%4) of the tile's k range [k0, k1).  With `sum`, the wave also adds up its
-// P (sum_p) or Q fragment over k into `sums` (every register of lane l: row or column l%32).
+// P (sum_p) or Q fragment over k into `sums` (see row_sum_selector).
 template <typename T, bool PT, bool QT>
 __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t i0, int64_t ni,
                                                const T* Q, int64_t ldq, int64_t j0, int64_t nj,
                                                int64_t k0, int64_t k1, f32x16_t& acc, bool sum,
-                                               bool sum_p, f32x16_t& sums) {
+                                               bool sum_p, f32x4_t& sums) {
   __shared__ __attribute__((aligned(16))) T lp[kAnyTile][kAnyPitch];
   __shared__ __attribute__((aligned(16))) T lq[kAnyTile][kAnyPitch];
   typedef typename Mfma<T>::vec vec;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  vec one;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) one[e] = from_f32<T>(1.0f);
+  const vec one = row_sum_selector<T>(lane);
   AnySlab<T, PT> sp;
   AnySlab<T, QT> sq;
   if (k0 < k1) {
@@ -101,7 +99,7 @@ __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t 
       const vec fp = *reinterpret_cast<const vec*>(&lp[(wave >> 1) * 32 + (lane & 31)][kk]);
       const vec fq = *reinterpret_cast<const vec*>(&lq[(wave & 1) * 32 + (lane & 31)][kk]);
       acc = Mfma<T>::run(fq, fp, acc);
-      if (sum) sums = Mfma<T>::run(one, sum_p ? fp : fq, sums);
+      if (sum) sums = Mfma<T>::run16(one, sum_p ? fp : fq, sums);
     }
   }
 }
@@ -115,7 +113,8 @@ __global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int64_t ti
     if (!row_tile<kAnyTile>(p.groups, p.rows, tile / tiles_n, &row0, &end, &group)) return;
     const int64_t j0 = (tile % tiles_n) * kAnyTile;
     const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
-    f32x16_t acc = {}, none = {};
+    f32x16_t acc = {};
+    f32x4_t none = {};
     any_accumulate<T, false, QT>(static_cast<const T*>(p.a), p.lda, row0, end, b,
                                  QT ? p.cols : p.depth, j0, p.cols, 0, group < 0 ? 0 : p.depth,
                                  acc, false, false, none);
@@ -170,15 +169,17 @@ __global__ __launch_bounds__(256) void any_weight_kernel(WeightProduct p, float*
         ((end - begin + splits - 1) / splits + kAnyDepth - 1) / kAnyDepth * kAnyDepth;
     const int64_t k0 = std::min(begin + s * part, end), k1 = std::min(k0 + part, end);
     const bool sum = p.db && (p.dz_is_q ? i0 == 0 && wave < 2 : j0 == 0 && (wave & 1) == 0);
-    f32x16_t acc = {}, sums = {};
+    f32x16_t acc = {};
+    f32x4_t sums = {};
     any_accumulate<T, true, true>(static_cast<const T*>(p.p), p.ldp, i0, p.pi,
                                   static_cast<const T*>(p.q), p.ldq, j0, p.qj, k0, k1, acc, sum,
                                   !p.dz_is_q, sums);
-    if (sum && lane < 32) {
+    if (sum && lane < 16) {
       const int64_t c = p.dz_is_q ? j0 + (wave & 1) * 32 + lane : i0 + (wave >> 1) * 32 + lane;
       if (c < width) {
         float* db = splits > 1 ? ws + splits * plane + (int64_t)s * groups * width : p.db;
         db[(int64_t)e * width + c] = sums[0];
+        if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[1];
       }
     }
     const int64_t i = i0 + (wave >> 1) * 32 + (lane & 31);

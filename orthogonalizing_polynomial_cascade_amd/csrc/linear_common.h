@@ -16,6 +16,9 @@ struct Mfma<bf16> {
   __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
+  __device__ static __forceinline__ f32x4_t run16(vec a, vec b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
 };
 template <>
 struct Mfma<f16> {
@@ -23,7 +26,24 @@ struct Mfma<f16> {
   __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
+  __device__ static __forceinline__ f32x4_t run16(vec a, vec b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
 };
+
+// Sums over k of a 32-row fragment (lane l: row l % 32, k 8 (l / 32) .. + 7) by a 16x16x32 multiply,
+// four registers instead of a fragment's sixteen.  That instruction takes the lane's column as
+// l % 16 and its k group as l / 16, so rows r and r + 16 of the fragment meet in one column, in k
+// groups of different parity: row 0 of the other operand holds ones for the even groups, row 1 for
+// the odd ones.  Sums of rows r and 16 + r arrive in entries 0 and 1 of lane r < 16.
+template <typename T>
+__device__ __forceinline__ typename Mfma<T>::vec row_sum_selector(int lane) {
+  typename Mfma<T>::vec v;
+  const float x = lane % 16 == (lane / 16) % 2 ? 1.0f : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(x);
+  return v;
+}
 
 // Offset j of the groups, clamped to [0, rows] (not yet a running maximum).
 __device__ __forceinline__ int64_t raw_offset(const Groups& g, int j, int64_t rows) {

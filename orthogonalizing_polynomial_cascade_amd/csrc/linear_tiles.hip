@@ -18,6 +18,7 @@
 //    and the first set adds the others' sums in order: for calls with fewer tiles than CUs.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "activation.h"
 #include "device_common.h"
@@ -30,7 +31,7 @@ namespace anvil {
 
 namespace {
 
-constexpr int kBK = 64;
+constexpr int kBK = 64;   // k of one slab
 
 // The copies of one operand's slabs.  `base` is the address of the next slab's origin (row 0 of the
 // tile, its first k), uniform over the wave and advanced slab by slab, so that offsets within it
@@ -39,7 +40,16 @@ template <bool KMAJOR, int ROWS, int NW>
 struct SlabStream {
   static constexpr int kInsts = ROWS * kBK / 512 / NW;
   static_assert(ROWS * kBK / 512 % NW == 0 && kInsts >= 1, "instructions split over the waves");
-  uint32_t off[kInsts];
+  // From one instruction of a wave to its next: rows (K-contiguous) or k (K-major).  Both are
+  // whole periods of the slot swizzle, so a lane keeps its slot.
+  static constexpr int kStep = KMAJOR ? NW * (512 / ROWS) : NW * (512 / kBK);
+  static_assert(kInsts == 1 || kStep % (KMAJOR ? 4 : 16) == 0 || (!KMAJOR && kStep % 8 == 0),
+                "slot swizzle period");
+  // K-major instructions differ by a uniform offset (soff); K-contiguous ones by rows that have to
+  // be checked against the edge one by one
+  uint32_t off[KMAJOR ? 1 : kInsts];
+  int kin;                 // the lane's k within the slab (of its first instruction)
+  uint32_t soff;           // K-major: bytes from one instruction to the next
   uint64_t base, step;
 
   __device__ static __forceinline__ void piece(int i, int wave, int lane, int* row, int* c) {
@@ -60,37 +70,31 @@ struct SlabStream {
                                         int lane) {
     base = reinterpret_cast<uint64_t>(origin);
     step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
+    soff = KMAJOR ? (uint32_t)ld * (2 * kStep) : 0;
+    int row, c;
+    piece(0, wave, lane, &row, &c);
+    kin = KMAJOR ? row : c * 8;
 #pragma unroll
-    for (int i = 0; i < kInsts; ++i) {
-      int row, c;
+    for (int i = 0; i < (KMAJOR ? 1 : kInsts); ++i) {
       piece(i, wave, lane, &row, &c);
-      if constexpr (!KMAJOR) {
-        off[i] = row < rows ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u : kOOB;
-      } else {
-        off[i] = c * 8 < rows ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u : kOOB;
-      }
+      off[i] = (KMAJOR ? c * 8 : row) < rows
+                   ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u
+                   : kOOB;
     }
   }
 
-  // Requests the slab at `base` into LDS address dst; left: depth from its first k on.
-  __device__ __forceinline__ void issue(uint32_t dst, int64_t left, int wave) {
+  // Instruction i of the slab at `base` into LDS address dst; left: depth from its first k on, at
+  // most kBK (no branch, so that the copies can stand among the multiplies).
+  __device__ __forceinline__ void issue(int i, uint32_t dst, int left, int wave) const {
     const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
-    if (left >= kBK) {
-#pragma unroll
-      for (int i = 0; i < kInsts; ++i)
-        dma16(rsrc, dst + (uint32_t)(wave + i * NW) * 1024u, off[i]);
+    const uint32_t to = dst + (uint32_t)(wave + i * NW) * 1024u;
+    if constexpr (KMAJOR) {
+      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB, (uint32_t)i * soff);
     } else {
-      const int lane = __lane_id();
-#pragma unroll
-      for (int i = 0; i < kInsts; ++i) {
-        int row, c;
-        piece(i, wave, lane, &row, &c);
-        dma16(rsrc, dst + (uint32_t)(wave + i * NW) * 1024u,
-              (KMAJOR ? row : c * 8) < left ? off[i] : kOOB);
-      }
+      dma16(rsrc, to, kin < left ? off[i] : kOOB);
     }
-    base += step;
   }
+  __device__ __forceinline__ void advance() { base += step; }
 };
 
 template <int BM, int BN, int WM, int WN, int KS>
@@ -110,17 +114,17 @@ struct Tile {
 
 // acc += the wave's block of sum over `depth` k of P(i, k) Q(j, k); `sum`: 0 none, 1 also the sums
 // over k of the wave's P fragment `wn`, 2 of its Q fragment `wm` into `sums`.
-template <typename T, bool PT, bool QT, int BM, int BN, int WM, int WN, int KS, bool SUMS>
-__device__ __forceinline__ void accumulate(
-    const uint16_t* P, int64_t ldp, int64_t rows_p, const uint16_t* Q, int64_t ldq, int64_t rows_q,
-    int64_t depth, char* smem, int wave, int kg,
-    f32x16_t (&acc)[Tile<BM, BN, WM, WN, KS>::kFM][Tile<BM, BN, WM, WN, KS>::kFN], int sum,
-    f32x16_t& sums) {
-  using C = Tile<BM, BN, WM, WN, KS>;
+template <typename T, bool PT, bool QT, typename C, int BM, int BN, int WM, int WN, int KS, bool SUMS>
+__device__ __forceinline__ void accumulate(const uint16_t* P, int64_t ldp, int64_t rows_p,
+                                           const uint16_t* Q, int64_t ldq, int64_t rows_q,
+                                           int64_t depth, char* smem, int wave, int kg,
+                                           f32x16_t (&acc)[C::kFM][C::kFN], int sum,
+                                           f32x4_t& sums) {
   typedef typename Mfma<T>::vec vec;
   const int lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
   constexpr int kSteps = kBK / 16;
+  static_assert(kSteps % 2 == 0, "the first k-step of a slab uses the first fragment buffer");
   // with KS sets every set runs the same number of slabs; slabs past the depth are zeros
   const int64_t slabs = (depth + kBK - 1) / kBK;
   const int KT = (int)(KS > 1 ? (slabs + KS - 1) / KS : slabs);
@@ -131,10 +135,22 @@ __device__ __forceinline__ void accumulate(
   SlabStream<PT, BM, C::kWaves> sp(P + k0 * (PT ? ldp : 1), ldp, rows_p, wave, lane);
   SlabStream<QT, BN, C::kWaves> sq(Q + k0 * (QT ? ldq : 1), ldq, rows_q, wave, lane);
   const uint32_t lds = lds_addr(smem);
-  auto request = [&](int stage) {
-    sp.issue(lds + (uint32_t)(stage * C::kStage), left, wave);
-    sq.issue(lds + (uint32_t)(stage * C::kStage + C::kQ), left, wave);
+  constexpr int kCopies = sp.kInsts + sq.kInsts;
+  auto copy = [&](int i, int stage) {      // instruction i of the next slab's copies
+    const uint32_t to = lds + (uint32_t)(stage * C::kStage);
+    const int here = (int)(left < kBK ? left : kBK);
+    if (i < sp.kInsts) sp.issue(i, to, here, wave);
+    else sq.issue(i - sp.kInsts, to + C::kQ, here, wave);
+  };
+  auto advance = [&]() {
+    sp.advance();
+    sq.advance();
     left -= kBK;
+  };
+  auto request = [&](int stage) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(i, stage);
+    advance();
   };
 
   vec fa[2][C::kFM], fb[2][C::kFN];
@@ -150,48 +166,65 @@ __device__ __forceinline__ void accumulate(
       fb[buf][f] = __builtin_bit_cast(
           vec, (read_frag<QT, BN, kBK>(tq, wn * C::kWTN + f * 32, ks, lane)));
   };
-  vec one;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) one[e] = from_f32<T>(1.0f);
+  const vec one = row_sum_selector<T>(lane);
 
+  // Slab kt from buffer `stage`.  MORE: there is a slab after it; REQUEST: and one after that, whose
+  // copies go out among the last step's multiplies.
+  auto slab = [&](int stage, auto more, auto req) {
+    constexpr bool MORE = decltype(more)::value, REQUEST = decltype(req)::value;
+    constexpr int kMults = C::kFM * C::kFN;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      const bool last = ks + 1 == kSteps;
+      if (!last) {
+        read(stage, ks + 1, (ks + 1) & 1);
+      } else {
+        // this wave's reads of the slab are done and its part of the next one has landed; past the
+        // barrier that holds for every wave
+        wait_lds();
+        if (MORE) {
+          wait_vmcnt<0>();
+          __syncthreads();
+          read(stage ^ 1, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);   // the reads stay ahead of the multiplies
+#pragma unroll
+      for (int m = 0; m < kMults; ++m) {
+        const int fm = m / C::kFN, fn = m % C::kFN;
+        acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
+        if (last && REQUEST) {
+#pragma unroll
+          for (int i = m * kCopies / kMults; i < (m + 1) * kCopies / kMults; ++i) copy(i, stage);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if constexpr (SUMS) {
+        if (sum == 1) {
+#pragma unroll
+          for (int f = 0; f < C::kFM; ++f)
+            if (f == wn) sums = Mfma<T>::run16(one, fa[ks & 1][f], sums);
+        } else if (sum == 2) {
+#pragma unroll
+          for (int f = 0; f < C::kFN; ++f)
+            if (f == wm) sums = Mfma<T>::run16(one, fb[ks & 1][f], sums);
+        }
+      }
+      if (last && REQUEST) advance();
+    }
+  };
+
+  constexpr std::integral_constant<bool, true> yes{};
+  constexpr std::integral_constant<bool, false> no{};
   request(0);
   wait_vmcnt<0>();
   __syncthreads();
   if (KT > 1) request(1);
   read(0, 0, 0);
-  for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      if (ks + 1 < kSteps) {
-        read(kt & 1, ks + 1, (ks + 1) & 1);
-      } else if (kt + 1 < KT) {
-        // this wave's reads of slab kt are done and its part of slab kt + 1 has landed; past the
-        // barrier that holds for every wave
-        wait_lds();
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (kt + 2 < KT) request(kt & 1);
-        read((kt + 1) & 1, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);   // the reads stay ahead of the multiplies
-#pragma unroll
-      for (int fm = 0; fm < C::kFM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < C::kFN; ++fn)
-          acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
-      if constexpr (SUMS) {
-        if (sum == 1) {
-#pragma unroll
-          for (int f = 0; f < C::kFM; ++f)
-            if (f == wn) sums = Mfma<T>::run(one, fa[ks & 1][f], sums);
-        } else if (sum == 2) {
-#pragma unroll
-          for (int f = 0; f < C::kFN; ++f)
-            if (f == wm) sums = Mfma<T>::run(one, fb[ks & 1][f], sums);
-        }
-      }
-    }
-  }
+  int kt = 0;
+  for (; kt + 2 < KT; ++kt) slab(kt & 1, yes, yes);
+  if (kt + 1 < KT) slab(kt++ & 1, yes, no);
+  slab(kt & 1, no, no);
   if constexpr (KS > 1) {
     // each set's sums go through its own buffers; the first set adds them in order
     __syncthreads();
@@ -334,9 +367,9 @@ void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
   for (int fm = 0; fm < C::kFM; ++fm)
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
-  f32x16_t none;
+  f32x4_t none;
   const int64_t depth = group < 0 ? 0 : p.depth;
-  accumulate<T, false, QT, BM, BN, WM, WN, KS, false>(
+  accumulate<T, false, QT, C, BM, BN, WM, WN, KS, false>(
       static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, Q,
       QT ? p.cols : p.depth, p.cols - j0, depth, smem_all + kg * C::kRing, wave,
       kg, acc, 0, none);
@@ -437,9 +470,9 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   for (int fm = 0; fm < C::kFM; ++fm)
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
-  f32x16_t sums{};
+  f32x4_t sums{};
   const int sum = !p.db ? 0 : p.dz_is_q ? (ti == 0 ? 2 : 0) : (tj == 0 ? 1 : 0);
-  accumulate<T, true, true, BM, BN, WM, WN, 1, true>(
+  accumulate<T, true, true, C, BM, BN, WM, WN, 1, true>(
       static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.pi - i0,
       static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.qj - j0, k1 - k0, smem, wave, 0,
       acc, sum, sums);
@@ -447,10 +480,11 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   const int wm = wave / WN, wn = wave % WN;
   const int width = p.dz_is_q ? p.qj : p.pi;
   const int64_t plane = (int64_t)p.groups.count * p.pi * p.qj;
-  if (sum && lane < 32 && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
+  if (sum && lane < 16 && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
     const int c = (sum == 1 ? i0 + wm * C::kWTM + wn * 32 : j0 + wn * C::kWTN + wm * 32) + lane;
     float* db = splits > 1 ? ws + splits * plane + (int64_t)s * p.groups.count * width : p.db;
     if (c < width) db[(int64_t)e * width + c] = sums[0];
+    if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[1];
   }
   using S = OutStage<C::kWTN>;
   char* stage = smem + out_stage<C>(k1 - k0) + wave * S::kBytes;

@@ -82,6 +82,14 @@ __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t lds, uint32_t voff)
                : "memory", "m0");
 }
 
+// The same with a uniform byte offset `soff` on top of the lanes'; a lane at kOOB stays out of range.
+__device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
+
 // MFMA operand of a 32-row fragment (rows R0..R0+31) at k-step ks (k = 16ks .. 16ks+15):
 // lane l holds row R0 + l%32, k = 16ks + 8(l/32) + 0..7.
 template <bool KMAJOR, int ROWS, int BK>
