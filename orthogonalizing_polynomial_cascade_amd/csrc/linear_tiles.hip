@@ -40,11 +40,12 @@ template <bool KMAJOR, int ROWS, int NW>
 struct SlabStream {
   static constexpr int kInsts = ROWS * kBK / 512 / NW;
   static_assert(ROWS * kBK / 512 % NW == 0 && kInsts >= 1, "instructions split over the waves");
-  // From one instruction of a wave to its next: rows (K-contiguous) or k (K-major).  Both are
-  // whole periods of the slot swizzle, so a lane keeps its slot.
+  // From one instruction of a wave to its next: rows (K-contiguous) or k (K-major).  A lane keeps its
+  // slot where that is a whole period of the slot swizzle; eight rows are half a period of the
+  // K-contiguous one, which exchanges the halves of the slab's k.
   static constexpr int kStep = KMAJOR ? NW * (512 / ROWS) : NW * (512 / kBK);
-  static_assert(kInsts == 1 || kStep % (KMAJOR ? 4 : 16) == 0 || (!KMAJOR && kStep % 8 == 0),
-                "slot swizzle period");
+  static constexpr bool kHalf = !KMAJOR && kStep == 8;
+  static_assert(kInsts == 1 || kHalf || kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
   // K-major instructions differ by a uniform offset (soff); K-contiguous ones by rows that have to
   // be checked against the edge one by one
   uint32_t off[KMAJOR ? 1 : kInsts];
@@ -66,8 +67,8 @@ struct SlabStream {
   }
 
   // origin: the element of tile row 0 at the first k; rows: valid rows from there
-  __device__ __forceinline__ SlabStream(const uint16_t* origin, int64_t ld, int64_t rows, int wave,
-                                        int lane) {
+  __device__ __forceinline__ void init(const uint16_t* origin, int64_t ld, int64_t rows, int wave,
+                                       int lane) {
     base = reinterpret_cast<uint64_t>(origin);
     step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
     soff = KMAJOR ? (uint32_t)ld * (2 * kStep) : 0;
@@ -89,9 +90,11 @@ struct SlabStream {
     const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
     const uint32_t to = dst + (uint32_t)(wave + i * NW) * 1024u;
     if constexpr (KMAJOR) {
-      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB, (uint32_t)i * soff);
+      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB,
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)i * soff)));
     } else {
-      dma16(rsrc, to, kin < left ? off[i] : kOOB);
+      const int k = kHalf && (i & 1) ? kin ^ (kBK / 2) : kin;
+      dma16(rsrc, to, k < left ? off[i] : kOOB);
     }
   }
   __device__ __forceinline__ void advance() { base += step; }
@@ -112,121 +115,145 @@ struct Tile {
   static_assert(KS == 1 || kWaves * kFM * kFN * 4096 <= kRing, "a set's sums fit its buffers");
 };
 
-// acc += the wave's block of sum over `depth` k of P(i, k) Q(j, k); `sum`: 0 none, 1 also the sums
-// over k of the wave's P fragment `wn`, 2 of its Q fragment `wm` into `sums`.
-template <typename T, bool PT, bool QT, typename C, int BM, int BN, int WM, int WN, int KS, bool SUMS>
-__device__ __forceinline__ void accumulate(const uint16_t* P, int64_t ldp, int64_t rows_p,
-                                           const uint16_t* Q, int64_t ldq, int64_t rows_q,
-                                           int64_t depth, char* smem, int wave, int kg,
-                                           f32x16_t (&acc)[C::kFM][C::kFN], int sum,
-                                           f32x4_t& sums) {
+// The multiplies of one tile: acc += the wave's block of the sum over `depth` k of P(i, k) Q(j, k).
+template <typename T, bool PT, bool QT, int BM, int BN, int WM, int WN, int KS>
+struct Pipe {
+  using C = Tile<BM, BN, WM, WN, KS>;
   typedef typename Mfma<T>::vec vec;
-  const int lane = threadIdx.x & 63;
-  const int wm = wave / WN, wn = wave % WN;
-  constexpr int kSteps = kBK / 16;
+  typedef SlabStream<PT, BM, C::kWaves> StreamP;
+  typedef SlabStream<QT, BN, C::kWaves> StreamQ;
+  static constexpr int kSteps = kBK / 16;
+  static constexpr int kCopies = StreamP::kInsts + StreamQ::kInsts;
   static_assert(kSteps % 2 == 0, "the first k-step of a slab uses the first fragment buffer");
-  // with KS sets every set runs the same number of slabs; slabs past the depth are zeros
-  const int64_t slabs = (depth + kBK - 1) / kBK;
-  const int KT = (int)(KS > 1 ? (slabs + KS - 1) / KS : slabs);
-  if (KT == 0) return;
-  const int64_t k0 = KS > 1 ? (int64_t)kg * KT * kBK : 0;
-  int64_t left = depth - k0;     // of the next slab to request
 
-  SlabStream<PT, BM, C::kWaves> sp(P + k0 * (PT ? ldp : 1), ldp, rows_p, wave, lane);
-  SlabStream<QT, BN, C::kWaves> sq(Q + k0 * (QT ? ldq : 1), ldq, rows_q, wave, lane);
-  const uint32_t lds = lds_addr(smem);
-  constexpr int kCopies = sp.kInsts + sq.kInsts;
-  auto copy = [&](int i, int stage) {      // instruction i of the next slab's copies
+  char* smem;        // this set's two buffers
+  uint32_t lds;
+  int wave, lane, wm, wn;
+  StreamP sp;
+  StreamQ sq;
+  int64_t left;      // depth from the next slab to request on
+  int KT;            // slabs
+
+  __device__ __forceinline__ Pipe(char* smem_, int wave_)
+      : smem(smem_), lds(lds_addr(smem_)), wave(wave_), lane((int)(threadIdx.x & 63)),
+        wm(wave_ / WN), wn(wave_ % WN) {}
+
+  // With KS sets (this is number kg) every set runs the same number of slabs; slabs past the depth
+  // are zeros.
+  __device__ __forceinline__ void begin(const uint16_t* P, int64_t ldp, int64_t rows_p,
+                                        const uint16_t* Q, int64_t ldq, int64_t rows_q,
+                                        int64_t depth, int kg) {
+    const int64_t slabs = (depth + kBK - 1) / kBK;
+    KT = (int)(KS > 1 ? (slabs + KS - 1) / KS : slabs);
+    const int64_t k0 = KS > 1 ? (int64_t)kg * KT * kBK : 0;
+    left = depth - k0;
+    sp.init(P + k0 * (PT ? ldp : 1), ldp, rows_p, wave, lane);
+    sq.init(Q + k0 * (QT ? ldq : 1), ldq, rows_q, wave, lane);
+  }
+
+  // Instruction i of the next slab's copies into buffer `stage`.
+  __device__ __forceinline__ void copy(int i, int stage) const {
     const uint32_t to = lds + (uint32_t)(stage * C::kStage);
     const int here = (int)(left < kBK ? left : kBK);
-    if (i < sp.kInsts) sp.issue(i, to, here, wave);
-    else sq.issue(i - sp.kInsts, to + C::kQ, here, wave);
-  };
-  auto advance = [&]() {
+    if (i < StreamP::kInsts) sp.issue(i, to, here, wave);
+    else sq.issue(i - StreamP::kInsts, to + C::kQ, here, wave);
+  }
+  __device__ __forceinline__ void advance() {
     sp.advance();
     sq.advance();
     left -= kBK;
-  };
-  auto request = [&](int stage) {
+  }
+  __device__ __forceinline__ void request(int stage) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy(i, stage);
     advance();
-  };
+  }
 
-  vec fa[2][C::kFM], fb[2][C::kFN];
-  auto read = [&](int stage, int ks, int buf) {
-    const char* tp = smem + stage * C::kStage;
-    const char* tq = tp + C::kQ;
-#pragma unroll
-    for (int f = 0; f < C::kFM; ++f)
-      fa[buf][f] = __builtin_bit_cast(
-          vec, (read_frag<PT, BM, kBK>(tp, wm * C::kWTM + f * 32, ks, lane)));
-#pragma unroll
-    for (int f = 0; f < C::kFN; ++f)
-      fb[buf][f] = __builtin_bit_cast(
-          vec, (read_frag<QT, BN, kBK>(tq, wn * C::kWTN + f * 32, ks, lane)));
-  };
-  const vec one = row_sum_selector<T>(lane);
+  // The buffer that no wave reads any more after run(): the one before the last slab's.
+  __device__ __forceinline__ char* spare() const { return smem + (KT & 1) * C::kStage; }
 
-  // Slab kt from buffer `stage`.  MORE: there is a slab after it; REQUEST: and one after that, whose
-  // copies go out among the last step's multiplies.
-  auto slab = [&](int stage, auto more, auto req) {
-    constexpr bool MORE = decltype(more)::value, REQUEST = decltype(req)::value;
-    constexpr int kMults = C::kFM * C::kFN;
+  // All slabs.  `sum`: 0 none, 1 also the sums over k of the wave's P fragment `wn`, 2 of its Q
+  // fragment `wm` into `sums`.
+  template <bool SUMS>
+  __device__ __forceinline__ void run(f32x16_t (&acc)[C::kFM][C::kFN], int sum, f32x4_t& sums) {
+    if (KT == 0) return;
+    vec fa[2][C::kFM], fb[2][C::kFN];
+    auto read = [&](int stage, int ks, int buf) {
+      const char* tp = smem + stage * C::kStage;
+      const char* tq = tp + C::kQ;
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      const bool last = ks + 1 == kSteps;
-      if (!last) {
-        read(stage, ks + 1, (ks + 1) & 1);
-      } else {
-        // this wave's reads of the slab are done and its part of the next one has landed; past the
-        // barrier that holds for every wave
-        wait_lds();
-        if (MORE) {
-          wait_vmcnt<0>();
-          __syncthreads();
-          read(stage ^ 1, 0, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);   // the reads stay ahead of the multiplies
+      for (int f = 0; f < C::kFM; ++f)
+        fa[buf][f] = __builtin_bit_cast(
+            vec, (read_frag<PT, BM, kBK>(tp, wm * C::kWTM + f * 32, ks, lane)));
 #pragma unroll
-      for (int m = 0; m < kMults; ++m) {
-        const int fm = m / C::kFN, fn = m % C::kFN;
-        acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
-        if (last && REQUEST) {
-#pragma unroll
-          for (int i = m * kCopies / kMults; i < (m + 1) * kCopies / kMults; ++i) copy(i, stage);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      if constexpr (SUMS) {
-        if (sum == 1) {
-#pragma unroll
-          for (int f = 0; f < C::kFM; ++f)
-            if (f == wn) sums = Mfma<T>::run16(one, fa[ks & 1][f], sums);
-        } else if (sum == 2) {
-#pragma unroll
-          for (int f = 0; f < C::kFN; ++f)
-            if (f == wm) sums = Mfma<T>::run16(one, fb[ks & 1][f], sums);
-        }
-      }
-      if (last && REQUEST) advance();
-    }
-  };
+      for (int f = 0; f < C::kFN; ++f)
+        fb[buf][f] = __builtin_bit_cast(
+            vec, (read_frag<QT, BN, kBK>(tq, wn * C::kWTN + f * 32, ks, lane)));
+    };
+    const vec one = row_sum_selector<T>(lane);
 
-  constexpr std::integral_constant<bool, true> yes{};
-  constexpr std::integral_constant<bool, false> no{};
-  request(0);
-  wait_vmcnt<0>();
-  __syncthreads();
-  if (KT > 1) request(1);
-  read(0, 0, 0);
-  int kt = 0;
-  for (; kt + 2 < KT; ++kt) slab(kt & 1, yes, yes);
-  if (kt + 1 < KT) slab(kt++ & 1, yes, no);
-  slab(kt & 1, no, no);
-  if constexpr (KS > 1) {
-    // each set's sums go through its own buffers; the first set adds them in order
+    // Slab kt from buffer `stage`.  MORE: there is a slab after it; REQUEST: and one after that,
+    // whose copies go out among the last step's multiplies.
+    auto slab = [&](int stage, auto more, auto req) {
+      constexpr bool MORE = decltype(more)::value, REQUEST = decltype(req)::value;
+      constexpr int kMults = C::kFM * C::kFN;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        const bool last = ks + 1 == kSteps;
+        if (!last) {
+          read(stage, ks + 1, (ks + 1) & 1);
+        } else {
+          // this wave's reads of the slab are done and its part of the next one has landed; past
+          // the barrier that holds for every wave
+          wait_lds();
+          if (MORE) {
+            wait_vmcnt<0>();
+            __syncthreads();
+            read(stage ^ 1, 0, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // the reads stay ahead of the multiplies
+#pragma unroll
+        for (int m = 0; m < kMults; ++m) {
+          const int fm = m / C::kFN, fn = m % C::kFN;
+          acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
+          if (last && REQUEST) {
+#pragma unroll
+            for (int i = m * kCopies / kMults; i < (m + 1) * kCopies / kMults; ++i) copy(i, stage);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        if constexpr (SUMS) {
+          if (sum == 1) {
+#pragma unroll
+            for (int f = 0; f < C::kFM; ++f)
+              if (f == wn) sums = Mfma<T>::run16(one, fa[ks & 1][f], sums);
+          } else if (sum == 2) {
+#pragma unroll
+            for (int f = 0; f < C::kFN; ++f)
+              if (f == wm) sums = Mfma<T>::run16(one, fb[ks & 1][f], sums);
+          }
+        }
+        if (last && REQUEST) advance();
+      }
+    };
+
+    constexpr std::integral_constant<bool, true> yes{};
+    constexpr std::integral_constant<bool, false> no{};
+    request(0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (KT > 1) request(1);
+    read(0, 0, 0);
+    int kt = 0;
+    for (; kt + 2 < KT; ++kt) slab(kt & 1, yes, yes);
+    if (kt + 1 < KT) slab(kt++ & 1, yes, no);
+    slab(kt & 1, no, no);
+  }
+
+  // KS > 1: each set's sums go through its own buffers; the first set adds them in order.
+  __device__ __forceinline__ void merge(int kg, f32x16_t (&acc)[C::kFM][C::kFN]) {
+    if (KT == 0) return;
     __syncthreads();
     char* mine = smem + wave * (C::kFM * C::kFN * 4096) + lane * 16;
     if (kg > 0) {
@@ -257,7 +284,7 @@ __device__ __forceinline__ void accumulate(const uint16_t* P, int64_t ldp, int64
             }
     }
   }
-}
+};
 
 // Eight 16-bit values of type T as they lie in memory, to fp32 and back.
 template <typename T>
@@ -323,13 +350,6 @@ struct OutStage {
   }
 };
 
-// LDS offset of the buffer that no wave reads any more after `depth` k of a tile: the one before the
-// last slab's (its readers have all met a barrier since).
-template <typename C>
-__device__ __forceinline__ int out_stage(int64_t depth) {
-  return (int)(((depth + kBK - 1) / kBK) & 1) * C::kStage;
-}
-
 // Tiles of one launch in an order that lets the workgroups that run together on an XCD share their
 // operands: consecutive ids go down kBand row tiles before they step to the next column tile.
 constexpr int kBand = 4;
@@ -341,25 +361,134 @@ __device__ __forceinline__ void banded(int t, int tiles_m, int tiles_n, int* ti,
   *tj = rest / high;
 }
 
+// The outgoing rows of a wave's block: rows r0 .. of a group that ends at `end`, the lane's columns
+// c .. c + 7.  One copy of the code for each activation, so that what a launch runs of it stays
+// within the instruction cache beside the multiplies (with the choice made at every element and
+// everything unrolled it did not, and took longer than the multiplies of twelve slabs).
+template <typename T, typename C, bool GRADIENT, int ACT>
+__device__ __forceinline__ void rows_out(const RowsProduct& p,
+                                         const f32x16_t (&acc)[C::kFM][C::kFN], char* stage,
+                                         int64_t r0, int64_t end, int group, int c, int lane) {
+  using S = OutStage<C::kWTN>;
+  const bool inside_c = c < p.cols;
+  float bias[8];
+  if (!GRADIENT) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
+    if (p.bias && group >= 0 && inside_c) {
+      const int64_t at = (int64_t)group * p.cols + c;
+      if (p.bias_f32) load_vec<float, 8>(static_cast<const float*>(p.bias) + at, bias);
+      else load_vec<T, 8>(static_cast<const T*>(p.bias) + at, bias);
+    }
+  }
+  const int64_t first = r0 + S::row(0, lane);
+  const int rows = inside_c ? (int)min(end - first, (int64_t)C::kWTM) : 0;   // below: row inside
+  T* out = static_cast<T*>(p.out) + first * p.ldout + c;
+  T* keep = static_cast<T*>(p.keep) + first * p.ldkeep + c;
+  const T* aux = static_cast<const T*>(p.aux) + first * p.ldaux + c;
+  const T* add = static_cast<const T*>(p.add) + first * p.ldadd + c;
+  // the lane's pieces of the operands, 32 rows ahead
+  u32x4_t aux_next[S::kPasses], add_next[S::kPasses];
+  auto fetch = [&](int fm) {
+#pragma unroll
+    for (int i = 0; i < S::kPasses; ++i) {
+      const int r = fm * 32 + i * S::kRows;
+      if (GRADIENT) {
+        aux_next[i] = u32x4_t{};
+        if (r < rows) aux_next[i] = *reinterpret_cast<const u32x4_t*>(aux + r * p.ldaux);
+      }
+      if (p.add) {
+        add_next[i] = u32x4_t{};
+        if (r < rows) add_next[i] = *reinterpret_cast<const u32x4_t*>(add + r * p.ldadd);
+      }
+    }
+  };
+  fetch(0);
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm) {
+    S::put(stage, acc[fm], lane);
+    u32x4_t aux_now[S::kPasses], add_now[S::kPasses];
+#pragma unroll
+    for (int i = 0; i < S::kPasses; ++i) {
+      aux_now[i] = aux_next[i];
+      add_now[i] = add_next[i];
+    }
+    if (fm + 1 < C::kFM) fetch(fm + 1);
+#pragma unroll
+    for (int i = 0; i < S::kPasses; ++i) {
+      const int r = fm * 32 + i * S::kRows;
+      const bool inside = r < rows;
+      float v[8];
+      S::get(stage, i, lane, v);
+      if (GRADIENT) {
+        float z[8];
+        unpack8<T>(aux_now[i], z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= act_slope(ACT, z[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += bias[e];
+        if (p.keep && inside)
+          *reinterpret_cast<u32x4_t*>(keep + r * p.ldkeep) = group < 0 ? u32x4_t{} : pack8<T>(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = act_value(ACT, v[e]);
+      }
+      if (p.add) {
+        float a[8];
+        unpack8<T>(add_now[i], a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += a[e];
+      }
+      if (inside)
+        *reinterpret_cast<u32x4_t*>(out + r * p.ldout) = group < 0 ? u32x4_t{} : pack8<T>(v);
+    }
+  }
+}
+
+template <typename T, typename C>
+__device__ __forceinline__ void rows_epilogue(const RowsProduct& p,
+                                              const f32x16_t (&acc)[C::kFM][C::kFN], char* stage,
+                                              int64_t r0, int64_t end, int group, int c, int lane) {
+  if (p.gradient && p.aux) {
+    switch (p.act) {
+      case kActRelu: return rows_out<T, C, true, kActRelu>(p, acc, stage, r0, end, group, c, lane);
+      case kActRelu2: return rows_out<T, C, true, kActRelu2>(p, acc, stage, r0, end, group, c, lane);
+      case kActGelu: return rows_out<T, C, true, kActGelu>(p, acc, stage, r0, end, group, c, lane);
+      default: return rows_out<T, C, true, kActSilu>(p, acc, stage, r0, end, group, c, lane);
+    }
+  }
+  // a gradient without an activation has neither bias nor kept preactivation
+  switch (p.act) {
+    case kActRelu: return rows_out<T, C, false, kActRelu>(p, acc, stage, r0, end, group, c, lane);
+    case kActRelu2: return rows_out<T, C, false, kActRelu2>(p, acc, stage, r0, end, group, c, lane);
+    case kActGelu: return rows_out<T, C, false, kActGelu>(p, acc, stage, r0, end, group, c, lane);
+    case kActSilu: return rows_out<T, C, false, kActSilu>(p, acc, stage, r0, end, group, c, lane);
+    default: return rows_out<T, C, false, kActNone>(p, acc, stage, r0, end, group, c, lane);
+  }
+}
+
 template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
 __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
 void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
+  using S = OutStage<C::kWTN>;
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int kg = wave_all / C::kWaves;
   const int wave = wave_all % C::kWaves;
+  char* smem = smem_all + kg * C::kRing;
 
   int ti, tj;
   banded(xcd_remap(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, &ti, &tj);
   int64_t row0, end;
   int group;
+  // with groups the launch counts one row tile more for each than there may be
   if (!row_tile<BM>(p.groups, p.rows, ti, &row0, &end, &group)) return;
   const int j0 = tj * BN;
-  const int64_t matrix = (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
-  const uint16_t* Q = static_cast<const uint16_t*>(p.b) + matrix +
+  const uint16_t* b = static_cast<const uint16_t*>(p.b) +
+                      (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth +
                       (QT ? (int64_t)j0 : (int64_t)j0 * p.depth);
 
   f32x16_t acc[C::kFM][C::kFN];
@@ -368,77 +497,17 @@ void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   f32x4_t none;
-  const int64_t depth = group < 0 ? 0 : p.depth;
-  accumulate<T, false, QT, C, BM, BN, WM, WN, KS, false>(
-      static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, Q,
-      QT ? p.cols : p.depth, p.cols - j0, depth, smem_all + kg * C::kRing, wave,
-      kg, acc, 0, none);
-  if (KS > 1 && kg > 0) return;
-
-  using S = OutStage<C::kWTN>;
+  Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
+  pipe.begin(static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, b,
+             QT ? p.cols : p.depth, p.cols - j0, group < 0 ? 0 : p.depth, kg);
+  pipe.template run<false>(acc, 0, none);
+  if constexpr (KS > 1) {
+    pipe.merge(kg, acc);
+    if (kg > 0) return;
+  }
   const int wm = wave / WN, wn = wave % WN;
-  char* stage = smem_all + out_stage<C>(depth) + wave * S::kBytes;
-  const int c = j0 + wn * C::kWTN + S::col(lane);
-  const bool inside_c = c < p.cols;
-  float bias[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
-  if (p.bias && group >= 0 && inside_c) {
-    const int64_t at = (int64_t)group * p.cols + c;
-    if (p.bias_f32) load_vec<float, 8>(static_cast<const float*>(p.bias) + at, bias);
-    else load_vec<T, 8>(static_cast<const T*>(p.bias) + at, bias);
-  }
-  // One copy of the epilogue's code for all rows (the loops are kept as loops): unrolled over the
-  // block, with every activation in it, it was larger than the instruction cache and took longer
-  // than twelve slabs' multiplies.
-#pragma unroll 1
-  for (int fm = 0; fm < C::kFM; ++fm) {
-#pragma unroll
-    for (int f = 0; f < C::kFM; ++f)
-      if (f == fm) S::put(stage, acc[f], lane);
-    const int64_t r0 = row0 + wm * C::kWTM + fm * 32 + S::row(0, lane);
-    // the lane's pieces of the operands, one pass ahead
-    u32x4_t aux{}, add{};
-    auto fetch = [&](int i) {
-      const int64_t r = r0 + i * S::kRows;
-      if (!inside_c || r >= end) return;
-      if (p.aux) aux = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.aux) + r * p.ldaux + c);
-      if (p.add) add = *reinterpret_cast<const u32x4_t*>(static_cast<const T*>(p.add) + r * p.ldadd + c);
-    };
-    fetch(0);
-#pragma unroll 1
-    for (int i = 0; i < S::kPasses; ++i) {
-      const int64_t r = r0 + i * S::kRows;
-      const bool inside = inside_c && r < end;
-      const u32x4_t aux_now = aux, add_now = add;
-      if (i + 1 < S::kPasses) fetch(i + 1);
-      float v[8];
-      S::get(stage, i, lane, v);
-      if (p.gradient) {
-        if (p.aux) {
-          float z[8];
-          unpack8<T>(aux_now, z);
-          scale_by_slope<8>(p.act, z, v);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += bias[e];
-        if (p.keep && inside)
-          *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.keep) + r * p.ldkeep + c) =
-              group < 0 ? u32x4_t{} : pack8<T>(v);
-        activate<8>(p.act, v);
-      }
-      if (p.add) {
-        float a[8];
-        unpack8<T>(add_now, a);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += a[e];
-      }
-      if (inside)
-        *reinterpret_cast<u32x4_t*>(static_cast<T*>(p.out) + r * p.ldout + c) =
-            group < 0 ? u32x4_t{} : pack8<T>(v);
-    }
-  }
+  rows_epilogue<T, C>(p, acc, pipe.spare() + wave * S::kBytes, row0 + wm * C::kWTM, end, group,
+                      j0 + wn * C::kWTN + S::col(lane), lane);
 }
 
 // Workgroups in the order [groups][splits][tiles]; split s of a group takes the s-th part of its
@@ -472,10 +541,10 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   f32x4_t sums{};
   const int sum = !p.db ? 0 : p.dz_is_q ? (ti == 0 ? 2 : 0) : (tj == 0 ? 1 : 0);
-  accumulate<T, true, true, C, BM, BN, WM, WN, 1, true>(
-      static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.pi - i0,
-      static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.qj - j0, k1 - k0, smem, wave, 0,
-      acc, sum, sums);
+  Pipe<T, true, true, BM, BN, WM, WN, 1> pipe(smem, wave);
+  pipe.begin(static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.pi - i0,
+             static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.qj - j0, k1 - k0, 0);
+  pipe.template run<true>(acc, sum, sums);
 
   const int wm = wave / WN, wn = wave % WN;
   const int width = p.dz_is_q ? p.qj : p.pi;
@@ -487,7 +556,7 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
     if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[1];
   }
   using S = OutStage<C::kWTN>;
-  char* stage = smem + out_stage<C>(k1 - k0) + wave * S::kBytes;
+  char* stage = pipe.spare() + wave * S::kBytes;
   const int c = j0 + wn * C::kWTN + S::col(lane);
 #pragma unroll
   for (int fm = 0; fm < C::kFM; ++fm) {
