@@ -458,222 +458,290 @@ def rail_scalars(step: int):
 
 ANVIL_F32, ANVIL_BF16, ANVIL_F16 = 0, 1, 2
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}
-_dtypes = {}
+_SIXTEEN = (ANVIL_BF16, ANVIL_F16)
+_torch = None
+_codes = {}
+
+# A call of a small layer lasts as long as its preparation on the host, so these checks read each
+# property of a tensor once.
 
 
-def _dtype_code(t, name, allowed=None):
-    if not _dtypes:
+def _module():
+    global _torch
+    if _torch is None:
         import torch
-        _dtypes.update({torch.float32: ANVIL_F32, torch.bfloat16: ANVIL_BF16,
-                        torch.float16: ANVIL_F16})
-    code = _dtypes.get(t.dtype)
-    if code is None or (allowed is not None and code not in allowed):
-        raise TypeError(f"{name} has an unsupported dtype ({t.dtype})")
-    return code
+        _codes.update({torch.float32: ANVIL_F32, torch.bfloat16: ANVIL_BF16,
+                       torch.float16: ANVIL_F16})
+        _torch = torch
+    return _torch
 
 
-def _on_gpu(t, name):
-    import torch
+def _device(t, name):
+    """The index of the current device, which t has to be on."""
+    torch = _module()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU (got {t.device})")
-    if t.get_device() != torch.cuda.current_device():
+    index = t.get_device()
+    if index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device "
                          f"cuda:{torch.cuda.current_device()} (use torch.cuda.set_device)")
+    return index
 
 
-def _rows(t, name, dtype=None, shape=None):
-    """Checks a [rows, width] operand and returns its row pitch in elements."""
-    _on_gpu(t, name)
+def _raw_stream(stream, device):
+    """The HIP stream handle of `stream`, by default the current one."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _code(t, name, allowed):
+    code = _codes.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{name} has an unsupported dtype ({t.dtype})")
+    return code
+
+
+def _same(t, name, dtype, device):
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+
+
+def _rows(t, name):
+    """Checks the layout of a [rows, width] operand; returns (rows, width, row pitch)."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be [rows, width] (got {t.dim()} dimensions)")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    width, (step, last) = t.shape[1], t.stride()
-    if last != 1 and width > 1:
+    rows, width = t.shape
+    pitch, step = t.stride()
+    if step != 1 and width > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.shape[0] > 1 and step < width:
-        raise ValueError(f"{name}: its rows overlap (pitch {step}, width {width})")
-    return max(step, width)
+    if pitch < width:
+        if rows > 1:
+            raise ValueError(f"{name}: its rows overlap (pitch {pitch}, width {width})")
+        pitch = width
+    return rows, width, pitch
+
+
+def _operand(t, name, dtype, device, rows, width):
+    """(pointer, pitch) of a further [rows, width] operand, or (None, 0)."""
+    if t is None:
+        return None, 0
+    _same(t, name, dtype, device)
+    r, w, pitch = _rows(t, name)
+    if r != rows or w != width:
+        raise ValueError(f"{name} must have shape {(rows, width)} (got {tuple(t.shape)})")
+    return t.data_ptr(), pitch
+
+
+def _dense(t, name, dtype, device, shape):
+    """Pointer of a contiguous operand of the given shape."""
+    _same(t, name, dtype, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _parameter(t, name, code, like, device, shape):
+    """(pointer, dtype code) of an optional parameter: fp32 or of the dtype of `like`."""
+    if t is None:
+        return None, code
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    own = _code(t, name, (ANVIL_F32, code))
+    return _dense(t, name, t.dtype, device, shape), own
 
 
 def _empty(shape, dtype, device, stream):
     """torch.empty for a call on `stream`: memory of another stream than the current one is kept
     from reuse until that stream is done with it."""
-    import torch
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = _torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        if s != torch.cuda.current_stream():
+        s = stream if isinstance(stream, _torch.cuda.Stream) else \
+            _torch.cuda.ExternalStream(int(stream))
+        if s != _torch.cuda.current_stream():
             t.record_stream(s)
     return t
 
 
 def _act(name):
-    if name not in ACTIVATIONS:
+    code = ACTIVATIONS.get(name)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)} (got {name!r})")
-    return ACTIVATIONS[name]
+    return code
 
 
 def _scratch(workspace, need, device, stream):
-    """(pointer, bytes) of the workspace: the caller's, or one of `need` bytes."""
-    import torch
+    """The workspace: the caller's, or one of `need` bytes (None for 0)."""
     if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = _empty((need,), torch.uint8, device, stream)
-    else:
-        _need(workspace, "workspace", torch.uint8)
-    return _ptr(workspace), workspace.numel(), workspace
+        return _empty((need,), _torch.uint8, device, stream) if need else None
+    _same(workspace, "workspace", _torch.uint8, device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
 
 
 def anvil_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """Layer norm of each row of x (bf16, fp16 or fp32 [rows, cols]); weight and bias [cols] are
     fp32 or of x's dtype.  Returns (y, mean, rstd), the last two fp32 [rows] for the backward
     pass."""
-    import torch
-    ldx = _rows(x, "x")
-    code = _dtype_code(x, "x")
-    rows, cols = x.shape
-    param = code
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            param = _dtype_code(t, name, (ANVIL_F32, code))
-            _need(t, name, t.dtype, (cols,))
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    device = _device(x, "x")
+    code = _code(x, "x", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
+    rows, cols, ldx = _rows(x, "x")
+    w, w_code = _parameter(weight, "weight", code, x, device, (cols,))
+    b, b_code = _parameter(bias, "bias", code, x, device, (cols,))
+    if w is not None and b is not None and w_code != b_code:
         raise TypeError("weight and bias must have one dtype")
     if out is None:
         out = _empty((rows, cols), x.dtype, x.device, stream)
-    ldy = _rows(out, "out", x.dtype, (rows, cols))
-    mean = _empty((rows,), torch.float32, x.device, stream)
-    rstd = _empty((rows,), torch.float32, x.device, stream)
-    _check("anvil_layer_norm", load().anvil_layer_norm(
-        _ptr(x), ldx, _ptr(weight), _ptr(bias), param, eps, _ptr(out), ldy, _ptr(mean), _ptr(rstd),
-        code, rows, cols, _stream(stream)))
+    y, ldy = _operand(out, "out", x.dtype, device, rows, cols)
+    stats = _empty((2, rows), _torch.float32, x.device, stream)
+    mean, rstd = stats.unbind()
+    at = stats.data_ptr()
+    status = load().anvil_layer_norm(x.data_ptr(), ldx, w, b, w_code if w is not None else b_code,
+                                     eps, y, ldy, at, at + 4 * rows, code, rows, cols,
+                                     _raw_stream(stream, device))
+    if status:
+        _check("anvil_layer_norm", status)
     return out, mean, rstd
 
 
 def anvil_layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, stream=None):
     """Backward pass of anvil_layer_norm: returns (dx, dweight, dbias), the last two fp32 [cols].
     Without a weight (None) it was 1; dweight and dbias are returned all the same."""
-    import torch
-    ldx = _rows(x, "x")
-    code = _dtype_code(x, "x")
-    rows, cols = x.shape
-    lddy = _rows(dy, "dy", x.dtype, (rows, cols))
-    param = code
-    if weight is not None:
-        param = _dtype_code(weight, "weight", (ANVIL_F32, code))
-        _need(weight, "weight", weight.dtype, (cols,))
-    _need(mean, "mean", torch.float32, (rows,))
-    _need(rstd, "rstd", torch.float32, (rows,))
+    device = _device(x, "x")
+    code = _code(x, "x", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
+    rows, cols, ldx = _rows(x, "x")
+    g, lddy = _operand(dy, "dy", x.dtype, device, rows, cols)
+    w, w_code = _parameter(weight, "weight", code, x, device, (cols,))
+    m = _dense(mean, "mean", _torch.float32, device, (rows,))
+    r = _dense(rstd, "rstd", _torch.float32, device, (rows,))
     if out is None:
         out = _empty((rows, cols), x.dtype, x.device, stream)
-    lddx = _rows(out, "out", x.dtype, (rows, cols))
-    sums = _empty((2, cols), torch.float32, x.device, stream)
-    dweight, dbias = sums[0], sums[1]
+    dx, lddx = _operand(out, "out", x.dtype, device, rows, cols)
+    sums = _empty((2, cols), _torch.float32, x.device, stream)
+    dweight, dbias = sums.unbind()
+    at = sums.data_ptr()
     lib = load()
-    ws, wsb, keep = _scratch(workspace, lib.anvil_layer_norm_grad_workspace(rows, cols), x.device,
-                             stream)
-    _check("anvil_layer_norm_grad", lib.anvil_layer_norm_grad(
-        _ptr(dy), lddy, _ptr(x), ldx, _ptr(weight), param, _ptr(mean), _ptr(rstd), _ptr(out), lddx,
-        _ptr(dweight), _ptr(dbias), code, rows, cols, ws, wsb, _stream(stream)))
+    ws = _scratch(workspace, lib.anvil_layer_norm_grad_workspace(rows, cols), device, stream)
+    status = lib.anvil_layer_norm_grad(
+        g, lddy, x.data_ptr(), ldx, w, w_code, m, r, dx, lddx, at, at + 4 * cols, code, rows, cols,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _raw_stream(stream, device))
+    if status:
+        _check("anvil_layer_norm_grad", status)
     return out, dweight, dbias
 
 
-def _weight(w, x, w_kn, experts):
-    """(n, k) of a weight matrix or stack of x's dtype."""
-    _need(w, "w", x.dtype)
-    if w.dim() != (2 if experts is None else 3):
+def _weight(w, dtype, device, w_kn, experts):
+    """(pointer, n, k) of a weight matrix or stack."""
+    _same(w, "w", dtype, device)
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    shape = w.shape
+    if len(shape) != (2 if experts is None else 3):
         raise ValueError("w must be [n, k], or [experts, n, k] for experts")
-    if experts is not None and w.shape[0] != experts:
-        raise ValueError(f"w holds {w.shape[0]} experts, offsets {experts}")
-    n, k = w.shape[-2:]
-    return (k, n) if w_kn else (n, k)
+    if experts is not None and shape[0] != experts:
+        raise ValueError(f"w holds {shape[0]} experts, offsets {experts}")
+    n, k = shape[-2:]
+    return (w.data_ptr(), k, n) if w_kn else (w.data_ptr(), n, k)
 
 
-def _offsets(offsets):
+def _offsets(offsets, device):
     """(pointer, bits, experts) of the row offsets."""
-    import torch
-    _on_gpu(offsets, "offsets")
-    if offsets.dtype not in (torch.int32, torch.int64):
+    if not isinstance(offsets, _torch.Tensor):
+        raise TypeError("offsets must be a torch.Tensor")
+    if offsets.dtype not in (_torch.int32, _torch.int64):
         raise TypeError("offsets must be int32 or int64")
+    if offsets.get_device() != device:
+        raise ValueError(f"offsets must be on cuda:{device} (got {offsets.device})")
     if offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous [experts + 1] tensor")
-    return _ptr(offsets), 32 if offsets.dtype == torch.int32 else 64, offsets.numel() - 1
+    return offsets.data_ptr(), 32 if offsets.dtype == _torch.int32 else 64, offsets.numel() - 1
 
 
 def _linear(fn, x, w, offsets, bias, residual, act, w_kn, keep_preact, preact, out, stream):
-    ldx = _rows(x, "x")
-    code = _dtype_code(x, "x", (ANVIL_BF16, ANVIL_F16))
-    group = () if offsets is None else _offsets(offsets)
+    device = _device(x, "x")
+    code = _code(x, "x", _SIXTEEN)
+    dtype = x.dtype
+    rows, k, ldx = _rows(x, "x")
+    group = () if offsets is None else _offsets(offsets, device)
     experts = group[2] if group else None
-    n, k = _weight(w, x, w_kn, experts)
-    rows = x.shape[0]
-    if x.shape[1] != k:
-        raise ValueError(f"x has width {x.shape[1]}, w takes {k}")
-    bias_code = code
-    if bias is not None:
-        bias_code = _dtype_code(bias, "bias", (ANVIL_F32, code))
-        _need(bias, "bias", bias.dtype, (n,) if experts is None else (experts, n))
-    ldr = _rows(residual, "residual", x.dtype, (rows, n)) if residual is not None else 0
+    wp, n, wk = _weight(w, dtype, device, w_kn, experts)
+    if k != wk:
+        raise ValueError(f"x has width {k}, w takes {wk}")
+    b, b_code = _parameter(bias, "bias", code, x, device,
+                           (n,) if experts is None else (experts, n))
+    r, ldr = _operand(residual, "residual", dtype, device, rows, n)
     if out is None:
-        out = _empty((rows, n), x.dtype, x.device, stream)
-    ldy = _rows(out, "out", x.dtype, (rows, n))
+        out = _empty((rows, n), dtype, x.device, stream)
+    y, ldy = _operand(out, "out", dtype, device, rows, n)
     if preact is None and keep_preact:
-        preact = _empty((rows, n), x.dtype, x.device, stream)
-    ldz = _rows(preact, "preact", x.dtype, (rows, n)) if preact is not None else 0
-    _check(fn, getattr(load(), fn)(
-        _ptr(x), ldx, _ptr(w), int(w_kn), *group, _ptr(bias), bias_code, _act(act), _ptr(residual),
-        ldr, _ptr(out), ldy, _ptr(preact), ldz, code, rows, n, k, _stream(stream)))
+        preact = _empty((rows, n), dtype, x.device, stream)
+    z, ldz = _operand(preact, "preact", dtype, device, rows, n)
+    status = getattr(load(), fn)(
+        x.data_ptr(), ldx, wp, 1 if w_kn else 0, *group, b, b_code, _act(act), r, ldr, y, ldy, z,
+        ldz, code, rows, n, k, _raw_stream(stream, device))
+    if status:
+        _check(fn, status)
     return out, preact
 
 
 def _grad_input(fn, dz, w, offsets, preact, act, add, w_kn, out, stream):
-    lddz = _rows(dz, "dz")
-    code = _dtype_code(dz, "dz", (ANVIL_BF16, ANVIL_F16))
-    group = () if offsets is None else _offsets(offsets)
-    n, k = _weight(w, dz, w_kn, group[2] if group else None)
-    rows = dz.shape[0]
-    if dz.shape[1] != n:
-        raise ValueError(f"dz has width {dz.shape[1]}, w gives {n}")
-    ldz = _rows(preact, "preact", dz.dtype, (rows, k)) if preact is not None else 0
-    ldadd = _rows(add, "add", dz.dtype, (rows, k)) if add is not None else 0
+    device = _device(dz, "dz")
+    code = _code(dz, "dz", _SIXTEEN)
+    dtype = dz.dtype
+    rows, n, lddz = _rows(dz, "dz")
+    group = () if offsets is None else _offsets(offsets, device)
+    wp, wn, k = _weight(w, dtype, device, w_kn, group[2] if group else None)
+    if n != wn:
+        raise ValueError(f"dz has width {n}, w gives {wn}")
+    z, ldz = _operand(preact, "preact", dtype, device, rows, k)
+    a, lda = _operand(add, "add", dtype, device, rows, k)
     if out is None:
-        out = _empty((rows, k), dz.dtype, dz.device, stream)
-    lddx = _rows(out, "out", dz.dtype, (rows, k))
-    _check(fn, getattr(load(), fn)(
-        _ptr(dz), lddz, _ptr(w), int(w_kn), *group, _ptr(preact), ldz, _act(act), _ptr(add), ldadd,
-        _ptr(out), lddx, code, rows, n, k, _stream(stream)))
+        out = _empty((rows, k), dtype, dz.device, stream)
+    dx, lddx = _operand(out, "out", dtype, device, rows, k)
+    status = getattr(load(), fn)(
+        dz.data_ptr(), lddz, wp, 1 if w_kn else 0, *group, z, ldz, _act(act), a, lda, dx, lddx,
+        code, rows, n, k, _raw_stream(stream, device))
+    if status:
+        _check(fn, status)
     return out
 
 
 def _grad_weight(fn, dz, x, offsets, w_kn, out, out_dtype, want_bias, workspace, stream):
-    import torch
-    lddz = _rows(dz, "dz")
-    code = _dtype_code(dz, "dz", (ANVIL_BF16, ANVIL_F16))
-    rows, n = dz.shape
-    ldx = _rows(x, "x", dz.dtype)
-    k = x.shape[1]
-    if x.shape[0] != rows:
-        raise ValueError(f"x has {x.shape[0]} rows, dz {rows}")
-    group = () if offsets is None else _offsets(offsets)
+    device = _device(dz, "dz")
+    code = _code(dz, "dz", _SIXTEEN)
+    rows, n, lddz = _rows(dz, "dz")
+    _same(x, "x", dz.dtype, device)
+    x_rows, k, ldx = _rows(x, "x")
+    if x_rows != rows:
+        raise ValueError(f"x has {x_rows} rows, dz {rows}")
+    group = () if offsets is None else _offsets(offsets, device)
     stack = (group[2],) if group else ()
     shape = stack + ((k, n) if w_kn else (n, k))
     if out is None:
-        out = _empty(shape, out_dtype or torch.float32, dz.device, stream)
-    out_code = _dtype_code(out, "out", (ANVIL_F32, code))
-    _need(out, "out", out.dtype, shape)
-    dbias = _empty(stack + (n,), torch.float32, dz.device, stream) if want_bias else None
+        out = _empty(shape, out_dtype or _torch.float32, dz.device, stream)
+    dw, out_code = _parameter(out, "out", code, dz, device, shape)
+    dbias = _empty(stack + (n,), _torch.float32, dz.device, stream) if want_bias else None
     lib = load()
-    need = lib.anvil_linear_grad_weight_workspace(int(w_kn), rows, n, k, stack[0] if stack else 1)
-    ws, wsb, keep = _scratch(workspace, need, dz.device, stream)
-    _check(fn, getattr(lib, fn)(
-        _ptr(dz), lddz, _ptr(x), ldx, int(w_kn), *group, _ptr(out), out_code, _ptr(dbias), code,
-        rows, n, k, ws, wsb, _stream(stream)))
+    need = lib.anvil_linear_grad_weight_workspace(1 if w_kn else 0, rows, n, k,
+                                                  stack[0] if stack else 1)
+    ws = _scratch(workspace, need, device, stream)
+    status = getattr(lib, fn)(
+        dz.data_ptr(), lddz, x.data_ptr(), ldx, 1 if w_kn else 0, *group, dw, out_code,
+        dbias.data_ptr() if want_bias else None, code, rows, n, k,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _raw_stream(stream, device))
+    if status:
+        _check(fn, status)
     return out, dbias
 
 
@@ -703,16 +771,19 @@ def anvil_linear_grad_weight(dz, x, w_kn=False, out=None, out_dtype=None, want_b
 
 def anvil_activation_grad(dy, preact, act, out=None, stream=None):
     """dz = dy * act'(preact), elementwise on [rows, n]."""
-    lddy = _rows(dy, "dy")
-    code = _dtype_code(dy, "dy", (ANVIL_BF16, ANVIL_F16))
-    rows, n = dy.shape
-    ldz = _rows(preact, "preact", dy.dtype, (rows, n))
+    device = _device(dy, "dy")
+    code = _code(dy, "dy", _SIXTEEN)
+    rows, n, lddy = _rows(dy, "dy")
+    z, ldz = _operand(preact, "preact", dy.dtype, device, rows, n)
+    if z is None:
+        raise ValueError("preact must be given")
     if out is None:
         out = _empty((rows, n), dy.dtype, dy.device, stream)
-    lddz = _rows(out, "out", dy.dtype, (rows, n))
-    _check("anvil_activation_grad", load().anvil_activation_grad(
-        _ptr(dy), lddy, _ptr(preact), ldz, _act(act), _ptr(out), lddz, code, rows, n,
-        _stream(stream)))
+    dz, lddz = _operand(out, "out", dy.dtype, device, rows, n)
+    status = load().anvil_activation_grad(dy.data_ptr(), lddy, z, ldz, _act(act), dz, lddz, code,
+                                          rows, n, _raw_stream(stream, device))
+    if status:
+        _check("anvil_activation_grad", status)
     return out
 
 
