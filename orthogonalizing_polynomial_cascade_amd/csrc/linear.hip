@@ -196,13 +196,36 @@ __global__ __launch_bounds__(256) void any_weight_kernel(WeightProduct p, float*
   }
 }
 
-// Adds the splits' planes in order: n words of `out` from planes n words apart.
+// Adds the splits' planes in order: dw (n words, then the nb words of db, which has planes of its own
+// behind dw's).  Bound by memory: four words a lane and access, two planes' reads in flight.
 template <typename O>
-__global__ __launch_bounds__(256) void join_kernel(const float* ws, int splits, int64_t n, O* out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void join_kernel(const float* ws, int splits, int64_t n, O* dw,
+                                                   int64_t nb, float* db) {
+  const int64_t wide = n / 4;   // n is a multiple of 4, or the last words go one by one
+  const int64_t step = (int64_t)gridDim.x * 256;
+  const int64_t me = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (int64_t i = me; i < wide; i += step) {
+    float s[4];
+    load_vec<float, 4>(ws + i * 4, s);
+#pragma unroll 2
+    for (int k = 1; k < splits; ++k) {
+      float v[4];
+      load_vec<float, 4>(ws + k * n + i * 4, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    store_vec<O, 4>(dw + i * 4, s);
+  }
+  for (int64_t i = wide * 4 + me; i < n; i += step) {
     float s = ws[i];
     for (int k = 1; k < splits; ++k) s += ws[k * n + i];
-    out[i] = from_f32<O>(s);
+    dw[i] = from_f32<O>(s);
+  }
+  const float* wb = ws + splits * n;
+  for (int64_t i = me; i < nb; i += step) {
+    float s = wb[i];
+    for (int k = 1; k < splits; ++k) s += wb[k * nb + i];
+    db[i] = s;
   }
 }
 
@@ -244,14 +267,12 @@ hipError_t launch_weight_t(const WeightProduct& a, float* ws, hipStream_t stream
   }
   if (e != hipSuccess || splits == 1) return e;
   const int64_t n = (int64_t)a.groups.count * a.pi * a.qj;
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil64(n, 256), 4096);
-  if (a.dw_f32) join_kernel<float><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<float*>(a.dw));
-  else join_kernel<T><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<T*>(a.dw));
-  e = hipGetLastError();
-  if (e != hipSuccess || !a.db) return e;
-  const int64_t nb = (int64_t)a.groups.count * (a.dz_is_q ? a.qj : a.pi);
-  join_kernel<float><<<(unsigned)std::min<int64_t>(ceil64(nb, 256), 4096), 256, 0, stream>>>(
-      ws + splits * n, splits, nb, a.db);
+  const int64_t nb = a.db ? (int64_t)a.groups.count * (a.dz_is_q ? a.qj : a.pi) : 0;
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil64(n, 1024), 4096);
+  if (a.dw_f32)
+    join_kernel<float><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<float*>(a.dw), nb, a.db);
+  else
+    join_kernel<T><<<grid, 256, 0, stream>>>(ws, splits, n, static_cast<T*>(a.dw), nb, a.db);
   return hipGetLastError();
 }
 

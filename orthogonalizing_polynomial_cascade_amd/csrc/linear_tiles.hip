@@ -18,6 +18,7 @@
 //    and the first set adds the others' sums in order: for calls with fewer tiles than CUs.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "activation.h"
@@ -608,13 +609,50 @@ int64_t row_tiles(const RowsProduct& a, int side) {
   return ceil64(a.rows, side) + (a.groups.offsets ? a.groups.count + 1 : 0);
 }
 
+// Time of one launch in microseconds, from a fit of measured calls (32 .. 32768 rows, 256 .. 4096
+// columns, depths 512 .. 4096): rounds of workgroups, each a fixed part (first slab, epilogue) and
+// one for each 64-deep slab.  128x128 tiles run two to a CU; where one round leaves CUs with one,
+// that one is faster.  GELU and SiLU lengthen the epilogue by what their instructions take on the
+// rows one CU finishes at once.  Examples, us measured with 64 / 128 / 256 rows and columns:
+//   4096 x 768, depth 2816      42.9 / 36.3 / 56.9        2048 x 2816, depth 768  35.9 / 17.4 / 23.4
+//   16384 x 768, depth 2816    161.2 / 79.9 / 65.8        4096 x 2816, depth 768  63.5 / 28.6 / 25.8
+//   2048 x 512, depth 4096      20.0 / 44.0 / 76.6        with gelu               70.0 / 33.3 / 34.2
+double rounds(double workgroups, double slots) { return std::ceil(workgroups / slots); }
+
+double tile_cost(int side, double tiles, double slabs, bool heavy) {
+  switch (side) {
+    case 64: return rounds(tiles, 256) * (2.2 + 0.25 * slabs + (heavy ? 0.6 : 0.0));
+    case 128: {
+      const double pair = 4.0 + 0.9 * slabs + (heavy ? 4.0 : 0.0);
+      const double one = 5.0 + 0.6 * slabs + (heavy ? 2.0 : 0.0);
+      const double whole = std::floor(tiles / 512), rest = tiles - whole * 512;
+      return whole * pair + (rest == 0 ? 0.0 : rest <= 256 ? one : pair);
+    }
+    default: return rounds(tiles, 256) * (10.0 + 1.2 * slabs + (heavy ? 8.0 : 0.0));
+  }
+}
+
 RowsTile rows_tile(const RowsProduct& a) {
   const int64_t stack = a.groups.offsets ? std::max(1, a.groups.count) : 1;
   const int64_t height = ceil64(a.rows, stack);   // rows of a typical group
+  // up to 32 rows a taller tile only adds work on rows that are not there
   if (height <= 32) return kRows32;
-  if (stack * ceil64(height, 256) * ceil64(a.cols, 256) >= 200) return kRows256;
-  if (stack * ceil64(height, 128) * ceil64(a.cols, 128) >= 256) return kRows128;
-  return kRows64;
+  const bool heavy = a.act == kActGelu || a.act == kActSilu;
+  const double slabs = (double)ceil64(a.depth, kBK);
+  RowsTile best = kRows64;
+  double least = 0;
+  for (RowsTile t : {kRows64, kRows128, kRows256}) {
+    const int side = kRowsSide[t];
+    // a group's last tile is half full on average
+    const double tiles_m = a.groups.offsets ? (double)a.rows / side + 0.5 * (double)stack
+                                            : (double)ceil64(a.rows, side);
+    const double cost = tile_cost(side, tiles_m * (double)ceil64(a.cols, side), slabs, heavy);
+    if (t == kRows64 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
@@ -639,8 +677,35 @@ hipError_t rows_variant(const RowsProduct& a, hipStream_t stream) {
 bool multiple8(int64_t v) { return v % 8 == 0; }
 bool wide_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-bool big_weight_tiles(const WeightProduct& a) {
-  return ceil64(a.pi, 256) * ceil64(a.qj, 256) * a.groups.count >= 24 && a.rows / a.groups.count >= 512;
+// Tile side and splits of each group's rows: the least of the tiles' time (as above; the K-major
+// operands' slabs take 1.25 and 0.95 us) and the join's, which writes and reads each split's sums.
+struct WeightPlan {
+  int side, splits;
+};
+
+WeightPlan weight_plan(const WeightProduct& a) {
+  const double slabs = std::max(1.0, (double)a.rows / a.groups.count / kBK);
+  const double bytes = 4.0 * a.groups.count * a.pi * a.qj;
+  WeightPlan best{128, 1};
+  double least = 0;
+  for (int side : {128, 256}) {
+    const double tiles =
+        (double)ceil64(a.pi, side) * (double)ceil64(a.qj, side) * (double)a.groups.count;
+    for (int splits = 1; splits <= 64; ++splits) {
+      const double each = std::ceil(slabs / splits);
+      if (splits > 1 && each < 4) break;   // at least 256 rows a split
+      const double workgroups = tiles * splits;
+      double cost = side == 256 ? rounds(workgroups, 256) * (10.0 + 1.25 * each)
+                                : rounds(workgroups, 512) * (4.0 + 0.95 * each);
+      if (side == 128 && workgroups <= 256) cost = 5.0 + 0.62 * each;
+      if (splits > 1) cost += 5.0 + (2 * splits + 1) * bytes / 5e6;
+      if ((side == 128 && splits == 1) || cost < least) {
+        best = {side, splits};
+        least = cost;
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int OCC>
@@ -655,7 +720,7 @@ hipError_t weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream
 
 template <typename T>
 hipError_t weight_variant(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
-  if (big_weight_tiles(a)) return weight_tiles<T, 256, 256, 2, 4, 2>(a, ws, splits, stream);
+  if (weight_plan(a).side == 256) return weight_tiles<T, 256, 256, 2, 4, 2>(a, ws, splits, stream);
   return weight_tiles<T, 128, 128, 2, 2, 2>(a, ws, splits, stream);
 }
 
@@ -678,21 +743,14 @@ hipError_t launch_rows_tiles(const RowsProduct& a, hipStream_t stream) {
 }
 
 bool tiles_take_weight(const WeightProduct& a) {
-  const int side = big_weight_tiles(a) ? 256 : 128;
-  if (ceil64(a.pi, side) * ceil64(a.qj, side) * a.groups.count * weight_tile_splits(a) > kMaxGrid)
+  const WeightPlan plan = weight_plan(a);
+  if (ceil64(a.pi, plan.side) * ceil64(a.qj, plan.side) * a.groups.count * plan.splits > kMaxGrid)
     return false;
   return multiple8(a.pi) && multiple8(a.qj) && multiple8(a.ldp) && multiple8(a.ldq) &&
          wide_aligned(a.p) && wide_aligned(a.q) && wide_aligned(a.dw);
 }
 
-int weight_tile_splits(const WeightProduct& a) {
-  const bool big = big_weight_tiles(a);
-  const int side = big ? 256 : 128;
-  const int64_t slots = big ? 256 : 512;
-  const int64_t tiles = ceil64(a.pi, side) * ceil64(a.qj, side) * a.groups.count;
-  const int64_t most = std::max<int64_t>(1, a.rows / a.groups.count / 512);
-  return (int)std::max<int64_t>(1, std::min({slots / tiles, most, int64_t(64)}));
-}
+int weight_tile_splits(const WeightProduct& a) { return weight_plan(a).splits; }
 
 hipError_t launch_weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
   return a.f16 ? weight_variant<f16>(a, ws, splits, stream)
