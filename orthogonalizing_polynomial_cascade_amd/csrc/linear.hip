@@ -105,12 +105,13 @@ __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t 
 }
 
 template <typename T, bool QT>
-__global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int64_t tiles_m, int tiles_n) {
+__global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int tiles_n) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t tile = blockIdx.x; tile < tiles_m * tiles_n; tile += gridDim.x) {
+  RowTiles<kAnyTile> tiles(p.groups, p.rows);
+  for (int64_t tile = blockIdx.x; tile < (int64_t)tiles.total * tiles_n; tile += gridDim.x) {
     int64_t row0, end;
     int group;
-    if (!row_tile<kAnyTile>(p.groups, p.rows, tile / tiles_n, &row0, &end, &group)) return;
+    tiles.find((int)(tile / tiles_n), &row0, &end, &group);
     const int64_t j0 = (tile % tiles_n) * kAnyTile;
     const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
     f32x16_t acc = {};
@@ -237,9 +238,9 @@ hipError_t launch_rows_t(const RowsProduct& a, hipStream_t stream) {
   const int64_t tiles_m = ceil64(a.rows, kAnyTile) + (a.groups.offsets ? a.groups.count + 1 : 0);
   const int tiles_n = (int)ceil64(a.cols, kAnyTile);
   if (a.b_kmajor)
-    any_rows_kernel<T, true><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_m, tiles_n);
+    any_rows_kernel<T, true><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
   else
-    any_rows_kernel<T, false><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_m, tiles_n);
+    any_rows_kernel<T, false><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
   return hipGetLastError();
 }
 

@@ -80,55 +80,102 @@ __device__ __forceinline__ void group_rows(const Groups& g, int64_t rows, int e,
   *end = hi > lo ? hi : lo;
 }
 
+__device__ __forceinline__ int scan_max(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o && u > v) v = u;
+  }
+  return v;
+}
+__device__ __forceinline__ int scan_sum(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
 // The rows in tiles of TILE, group by group; rows without an owner form two groups of their own,
-// before the first and after the last.  Finds tile t: its first row and the end of its group's
-// rows, and its group (-1: no owner).  Returns false past the last tile.
+// before the first and after the last.  Segment s = 0 .. count + 1 spans bound(s) .. bound(s + 1):
+// bound(0) = 0, bound(s) = the running maximum of the offsets up to s - 1, bound(count + 2) = rows.
+// A wave looks at 64 segments at a time, one a lane.
 template <int TILE>
-__device__ __forceinline__ bool row_tile(const Groups& g, int64_t rows, int64_t t, int64_t* row0,
-                                         int64_t* end, int* group) {
-  if (!g.offsets) {
-    *row0 = t * TILE;
-    *end = rows;
-    *group = 0;
-    return *row0 < rows;
-  }
-  // segment s = 0 .. count + 1 spans bound(s) .. bound(s + 1): bound(0) = 0, bound(s) = the running
-  // maximum of the offsets up to s - 1, bound(count + 2) = rows
-  const int lane = threadIdx.x & 63;
-  int64_t start = 0;      // bound at the chunk's first segment
-  int64_t done = 0;       // tiles of the segments before the chunk
-  for (int s0 = 0; s0 < g.count + 2; s0 += 64) {
+struct RowTiles {
+  const Groups& g;
+  int rows, lane;
+  int lo, hi, upto;   // the lane's segment of the current chunk, tiles up to and with it
+  int start, done;    // bound at the next chunk's first segment, tiles before the next chunk
+  int total;          // tiles in all
+
+  __device__ __forceinline__ void chunk(int s0) {
     const int s = s0 + lane;
-    int64_t hi = s <= g.count ? raw_offset(g, s, rows) : rows;   // bound(s + 1), to be a maximum
-    hi = hi > start ? hi : start;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up(hi, o);
-      if (lane >= o && u > hi) hi = u;
-    }
-    int64_t lo = __shfl_up(hi, 1);
+    int v = s <= g.count ? (int)raw_offset(g, s, rows) : rows;
+    v = v > start ? v : start;
+    hi = scan_max(v, lane);
+    lo = __shfl_up(hi, 1);
     if (lane == 0) lo = start;
-    const int64_t mine = (hi - lo + TILE - 1) / TILE;
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up(upto, o);
-      if (lane >= o) upto += u;
-    }
-    const uint64_t past = __ballot(done + upto > t);
-    if (past) {
-      const int who = __ffsll((unsigned long long)past) - 1;
-      const int64_t first = done + __shfl(upto - mine, who);   // tiles before the segment
-      *row0 = __shfl(lo, who) + (t - first) * TILE;
-      *end = __shfl(hi, who);
-      const int seg = s0 + who;
-      *group = seg == 0 || seg > g.count ? -1 : seg - 1;
-      return true;
-    }
-    done += __shfl(upto, 63);
+    upto = done + scan_sum((int)(((unsigned)(hi - lo) + TILE - 1) / TILE), lane);
     start = __shfl(hi, 63);
+    done = __shfl(upto, 63);
   }
-  return false;
+  __device__ __forceinline__ RowTiles(const Groups& g_, int64_t rows_)
+      : g(g_), rows((int)rows_), lane((int)(threadIdx.x & 63)), start(0), done(0) {
+    if (!g.offsets) {
+      total = (int)(((unsigned)rows + TILE - 1) / TILE);
+      return;
+    }
+    for (int s0 = 0; s0 < g.count + 2; s0 += 64) chunk(s0);
+    total = done;
+  }
+  // Tile t < total: its first row, the end of its group's rows, its group (-1: no owner).
+  __device__ __forceinline__ void find(int t, int64_t* row0, int64_t* end, int* group) {
+    if (!g.offsets) {
+      *row0 = (int64_t)t * TILE;
+      *end = rows;
+      *group = 0;
+      return;
+    }
+    int s0 = 0;
+    if (g.count + 2 > 64) {   // several chunks: walk over them again
+      start = done = 0;
+      for (;; s0 += 64) {
+        chunk(s0);
+        if (t < done) break;
+      }
+    }
+    const int who = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
+    const int left = __shfl(upto, who) - t;    // tiles from t to the segment's end
+    const int first = __shfl(lo, who), last = __shfl(hi, who);
+    const int tiles = (int)(((unsigned)(last - first) + TILE - 1) / TILE);
+    *row0 = first + (int64_t)(tiles - left) * TILE;
+    *end = last;
+    const int seg = s0 + who;
+    *group = seg == 0 || seg > g.count ? -1 : seg - 1;
+  }
+};
+
+// The group at place j when the groups are taken from the one with the most rows down (in their own
+// order from 65 groups on).  Work on the long groups starts first, so that the short ones fill up
+// the end.
+__device__ __forceinline__ int longest_first(const Groups& g, int64_t rows, int j) {
+  if (!g.offsets || g.count > 64) return j;
+  const int lane = threadIdx.x & 63;
+  const int mine = lane <= g.count ? (int)raw_offset(g, lane, rows) : 0;
+  const int bound = scan_max(mine, lane);
+  int next = __shfl_down(bound, 1);
+  if (lane == 63) {   // the 64th group's end is the 65th offset
+    const int v = g.count == 64 ? (int)raw_offset(g, 64, rows) : bound;
+    next = v > bound ? v : bound;
+  }
+  const int size = lane < g.count ? next - bound : -1;
+  int rank = 0;
+  for (int f = 0; f < g.count; ++f) {
+    const int other = __builtin_amdgcn_readlane(size, f);
+    rank += other > size || (other == size && f < lane) ? 1 : 0;
+  }
+  return __ffsll((unsigned long long)__ballot(lane < g.count && rank == j)) - 1;
 }
 
 // linear_tiles.hip: the tiled kernels, for widths and pitches that are multiples of 8 and pointers

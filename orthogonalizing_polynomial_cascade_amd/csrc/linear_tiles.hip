@@ -471,7 +471,7 @@ __device__ __forceinline__ void rows_epilogue(const RowsProduct& p,
 template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
 __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
-void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
+void rows_tile_kernel(RowsProduct p, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
   using S = OutStage<C::kWTN>;
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
@@ -481,12 +481,16 @@ void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
   const int wave = wave_all % C::kWaves;
   char* smem = smem_all + kg * C::kRing;
 
+  // The launch counts one row tile more for each group than there may be.  The tiles that do exist
+  // are dealt out evenly to the XCDs (counted with the others, the last XCD got the empty ones: 24
+  // groups of 32768 rows, 2816 columns of depth 768 took 252 us).
+  RowTiles<BM> rows(p.groups, p.rows);
+  if ((int)blockIdx.x >= rows.total * tiles_n) return;
   int ti, tj;
-  banded(xcd_remap(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, &ti, &tj);
+  banded(xcd_remap(blockIdx.x, rows.total * tiles_n), rows.total, tiles_n, &ti, &tj);
   int64_t row0, end;
   int group;
-  // with groups the launch counts one row tile more for each than there may be
-  if (!row_tile<BM>(p.groups, p.rows, ti, &row0, &end, &group)) return;
+  rows.find(ti, &row0, &end, &group);
   const int j0 = tj * BN;
   const uint16_t* b = static_cast<const uint16_t*>(p.b) +
                       (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth +
@@ -511,7 +515,7 @@ void rows_tile_kernel(RowsProduct p, int tiles_m, int tiles_n) {
                       j0 + wn * C::kWTN + S::col(lane), lane);
 }
 
-// Workgroups in the order [groups][splits][tiles]; split s of a group takes the s-th part of its
+// Split s of a group takes the s-th part of its
 // rows (whole slabs).  Where a group's rows are split, its sums go as fp32 to plane s of the
 // workspace: [splits][groups * pi * qj], then [splits][groups * width of dz].
 template <typename T, int BM, int BN, int WM, int WN, int OCC>
@@ -523,12 +527,17 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int tiles = tiles_i * tiles_j;
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int s = id / tiles % splits;
-  const int e = id / tiles / splits;
+  // Each XCD takes an eighth of every group's tiles (not whole groups, which differ in length), the
+  // longest group's first.
+  const int tiles = tiles_i * tiles_j * splits;
+  const int share = (tiles + 7) / 8;
+  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+  const int unit = xcd * share + at % share;
+  if (unit >= tiles) return;
+  const int e = longest_first(p.groups, p.rows, at / share);
+  const int s = unit / (tiles_i * tiles_j);
   int ti, tj;
-  banded(id % tiles, tiles_i, tiles_j, &ti, &tj);
+  banded(unit % (tiles_i * tiles_j), tiles_i, tiles_j, &ti, &tj);
   const int i0 = ti * BM, j0 = tj * BN;
   int64_t begin, end;
   group_rows(p.groups, p.rows, e, &begin, &end);
@@ -600,10 +609,12 @@ hipError_t launch_lds(K kern, std::atomic<uint64_t>& configured, int64_t grid, i
   return hipGetLastError();
 }
 
-// Tile shapes of the rows product: 32x32 with eight sets of one wave, 64x64 with four sets of four,
-// 128x128 of four waves (two workgroups a CU), 256x256 of eight.
-enum RowsTile { kRows32, kRows64, kRows128, kRows256 };
-constexpr int kRowsSide[] = {32, 64, 128, 256};
+// Tile shapes of the rows product: 32x32 with eight sets of one wave, 32x128 with two sets of four
+// (two workgroups a CU), 64x64 with four sets of four, 128x128 of four waves (two workgroups a CU),
+// 256x256 of eight.
+enum RowsTile { kRows32, kRows32x128, kRows64, kRows128, kRows256 };
+constexpr int kTileRows[] = {32, 32, 64, 128, 256};
+constexpr int kTileCols[] = {32, 128, 64, 128, 256};
 
 int64_t row_tiles(const RowsProduct& a, int side) {
   return ceil64(a.rows, side) + (a.groups.offsets ? a.groups.count + 1 : 0);
@@ -636,13 +647,19 @@ RowsTile rows_tile(const RowsProduct& a) {
   const int64_t stack = a.groups.offsets ? std::max(1, a.groups.count) : 1;
   const int64_t height = ceil64(a.rows, stack);   // rows of a typical group
   // up to 32 rows a taller tile only adds work on rows that are not there
-  if (height <= 32) return kRows32;
+  if (height <= 32) {
+    const double tiles_m = a.groups.offsets ? (double)a.rows / 32 + 0.5 * (double)stack : 1.0;
+    const double slabs = (double)ceil64(a.depth, kBK);
+    const double narrow = rounds(tiles_m * (double)ceil64(a.cols, 32), 256) * (4.5 + 0.7 * std::ceil(slabs / 8));
+    const double wide = rounds(tiles_m * (double)ceil64(a.cols, 128), 512) * (4.5 + 0.6 * std::ceil(slabs / 2));
+    return narrow <= wide ? kRows32 : kRows32x128;
+  }
   const bool heavy = a.act == kActGelu || a.act == kActSilu;
   const double slabs = (double)ceil64(a.depth, kBK);
   RowsTile best = kRows64;
   double least = 0;
   for (RowsTile t : {kRows64, kRows128, kRows256}) {
-    const int side = kRowsSide[t];
+    const int side = kTileRows[t];
     // a group's last tile is half full on average
     const double tiles_m = a.groups.offsets ? (double)a.rows / side + 0.5 * (double)stack
                                             : (double)ceil64(a.rows, side);
@@ -661,13 +678,14 @@ hipError_t rows_tiles(const RowsProduct& a, hipStream_t stream) {
   static std::atomic<uint64_t> configured{0};
   const int64_t tiles_m = row_tiles(a, BM), tiles_n = ceil64(a.cols, BN);
   return launch_lds(rows_tile_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured, tiles_m * tiles_n,
-                    C::kThreads, C::kLds, stream, a, (int)tiles_m, (int)tiles_n);
+                    C::kThreads, C::kLds, stream, a, (int)tiles_n);
 }
 
 template <typename T, bool QT>
 hipError_t rows_variant(const RowsProduct& a, hipStream_t stream) {
   switch (rows_tile(a)) {
     case kRows32: return rows_tiles<T, QT, 32, 32, 1, 1, 8, 2>(a, stream);
+    case kRows32x128: return rows_tiles<T, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return rows_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return rows_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
     default: return rows_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
@@ -714,7 +732,7 @@ hipError_t weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream
   static std::atomic<uint64_t> configured{0};
   const int64_t tiles_i = ceil64(a.pi, BM), tiles_j = ceil64(a.qj, BN);
   return launch_lds(weight_tile_kernel<T, BM, BN, WM, WN, OCC>, configured,
-                    tiles_i * tiles_j * splits * a.groups.count, C::kThreads, C::kLds, stream, a, ws,
+                    ceil64(tiles_i * tiles_j * splits, 8) * 8 * a.groups.count, C::kThreads, C::kLds, stream, a, ws,
                     splits, (int)tiles_i, (int)tiles_j);
 }
 
@@ -727,8 +745,8 @@ hipError_t weight_variant(const WeightProduct& a, float* ws, int splits, hipStre
 }  // namespace
 
 bool tiles_take_rows(const RowsProduct& a) {
-  const int side = kRowsSide[rows_tile(a)];
-  if (row_tiles(a, side) * ceil64(a.cols, side) > kMaxGrid) return false;
+  const RowsTile t = rows_tile(a);
+  if (row_tiles(a, kTileRows[t]) * ceil64(a.cols, kTileCols[t]) > kMaxGrid) return false;
   return a.depth > 0 && multiple8(a.depth) && multiple8(a.cols) && multiple8(a.lda) &&
          multiple8(a.ldout) && wide_aligned(a.a) && wide_aligned(a.b) && wide_aligned(a.out) &&
          (!a.aux || (multiple8(a.ldaux) && wide_aligned(a.aux))) &&
@@ -744,7 +762,7 @@ hipError_t launch_rows_tiles(const RowsProduct& a, hipStream_t stream) {
 
 bool tiles_take_weight(const WeightProduct& a) {
   const WeightPlan plan = weight_plan(a);
-  if (ceil64(a.pi, plan.side) * ceil64(a.qj, plan.side) * a.groups.count * plan.splits > kMaxGrid)
+  if (ceil64(a.pi, plan.side) * ceil64(a.qj, plan.side) * a.groups.count * plan.splits + 8 * a.groups.count > kMaxGrid)
     return false;
   return multiple8(a.pi) && multiple8(a.qj) && multiple8(a.ldp) && multiple8(a.ldq) &&
          wide_aligned(a.p) && wide_aligned(a.q) && wide_aligned(a.dw);
