@@ -12,8 +12,9 @@
 // Both passes are bound by memory: forward reads x and writes y, backward reads dy and x and
 // writes dx, one pass each.  A row lives in the registers of one wave (up to 2048 columns) or of
 // one workgroup of 256 lanes (up to 8192); longer rows are read again from memory for each step.
-// In the backward pass every wave takes rows at a stride and keeps its columns' sums of dy h and
-// dy in registers; a workgroup joins its waves' sums in LDS and leaves one partial row, and a second
+// A wave walks over rows with weight and bias in registers and the next row on its way while it
+// works on this one.  In the backward pass it also keeps its columns' sums of dy h and dy; the
+// workgroup (one to a CU) joins its waves' sums in LDS and leaves one partial row, and a second
 // launch adds the partial rows in a fixed order (no atomics: the same bits on every run).
 #include <algorithm>
 
@@ -27,16 +28,39 @@ namespace {
 
 constexpr int kVec = 8;   // consecutive columns of one lane
 
-// Eight consecutive columns of a row from column c on, as fp32; columns at or past `cols` are 0.
-// The pieces are read with one wide access each at whatever alignment the row starts.
+// Eight consecutive columns of a row as they lie in memory, read with wide accesses at whatever
+// alignment the row starts; columns at or past the width are 0.
+template <typename T>
+struct Raw {
+  T t[kVec];
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+    if (c + kVec <= cols) {
+      __builtin_memcpy(t, row + c, sizeof(t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) t[e] = c + e < cols ? row[c + e] : from_f32<T>(0.0f);
+    }
+  }
+  // The width is a multiple of kVec: all of the columns are there or none.
+  __device__ __forceinline__ void load_even(const T* row, int c, int cols) {
+    if (c < cols) {
+      __builtin_memcpy(t, row + c, sizeof(t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) t[e] = from_f32<T>(0.0f);
+    }
+  }
+  __device__ __forceinline__ void get(float v[kVec]) const {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = to_f32(t[e]);
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* row, int c, int cols, float v[kVec]) {
-  if (c + kVec <= cols) {
-    load_vec<T, kVec>(row + c, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = c + e < cols ? to_f32(row[c + e]) : 0.0f;
-  }
+  Raw<T> r;
+  r.load(row, c, cols);
+  r.get(v);
 }
 
 template <typename T>
@@ -103,35 +127,73 @@ struct NormParams {
   float* partial;      // backward: [blocks][2][cols] column sums, or null
 };
 
-// THREADS lanes hold a row, CHUNKS pieces of eight columns each; a workgroup is 256 lanes, so
-// 256 / THREADS rows at a time.
-template <typename T, int THREADS, int CHUNKS>
+// A row in pieces: THREADS lanes, CHUNKS pieces of eight columns each.  EVEN: the width is a multiple
+// of eight.
+template <typename T, int THREADS, int CHUNKS, bool EVEN>
+struct Row {
+  Raw<T> raw[CHUNKS];
+  __device__ static __forceinline__ int col(int k) {
+    return (k * THREADS + (int)threadIdx.x % THREADS) * kVec;
+  }
+  __device__ __forceinline__ void load(const void* base, int64_t at, int cols) {
+    const T* row = static_cast<const T*>(base) + at;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+      if (EVEN) raw[k].load_even(row, col(k), cols);
+      else raw[k].load(row, col(k), cols);
+    }
+  }
+};
+
+template <typename T, bool EVEN>
+__device__ __forceinline__ void store_row(T* row, int c, int cols, const float v[kVec]) {
+  if (EVEN) {
+    if (c < cols) store_vec<T, kVec>(row + c, v);
+  } else {
+    store8(row, c, cols, v);
+  }
+}
+
+// A workgroup is 256 lanes: 256 / THREADS rows at a time, the groups of rows gridDim.x apart.
+template <typename T, int THREADS, int CHUNKS, bool EVEN>
 __global__ __launch_bounds__(256) void norm_kernel(NormParams p) {
-  __shared__ float red[2][4];
+  __shared__ float red[4][4];
   constexpr int kRows = 256 / THREADS;
   const int t = threadIdx.x % THREADS;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / THREADS; row < p.rows;
-       row += (int64_t)gridDim.x * kRows) {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / THREADS;
+  typedef Row<T, THREADS, CHUNKS, EVEN> R;
+  R next;
+  if (row < p.rows) next.load(p.x, row * p.ldx, p.cols);
+  float w[CHUNKS][kVec], b[CHUNKS][kVec];
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    load_param<T>(p.w, p.param_f32, R::col(k), p.cols, 1.0f, w[k]);
+    load_param<T>(p.b, p.param_f32, R::col(k), p.cols, 0.0f, b[k]);
+  }
+  for (int turn = 0; row < p.rows; row += step, turn ^= 2) {
     float v[CHUNKS][kVec];
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k) {
-      load8(x, (k * THREADS + t) * kVec, p.cols, v[k]);
+      next.raw[k].get(v[k]);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) sum += v[k][e];
     }
-    const float mean = row_sum<THREADS>(sum, red[0]) / (float)p.cols;
+    if (row + step < p.rows) next.load(p.x, (row + step) * p.ldx, p.cols);
+    const float mean = row_sum<THREADS>(sum, red[turn]) / (float)p.cols;
     float sq = 0.0f;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k)
+    for (int k = 0; k < CHUNKS; ++k) {
+      const bool there = EVEN ? R::col(k) < p.cols : true;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const float d = v[k][e] - mean;
         v[k][e] = d;
-        if ((k * THREADS + t) * kVec + e < p.cols) sq = fmaf(d, d, sq);
+        if (EVEN ? there : R::col(k) + e < p.cols) sq = fmaf(d, d, sq);
       }
-    const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[1]) / (float)p.cols + p.eps);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[turn + 1]) / (float)p.cols + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
@@ -139,14 +201,10 @@ __global__ __launch_bounds__(256) void norm_kernel(NormParams p) {
     T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k) {
-      const int c = (k * THREADS + t) * kVec;
-      if (c >= p.cols) continue;
-      float w[kVec], b[kVec], o[kVec];
-      load_param<T>(p.w, p.param_f32, c, p.cols, 1.0f, w);
-      load_param<T>(p.b, p.param_f32, c, p.cols, 0.0f, b);
+      float o[kVec];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) o[e] = fmaf(v[k][e] * rstd, w[e], b[e]);
-      store8(y, c, p.cols, o);
+      for (int e = 0; e < kVec; ++e) o[e] = fmaf(v[k][e] * rstd, w[k][e], b[k][e]);
+      store_row<T, EVEN>(y, R::col(k), p.cols, o);
     }
   }
 }
@@ -193,49 +251,50 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormParams p) {
   }
 }
 
-// Backward pass.  Workgroup `blockIdx.x` takes row groups blockIdx.x, blockIdx.x + gridDim.x, ..
-// (kRows rows each) and leaves its column sums in its partial row.
-template <typename T, int THREADS, int CHUNKS>
-__global__ __launch_bounds__(256) void norm_grad_kernel(NormParams p) {
-  constexpr int kRows = 256 / THREADS;
-  // one wave's column sums at a time pass through LDS; row sums of 256-lane rows use `red`
-  __shared__ float red[4][4];
-  __shared__ float cs[kRows > 1 ? THREADS * CHUNKS * kVec : 1];
+// Backward pass in workgroups of LANES lanes, LANES / THREADS rows at a time; each workgroup leaves
+// its column sums in its partial row.
+template <typename T, int LANES, int THREADS, int CHUNKS, bool EVEN>
+__global__ __launch_bounds__(LANES) void norm_grad_kernel(NormParams p) {
+  constexpr int kRows = LANES / THREADS;
+  __shared__ float red[4][4];                              // rows of 256 lanes: their sums
+  __shared__ float cs[kRows > 1 ? kRows * THREADS * kVec : 1];   // the waves' column sums
   const int t = threadIdx.x % THREADS;
   const int sub = threadIdx.x / THREADS;
+  typedef Row<T, THREADS, CHUNKS, EVEN> R;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  R next_x, next_dy;
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto fetch = [&](int64_t r) {
+    next_x.load(p.x, r * p.ldx, p.cols);
+    next_dy.load(p.dy, r * p.lddy, p.cols);
+    next_mean = p.mean[r];
+    next_rstd = p.rstd[r];
+  };
+  if (row < p.rows) fetch(row);
   float w[CHUNKS][kVec], sw[CHUNKS][kVec], sb[CHUNKS][kVec];
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k) {
-    const int c = (k * THREADS + t) * kVec;
-    if (c < p.cols) {
-      load_param<T>(p.w, p.param_f32, c, p.cols, 1.0f, w[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) w[k][e] = 0.0f;
-    }
+    load_param<T>(p.w, p.param_f32, R::col(k), p.cols, 1.0f, w[k]);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sw[k][e] = sb[k][e] = 0.0f;
   }
   const float inv = 1.0f / (float)p.cols;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < p.rows;
-       row += (int64_t)gridDim.x * kRows, turn ^= 2) {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const float mean = p.mean[row], rstd = p.rstd[row];
+  for (int turn = 0; row < p.rows; row += step, turn ^= 2) {
+    const float mean = next_mean, rstd = next_rstd;
     float h[CHUNKS][kVec], g[CHUNKS][kVec];
-    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k) {
-      const int c = (k * THREADS + t) * kVec;
-      load8(x, c, p.cols, h[k]);
-      load8(dy, c, p.cols, g[k]);
+      next_x.raw[k].get(h[k]);
+      next_dy.raw[k].get(g[k]);
     }
+    if (row + step < p.rows) fetch(row + step);
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        // a column past the end has dy = 0 and w = 0: it adds nothing to any sum
+        // a column past the end has dy = 0: it adds nothing to any sum
         const float hv = (h[k][e] - mean) * rstd;
         const float d = g[k][e];
         sb[k][e] += d;
@@ -251,12 +310,10 @@ __global__ __launch_bounds__(256) void norm_grad_kernel(NormParams p) {
     T* dx = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k) {
-      const int c = (k * THREADS + t) * kVec;
-      if (c >= p.cols) continue;
       float o[kVec];
 #pragma unroll
       for (int e = 0; e < kVec; ++e) o[e] = rstd * (g[k][e] - s1 - h[k][e] * s2);
-      store8(dx, c, p.cols, o);
+      store_row<T, EVEN>(dx, R::col(k), p.cols, o);
     }
   }
   if (!p.partial) return;
@@ -264,42 +321,30 @@ __global__ __launch_bounds__(256) void norm_grad_kernel(NormParams p) {
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int k = 0; k < CHUNKS; ++k) {
-      const int c = (k * THREADS + t) * kVec;
-      store8(out, c, p.cols, sw[k]);
-      store8(out + p.cols, c, p.cols, sb[k]);
+      store8(out, R::col(k), p.cols, sw[k]);
+      store8(out + p.cols, R::col(k), p.cols, sb[k]);
     }
   } else {
-    // waves 1.. hand their sums to wave 0 one after the other (a fixed order)
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int s = 1; s < kRows; ++s) {
-        __syncthreads();
-        if (sub == s) {
+    // piece by piece: every wave lays its sums down, then each lane adds one or more columns over
+    // the waves in order
 #pragma unroll
-          for (int k = 0; k < CHUNKS; ++k)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-              cs[(k * kVec + e) * THREADS + t] = pass ? sb[k][e] : sw[k][e];
-        }
-        __syncthreads();
-        if (sub == 0) {
-#pragma unroll
-          for (int k = 0; k < CHUNKS; ++k)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              const float v = cs[(k * kVec + e) * THREADS + t];
-              if (pass) sb[k][e] += v; else sw[k][e] += v;
-            }
-        }
-      }
-    }
-    if (sub == 0) {
+    for (int pass = 0; pass < 2; ++pass)
 #pragma unroll
       for (int k = 0; k < CHUNKS; ++k) {
-        const int c = (k * THREADS + t) * kVec;
-        store8(out, c, p.cols, sw[k]);
-        store8(out + p.cols, c, p.cols, sb[k]);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          cs[(sub * kVec + e) * THREADS + t] = pass ? sb[k][e] : sw[k][e];
+        __syncthreads();
+        for (int j = threadIdx.x; j < THREADS * kVec; j += LANES) {
+          const int c = (k * THREADS + j / kVec) * kVec + j % kVec;
+          if (c >= p.cols) continue;
+          float s = 0.0f;
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) s += cs[(r * kVec + j % kVec) * THREADS + j / kVec];
+          out[pass * p.cols + c] = s;
+        }
       }
-    }
   }
 }
 
@@ -415,48 +460,73 @@ constexpr int64_t kMaxGrid = 1 << 22;
 
 int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups of the kernels whose waves walk over rows: enough to fill the chip with what its
+// registers hold (eight workgroups of 256 lanes a CU), each then takes further rows.
+constexpr int64_t kWalkers = 2048;
+
+template <typename T, bool EVEN>
+hipError_t launch_norm_rows(const NormParams& p, hipStream_t stream) {
+  const int c = p.cols;
+  const dim3 rows4((unsigned)std::min(ceil64(p.rows, 4), kWalkers));
+  const dim3 rows1((unsigned)std::min(p.rows, kWalkers));
+  if (c <= 512) norm_kernel<T, 64, 1, EVEN><<<rows4, 256, 0, stream>>>(p);
+  else if (c <= 1024) norm_kernel<T, 64, 2, EVEN><<<rows4, 256, 0, stream>>>(p);
+  else if (c <= 2048) norm_kernel<T, 64, 4, EVEN><<<rows4, 256, 0, stream>>>(p);
+  else if (c <= 4096) norm_kernel<T, 256, 2, EVEN><<<rows1, 256, 0, stream>>>(p);
+  else norm_kernel<T, 256, 4, EVEN><<<rows1, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T, bool EVEN>
+hipError_t launch_norm_grad_rows(const NormParams& p, int blocks, hipStream_t stream) {
+  const int c = p.cols;
+  const dim3 grid(blocks);
+  if (c <= 512) norm_grad_kernel<T, 1024, 64, 1, EVEN><<<grid, 1024, 0, stream>>>(p);
+  else if (c <= 1024) norm_grad_kernel<T, 512, 64, 2, EVEN><<<grid, 512, 0, stream>>>(p);
+  else if (c <= 2048) norm_grad_kernel<T, 256, 64, 4, EVEN><<<grid, 256, 0, stream>>>(p);
+  else if (c <= 4096) norm_grad_kernel<T, 256, 256, 2, EVEN><<<grid, 256, 0, stream>>>(p);
+  else norm_grad_kernel<T, 256, 256, 4, EVEN><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch_norm_t(const NormParams& p, hipStream_t stream) {
   const int c = p.cols;
   // a launch counts its work-items in 32 bits: past kMaxGrid workgroups each takes further rows
-  const dim3 rows4((unsigned)std::min(ceil64(p.rows, 4), kMaxGrid));
   const dim3 rows1((unsigned)std::min(p.rows, kMaxGrid));
-  if (c <= 512) norm_kernel<T, 64, 1><<<rows4, 256, 0, stream>>>(p);
-  else if (c <= 1024) norm_kernel<T, 64, 2><<<rows4, 256, 0, stream>>>(p);
-  else if (c <= 2048) norm_kernel<T, 64, 4><<<rows4, 256, 0, stream>>>(p);
-  else if (c <= 4096) norm_kernel<T, 256, 2><<<rows1, 256, 0, stream>>>(p);
-  else if (c <= 8192) norm_kernel<T, 256, 4><<<rows1, 256, 0, stream>>>(p);
-  else norm_long_kernel<T><<<rows1, 256, 0, stream>>>(p);
+  if (c <= 8192) {
+    const bool even = c % kVec == 0;
+    return even ? launch_norm_rows<T, true>(p, stream) : launch_norm_rows<T, false>(p, stream);
+  }
+  norm_long_kernel<T><<<rows1, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_norm_grad_t(const NormParams& p, int blocks, hipStream_t stream) {
   const int c = p.cols;
-  const dim3 grid(blocks);
-  if (c <= 512) norm_grad_kernel<T, 64, 1><<<grid, 256, 0, stream>>>(p);
-  else if (c <= 1024) norm_grad_kernel<T, 64, 2><<<grid, 256, 0, stream>>>(p);
-  else if (c <= 2048) norm_grad_kernel<T, 64, 4><<<grid, 256, 0, stream>>>(p);
-  else if (c <= 4096) norm_grad_kernel<T, 256, 2><<<grid, 256, 0, stream>>>(p);
-  else if (c <= 8192) norm_grad_kernel<T, 256, 4><<<grid, 256, 0, stream>>>(p);
-  else {
-    hipError_t e = hipSuccess;
-    if (p.rows > 0) {
-      norm_grad_long_kernel<T><<<dim3((unsigned)std::min(p.rows, kMaxGrid)), 256, 0, stream>>>(p);
-      e = hipGetLastError();
-    }
-    if (e != hipSuccess || !p.partial) return e;
-    norm_columns_kernel<T><<<dim3(blocks, (unsigned)ceil64(c, 512)), 256, 0, stream>>>(p);
+  if (c <= 8192) {
+    const bool even = c % kVec == 0;
+    return even ? launch_norm_grad_rows<T, true>(p, blocks, stream)
+                : launch_norm_grad_rows<T, false>(p, blocks, stream);
   }
+  hipError_t e = hipSuccess;
+  if (p.rows > 0) {
+    norm_grad_long_kernel<T><<<dim3((unsigned)std::min(p.rows, kMaxGrid)), 256, 0, stream>>>(p);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || !p.partial) return e;
+  norm_columns_kernel<T><<<dim3(blocks, (unsigned)ceil64(c, 512)), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int norm_grad_blocks(int64_t rows, int cols) {
-  // rows a workgroup holds at once; a row too long for registers has its own column workgroups
-  const int at_once = cols <= 2048 || cols > 8192 ? 4 : 1;
-  const int64_t most = cols <= 8192 ? 1024 : 64;
+  // rows a workgroup holds at once, and the workgroups that fill the chip (sixteen waves to a CU up
+  // to 1024 columns, then eight); a row too long for registers has its own column workgroups
+  const int at_once = cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 8192 ? 1 : 4;
+  const int64_t most = cols <= 512 ? 256 : cols <= 8192 ? 512 : 64;
   return (int)std::min(most, std::max<int64_t>(1, ceil64(rows, at_once)));
 }
 
