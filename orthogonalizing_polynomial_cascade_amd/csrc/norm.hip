@@ -253,8 +253,11 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormParams p) {
 
 // Backward pass in workgroups of LANES lanes, LANES / THREADS rows at a time; each workgroup leaves
 // its column sums in its partial row.
+// At least two waves a SIMD: with the 290 registers that the compiler takes for 2048 uneven columns
+// only one fits, and the 4099 x 1601 pass took 34 us instead of 24.
 template <typename T, int LANES, int THREADS, int CHUNKS, bool EVEN>
-__global__ __launch_bounds__(LANES) void norm_grad_kernel(NormParams p) {
+__global__ __launch_bounds__(LANES) __attribute__((amdgpu_waves_per_eu(2)))
+void norm_grad_kernel(NormParams p) {
   constexpr int kRows = LANES / THREADS;
   __shared__ float red[4][4];                              // rows of 256 lanes: their sums
   __shared__ float cs[kRows > 1 ? kRows * THREADS * kVec : 1];   // the waves' column sums
