@@ -125,25 +125,7 @@ __global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int tiles_
     for (int i = 0; i < 16; ++i) {
       const int64_t c = j0 + (wave & 1) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
       if (c >= p.cols) continue;
-      float z = acc[i];
-      if (group < 0) {
-        if (p.keep) static_cast<T*>(p.keep)[r * p.ldkeep + c] = from_f32<T>(0.0f);
-        static_cast<T*>(p.out)[r * p.ldout + c] = from_f32<T>(0.0f);
-        continue;
-      }
-      if (p.gradient) {
-        if (p.aux) z *= act_slope(p.act, to_f32(static_cast<const T*>(p.aux)[r * p.ldaux + c]));
-      } else {
-        if (p.bias) {
-          const int64_t bi = (int64_t)group * p.cols + c;
-          z += p.bias_f32 ? static_cast<const float*>(p.bias)[bi]
-                          : to_f32(static_cast<const T*>(p.bias)[bi]);
-        }
-        if (p.keep) static_cast<T*>(p.keep)[r * p.ldkeep + c] = from_f32<T>(z);
-        z = act_value(p.act, z);
-      }
-      if (p.add) z += to_f32(static_cast<const T*>(p.add)[r * p.ldadd + c]);
-      static_cast<T*>(p.out)[r * p.ldout + c] = from_f32<T>(z);
+      finish_element<T>(p, group, r, c, acc[i]);
     }
   }
 }

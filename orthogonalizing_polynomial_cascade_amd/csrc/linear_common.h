@@ -2,6 +2,7 @@
 // of rows.
 #pragma once
 
+#include "activation.h"
 #include "device_common.h"
 #include "launchers.h"
 #include "scalar_types.h"
@@ -100,34 +101,49 @@ __device__ __forceinline__ int scan_sum(int v, int lane) {
 // The rows in tiles of TILE, group by group; rows without an owner form two groups of their own,
 // before the first and after the last.  Segment s = 0 .. count + 1 spans bound(s) .. bound(s + 1):
 // bound(0) = 0, bound(s) = the running maximum of the offsets up to s - 1, bound(count + 2) = rows.
-// A wave looks at 64 segments at a time, one a lane.
+// Whole tiles come first, in the order of the rows; then the segments' last, partly filled ones
+// (more than half full, then the others), whose shorter work evens out the end of a launch.  A
+// wave looks at 64 segments at a time, one a lane; with more than 62 groups the tiles keep the
+// order of the rows.
 template <int TILE>
 struct RowTiles {
   const Groups& g;
   int rows, lane;
-  int lo, hi, upto;   // the lane's segment of the current chunk, tiles up to and with it
+  int lo, hi, upto;   // the lane's segment of the current chunk; tiles up to and with it (whole
+                      // ones where the partly filled ones come last)
   int start, done;    // bound at the next chunk's first segment, tiles before the next chunk
-  int total;          // tiles in all
+  int whole, total;   // whole tiles, all tiles
+  uint64_t large, small;   // segments whose last tile is more than half full, or less
 
-  __device__ __forceinline__ void chunk(int s0) {
+  __device__ __forceinline__ bool sorted() const { return g.count + 2 <= 64; }
+
+  __device__ __forceinline__ void chunk(int s0, bool round_up) {
     const int s = s0 + lane;
     int v = s <= g.count ? (int)raw_offset(g, s, rows) : rows;
     v = v > start ? v : start;
     hi = scan_max(v, lane);
     lo = __shfl_up(hi, 1);
     if (lane == 0) lo = start;
-    upto = done + scan_sum((int)(((unsigned)(hi - lo) + TILE - 1) / TILE), lane);
+    upto = done + scan_sum((int)(((unsigned)(hi - lo) + (round_up ? TILE - 1 : 0)) / TILE), lane);
     start = __shfl(hi, 63);
     done = __shfl(upto, 63);
   }
   __device__ __forceinline__ RowTiles(const Groups& g_, int64_t rows_)
-      : g(g_), rows((int)rows_), lane((int)(threadIdx.x & 63)), start(0), done(0) {
+      : g(g_), rows((int)rows_), lane((int)(threadIdx.x & 63)), start(0), done(0), large(0), small(0) {
     if (!g.offsets) {
-      total = (int)(((unsigned)rows + TILE - 1) / TILE);
-      return;
+      whole = rows / TILE;
+      total = whole + (rows % TILE ? 1 : 0);
+    } else if (sorted()) {
+      chunk(0, false);
+      const int rest = (hi - lo) % TILE;
+      large = __ballot(rest > TILE / 2);
+      small = __ballot(rest > 0 && rest <= TILE / 2);
+      whole = done;
+      total = done + __popcll(large) + __popcll(small);
+    } else {
+      for (int s0 = 0; s0 < g.count + 2; s0 += 64) chunk(s0, true);
+      whole = total = done;
     }
-    for (int s0 = 0; s0 < g.count + 2; s0 += 64) chunk(s0);
-    total = done;
   }
   // Tile t < total: its first row, the end of its group's rows, its group (-1: no owner).
   __device__ __forceinline__ void find(int t, int64_t* row0, int64_t* end, int* group) {
@@ -137,19 +153,34 @@ struct RowTiles {
       *group = 0;
       return;
     }
-    int s0 = 0;
-    if (g.count + 2 > 64) {   // several chunks: walk over them again
+    int s0 = 0, who;
+    bool tail = false;
+    if (sorted()) {
+      if (t < whole) {
+        who = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
+      } else {
+        tail = true;
+        int nth = t - whole;
+        uint64_t in = large;
+        if (nth >= __popcll(large)) {
+          nth -= __popcll(large);
+          in = small;
+        }
+        const uint64_t below = lane == 0 ? 0 : in << (64 - lane);
+        who = __ffsll((unsigned long long)__ballot((in >> lane & 1) && __popcll(below) == nth)) - 1;
+      }
+    } else {   // several chunks: walk over them again
       start = done = 0;
       for (;; s0 += 64) {
-        chunk(s0);
+        chunk(s0, true);
         if (t < done) break;
       }
+      who = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
     }
-    const int who = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-    const int left = __shfl(upto, who) - t;    // tiles from t to the segment's end
-    const int first = __shfl(lo, who), last = __shfl(hi, who);
-    const int tiles = (int)(((unsigned)(last - first) + TILE - 1) / TILE);
-    *row0 = first + (int64_t)(tiles - left) * TILE;
+    const int first = __shfl(lo, who), last = __shfl(hi, who), through = __shfl(upto, who);
+    const unsigned span = (unsigned)(last - first);
+    const int tiles = (int)((span + (sorted() ? 0 : TILE - 1)) / TILE);
+    *row0 = first + (int64_t)(tail ? tiles : tiles - (through - t)) * TILE;
     *end = last;
     const int seg = s0 + who;
     *group = seg == 0 || seg > g.count ? -1 : seg - 1;
@@ -176,6 +207,32 @@ __device__ __forceinline__ int longest_first(const Groups& g, int64_t rows, int 
     rank += other > size || (other == size && f < lane) ? 1 : 0;
   }
   return __ffsll((unsigned long long)__ballot(lane < g.count && rank == j)) - 1;
+}
+
+// Epilogue of one element: sum over the depth in, output (and kept preactivation) out.
+template <typename T>
+__device__ __forceinline__ void finish_element(const RowsProduct& p, int group, int64_t r, int64_t c,
+                                               float z) {
+  T* out = static_cast<T*>(p.out) + r * p.ldout + c;
+  T* keep = static_cast<T*>(p.keep) + r * p.ldkeep + c;
+  if (group < 0) {
+    if (p.keep) *keep = from_f32<T>(0.0f);
+    *out = from_f32<T>(0.0f);
+    return;
+  }
+  if (p.gradient) {
+    if (p.aux) z *= act_slope(p.act, to_f32(static_cast<const T*>(p.aux)[r * p.ldaux + c]));
+  } else {
+    if (p.bias) {
+      const int64_t at = (int64_t)group * p.cols + c;
+      z += p.bias_f32 ? static_cast<const float*>(p.bias)[at]
+                      : to_f32(static_cast<const T*>(p.bias)[at]);
+    }
+    if (p.keep) *keep = from_f32<T>(z);
+    z = act_value(p.act, z);
+  }
+  if (p.add) z += to_f32(static_cast<const T*>(p.add)[r * p.ldadd + c]);
+  *out = from_f32<T>(z);
 }
 
 // linear_tiles.hip: the tiled kernels, for widths and pitches that are multiples of 8 and pointers

@@ -252,6 +252,20 @@ struct Pipe {
     slab(kt & 1, no, no);
   }
 
+  // run() of a wave without multiplies: its share of the copies, and every barrier.
+  __device__ __forceinline__ void attend() {
+    if (KT == 0) return;
+    request(0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (KT > 1) request(1);
+    for (int kt = 0; kt + 1 < KT; ++kt) {
+      wait_vmcnt<0>();
+      __syncthreads();
+      if (kt + 2 < KT) request(kt & 1);
+    }
+  }
+
   // KS > 1: each set's sums go through its own buffers; the first set adds them in order.
   __device__ __forceinline__ void merge(int kg, f32x16_t (&acc)[C::kFM][C::kFN]) {
     if (KT == 0) return;
@@ -482,12 +496,21 @@ void rows_tile_kernel(RowsProduct p, int tiles_n) {
   char* smem = smem_all + kg * C::kRing;
 
   // The launch counts one row tile more for each group than there may be.  The tiles that do exist
-  // are dealt out evenly to the XCDs (counted with the others, the last XCD got the empty ones: 24
-  // groups of 32768 rows, 2816 columns of depth 768 took 252 us).
+  // are dealt out to the XCDs, an eighth of the whole ones to each and then an eighth of the partly
+  // filled ones.
   RowTiles<BM> rows(p.groups, p.rows);
-  if ((int)blockIdx.x >= rows.total * tiles_n) return;
-  int ti, tj;
-  banded(xcd_remap(blockIdx.x, rows.total * tiles_n), rows.total, tiles_n, &ti, &tj);
+  const int xcd = blockIdx.x % 8;
+  int at = blockIdx.x / 8, ti, tj;
+  const int whole = rows.whole * tiles_n, parts = (rows.total - rows.whole) * tiles_n;
+  const int mine = whole / 8 + (xcd < whole % 8 ? 1 : 0);
+  if (at < mine) {
+    banded(xcd * (whole / 8) + min(xcd, whole % 8) + at, rows.whole, tiles_n, &ti, &tj);
+  } else {
+    at = (at - mine) * 8 + (7 - xcd);   // the XCDs that have one whole tile less come first
+    if (at >= parts) return;
+    ti = rows.whole + at / tiles_n;
+    tj = at % tiles_n;
+  }
   int64_t row0, end;
   int group;
   rows.find(ti, &row0, &end, &group);
@@ -505,12 +528,15 @@ void rows_tile_kernel(RowsProduct p, int tiles_n) {
   Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
   pipe.begin(static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, b,
              QT ? p.cols : p.depth, p.cols - j0, group < 0 ? 0 : p.depth, kg);
-  pipe.template run<false>(acc, 0, none);
+  const int wm = wave / WN, wn = wave % WN;
+  const bool idle = row0 + wm * C::kWTM >= end;   // no row of the wave's block is there
+  if (idle) pipe.attend();
+  else pipe.template run<false>(acc, 0, none);
   if constexpr (KS > 1) {
     pipe.merge(kg, acc);
     if (kg > 0) return;
   }
-  const int wm = wave / WN, wn = wave % WN;
+  if (idle) return;
   rows_epilogue<T, C>(p, acc, pipe.spare() + wave * S::kBytes, row0 + wm * C::kWTM, end, group,
                       j0 + wn * C::kWTN + S::col(lane), lane);
 }
@@ -660,10 +686,17 @@ RowsTile rows_tile(const RowsProduct& a) {
   double least = 0;
   for (RowsTile t : {kRows64, kRows128, kRows256}) {
     const int side = kTileRows[t];
-    // a group's last tile is half full on average
-    const double tiles_m = a.groups.offsets ? (double)a.rows / side + 0.5 * (double)stack
-                                            : (double)ceil64(a.rows, side);
-    const double cost = tile_cost(side, tiles_m * (double)ceil64(a.cols, side), slabs, heavy);
+    double cost;
+    if (a.groups.offsets) {
+      // a group's last tile is half full on average, takes two thirds of a whole one's time and
+      // comes at the end, where it fills up what a round leaves over
+      const double tiles_m = (double)a.rows / side + 0.2 * (double)stack;
+      const double slots = side == 128 ? 512 : 256;
+      const double share = std::max(1.0, tiles_m * (double)ceil64(a.cols, side) / slots);
+      cost = share * tile_cost(side, slots, slabs, heavy);
+    } else {
+      cost = tile_cost(side, (double)(ceil64(a.rows, side) * ceil64(a.cols, side)), slabs, heavy);
+    }
     if (t == kRows64 || cost < least) {
       best = t;
       least = cost;
@@ -677,7 +710,9 @@ hipError_t rows_tiles(const RowsProduct& a, hipStream_t stream) {
   using C = Tile<BM, BN, WM, WN, KS>;
   static std::atomic<uint64_t> configured{0};
   const int64_t tiles_m = row_tiles(a, BM), tiles_n = ceil64(a.cols, BN);
-  return launch_lds(rows_tile_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured, tiles_m * tiles_n,
+  // every XCD gets the same number of workgroups, whatever its share of partly filled tiles
+  return launch_lds(rows_tile_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured,
+                    ceil64(tiles_m * tiles_n, 8) * 8 + 8,
                     C::kThreads, C::kLds, stream, a, (int)tiles_n);
 }
 
@@ -746,7 +781,7 @@ hipError_t weight_variant(const WeightProduct& a, float* ws, int splits, hipStre
 
 bool tiles_take_rows(const RowsProduct& a) {
   const RowsTile t = rows_tile(a);
-  if (row_tiles(a, kTileRows[t]) * ceil64(a.cols, kTileCols[t]) > kMaxGrid) return false;
+  if (row_tiles(a, kTileRows[t]) * ceil64(a.cols, kTileCols[t]) + 16 > kMaxGrid) return false;
   return a.depth > 0 && multiple8(a.depth) && multiple8(a.cols) && multiple8(a.lda) &&
          multiple8(a.ldout) && wide_aligned(a.a) && wide_aligned(a.b) && wide_aligned(a.out) &&
          (!a.aux || (multiple8(a.ldaux) && wide_aligned(a.aux))) &&

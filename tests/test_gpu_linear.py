@@ -87,6 +87,19 @@ def test_linear_shapes(gpu_lib, rows, n, k, w_kn, kind):
     _check_backward(gpu_lib, dz, x, w, _mat(rows, k, t, seed + 5), add, act, w_kn, t)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("n,k", [(768, 2816), (2816, 768), (4104, 200), (37, 1001), (5, 7), (4099, 513), (8, 4096)])
+@pytest.mark.parametrize("w_kn", [False, True])
+def test_linear_few_rows(gpu_lib, rows, n, k, w_kn):
+    """Single tokens and a few: depths of less and more than a pass, ragged columns."""
+    t = torch.float16 if n == 2816 else torch.bfloat16
+    x = _mat(rows, k, t, 1, pitch=k + 3 if rows % 2 else k)
+    w = _stack(1, n, k, t, 2, w_kn)[0]
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(3)).cuda()
+    _check_forward(gpu_lib, x, w, bias, _mat(rows, n, t, 4), "silu", w_kn, True, t)
+    _check_backward(gpu_lib, _mat(rows, n, t, 5, 0.1), x, w, _mat(rows, k, t, 6), _mat(rows, k, t, 7), "gelu", w_kn, t)
+
+
 # enough tiles for the larger tile shapes, with ragged last rows, columns and depths
 @pytest.mark.parametrize("rows,n,k", [(2100, 2000, 72), (5000, 2600, 136), (4100, 3336, 64), (700, 1288, 1032)])
 @pytest.mark.parametrize("w_kn", [False, True])
@@ -303,6 +316,16 @@ def test_expert_groups(gpu_lib, groups, w_kn, n, k):
 def test_expert_large_groups(gpu_lib, w_kn):
     """Groups longer than a tile and a split, one of them most of the rows, one empty."""
     _expert_case(gpu_lib, 6000, [0, 4096, 4100, 4100, 5999], 264, 520, w_kn, torch.bfloat16, "relu2", False)
+
+
+@pytest.mark.parametrize("experts", [2, 31, 61, 62, 63, 64, 65, 126, 127, 130])
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_expert_counts(gpu_lib, experts, rows):
+    """Group counts around one wave's 64 lanes, uneven groups, rows before and after them, and row
+    counts that give few-row tiles and full ones."""
+    g = torch.Generator().manual_seed(experts)
+    cuts = torch.sort(torch.randint(1, rows - 2, (experts + 1,), generator=g))[0].tolist()
+    _expert_case(gpu_lib, rows, cuts, 72, 136, experts % 2 == 0, torch.bfloat16, "silu", experts % 3 == 0)
 
 
 @pytest.mark.parametrize("w_kn", [False, True])
