@@ -26,60 +26,113 @@ namespace {
 constexpr int64_t kMaxGrid = 1 << 22;   // a launch counts its work-items in 32 bits
 
 // ---------------------------------------------------------------------------------------------
-// The kernels for any width, pitch and alignment: 64x64 tiles, four waves of one 32x32 fragment,
-// operands through registers into LDS.
+// The kernels for any width, pitch and alignment: tiles of SIDE x SIDE (64, or 128 where there are
+// enough of them), four waves of F x F 32x32 fragments, operands through registers into LDS.  Two
+// barriers a slab and, for K-major operands, two-byte LDS writes: bound by those, at about a fifth
+// of the aligned kernels' rate (see linear_tiles.hip, whose copies need 16-byte alignment).
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kAnyTile = 64;
-constexpr int kAnyDepth = 32;
+constexpr int kAnyDepth = 64;
 constexpr int kAnyPitch = kAnyDepth + 8;   // elements per LDS row: 16-byte slots, spread banks
 
-// One operand of the tile: 64 rows by 32 k, eight elements of one lane.  K-contiguous: element
-// (i, k) at base[i * ld + k]; K-major: at base[k * ld + i].
-template <typename T, bool KMAJOR>
+// One operand of the tile: SIDE rows by 64 k, SIDE / 32 pieces of eight elements a lane.
+// K-contiguous: element (i, k) at base[i * ld + k], eight lanes to a row; K-major: at
+// base[k * ld + i], four lanes to a k-row's 64 bytes and 16 k-rows to a wave, so that the two-byte
+// writes of a wave fall on different banks.
+template <typename T, bool KMAJOR, int SIDE>
 struct AnySlab {
-  T v[8];
+  static constexpr int kPieces = SIDE / 32;
+  uint32_t v[kPieces][4];   // two elements each
+  // Strided and contiguous index of the lane's piece i within the slab.
+  __device__ static __forceinline__ int major(int i) {
+    const int at = (int)threadIdx.x + i * 256;
+    return KMAJOR ? (at >> 2) % kAnyDepth : at / 8;
+  }
+  __device__ static __forceinline__ int minor(int i) {
+    const int at = (int)threadIdx.x + i * 256;
+    return (KMAJOR ? (at & 3) + 4 * ((at >> 2) / kAnyDepth) : at % 8) * 8;
+  }
+  // The piece of `there` >= 1 elements at p, which lies in a row of `row` elements that ends with it
+  // where there < 8: read as the row's last eight elements and moved down (or one by one in a row
+  // of fewer than eight).
+  __device__ static __forceinline__ void edge(const T* p, int there, int64_t row, uint32_t w[4]) {
+    if (row >= 8) {
+      const int back = there < 8 ? 8 - there : 0;
+      uint32_t u[5] = {0, 0, 0, 0, 0};
+      __builtin_memcpy(u, p - back, 16);
+#pragma unroll
+      for (int s = 2; s >= 1; --s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t from = i + s < 4 ? u[i + s] : 0u;
+          u[i] = (back >> s) & 1 ? from : u[i];   // back = 4 b2 + 2 b1 + b0: two words, one word
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t moved = (u[i] >> 16) | (u[i + 1] << 16);
+        w[i] = back & 1 ? moved : u[i];
+      }
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < there; ++e) {
+        const uint32_t x = (uint32_t)__builtin_bit_cast(uint16_t, p[e]) << (16 * (e & 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] |= e / 2 == i ? x : 0u;
+      }
+    }
+  }
   __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t i0, int64_t ni,
                                        int64_t k0, int64_t nk) {
-    const int t = threadIdx.x;
-    const int64_t major = KMAJOR ? k0 + t / 8 : i0 + t / 4;           // the strided index
-    const int64_t minor = KMAJOR ? i0 + (t % 8) * 8 : k0 + (t % 4) * 8;
-    const int64_t nmaj = KMAJOR ? nk : ni, nmin = KMAJOR ? ni : nk;
-    const T* p = base + major * ld + minor;
-    if (major < nmaj && minor + 8 <= nmin) {
-      __builtin_memcpy(v, p, sizeof(v));
-    } else {
+    const T* at = base + (KMAJOR ? k0 : i0) * ld + (KMAJOR ? i0 : k0);
+    if (i0 + SIDE <= ni && k0 + kAnyDepth <= nk) {   // no edge in the slab: loads back to back
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = major < nmaj && minor + e < nmin ? p[e] : from_f32<T>(0.0f);
+      for (int i = 0; i < kPieces; ++i)
+        __builtin_memcpy(v[i], at + major(i) * ld + minor(i), 16);
+      return;
+    }
+    const int64_t nmaj = KMAJOR ? nk - k0 : ni - i0, nmin = KMAJOR ? ni - i0 : nk - k0;
+    const int64_t row = KMAJOR ? ni : nk;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      const int there = (int)(nmin - minor(i) < 8 ? nmin - minor(i) : 8);
+      if (major(i) < nmaj && there > 0) edge(at + major(i) * ld + minor(i), there, row, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[i][q] = w[q];
     }
   }
   __device__ __forceinline__ void store(T (*lds)[kAnyPitch]) const {
-    const int t = threadIdx.x;
-    if constexpr (KMAJOR) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) lds[(t % 8) * 8 + e][t / 8] = v[e];
-    } else {
-      __builtin_memcpy(&lds[t / 4][(t % 4) * 8], v, sizeof(v));
+    for (int i = 0; i < kPieces; ++i) {
+      if constexpr (KMAJOR) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          lds[minor(i) + e][major(i)] =
+              __builtin_bit_cast(T, (uint16_t)(v[i][e / 2] >> (16 * (e & 1))));
+      } else {
+        __builtin_memcpy(&lds[major(i)][minor(i)], v[i], 16);
+      }
     }
   }
 };
 
-// acc (one fragment per wave, C transposed: register r of lane l is row l%32, column
-// 8(r/4) + 4(l/32) + r%4) of the tile's k range [k0, k1).  With `sum`, the wave also adds up its
-// P (sum_p) or Q fragment over k into `sums` (see row_sum_selector).
-template <typename T, bool PT, bool QT>
+// acc (the wave's fragments, C transposed: register r of lane l is row l%32, column
+// 8(r/4) + 4(l/32) + r%4 of a fragment) of the tile's k range [k0, k1).  `sum`: 1 the wave also adds
+// up its P fragments over k into `sums`, 2 its Q fragments (see row_sum_selector).
+template <typename T, bool PT, bool QT, int SIDE>
 __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t i0, int64_t ni,
                                                const T* Q, int64_t ldq, int64_t j0, int64_t nj,
-                                               int64_t k0, int64_t k1, f32x16_t& acc, bool sum,
-                                               bool sum_p, f32x4_t& sums) {
-  __shared__ __attribute__((aligned(16))) T lp[kAnyTile][kAnyPitch];
-  __shared__ __attribute__((aligned(16))) T lq[kAnyTile][kAnyPitch];
+                                               int64_t k0, int64_t k1,
+                                               f32x16_t (&acc)[SIDE / 64][SIDE / 64], int sum,
+                                               f32x4_t (&sums)[SIDE / 64]) {
+  __shared__ __attribute__((aligned(16))) T lp[SIDE][kAnyPitch];
+  __shared__ __attribute__((aligned(16))) T lq[SIDE][kAnyPitch];
   typedef typename Mfma<T>::vec vec;
+  constexpr int F = SIDE / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const vec one = row_sum_selector<T>(lane);
-  AnySlab<T, PT> sp;
-  AnySlab<T, QT> sq;
+  AnySlab<T, PT, SIDE> sp;
+  AnySlab<T, QT, SIDE> sq;
   if (k0 < k1) {
     sp.load(P, ldp, i0, ni, k0, k1);
     sq.load(Q, ldq, j0, nj, k0, k1);
@@ -96,36 +149,55 @@ __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t 
 #pragma unroll
     for (int ks = 0; ks < kAnyDepth / 16; ++ks) {
       const int kk = ks * 16 + 8 * (lane >> 5);
-      const vec fp = *reinterpret_cast<const vec*>(&lp[(wave >> 1) * 32 + (lane & 31)][kk]);
-      const vec fq = *reinterpret_cast<const vec*>(&lq[(wave & 1) * 32 + (lane & 31)][kk]);
-      acc = Mfma<T>::run(fq, fp, acc);
-      if (sum) sums = Mfma<T>::run16(one, sum_p ? fp : fq, sums);
+      vec fp[F], fq[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        fp[f] = *reinterpret_cast<const vec*>(&lp[((wave >> 1) * F + f) * 32 + (lane & 31)][kk]);
+        fq[f] = *reinterpret_cast<const vec*>(&lq[((wave & 1) * F + f) * 32 + (lane & 31)][kk]);
+      }
+#pragma unroll
+      for (int m = 0; m < F; ++m)
+#pragma unroll
+        for (int n = 0; n < F; ++n) acc[m][n] = Mfma<T>::run(fq[n], fp[m], acc[m][n]);
+      if (sum) {
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          sums[f] = Mfma<T>::run16(one, sum == 1 ? fp[f] : fq[f], sums[f]);
+      }
     }
   }
 }
 
-template <typename T, bool QT>
-__global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int tiles_n) {
+template <typename T, bool QT, int SIDE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void any_rows_kernel(RowsProduct p, int tiles_n) {
+  constexpr int F = SIDE / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  RowTiles<kAnyTile> tiles(p.groups, p.rows);
+  RowTiles<SIDE> tiles(p.groups, p.rows);
   for (int64_t tile = blockIdx.x; tile < (int64_t)tiles.total * tiles_n; tile += gridDim.x) {
     int64_t row0, end;
     int group;
     tiles.find((int)(tile / tiles_n), &row0, &end, &group);
-    const int64_t j0 = (tile % tiles_n) * kAnyTile;
+    const int64_t j0 = (tile % tiles_n) * SIDE;
     const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
-    f32x16_t acc = {};
-    f32x4_t none = {};
-    any_accumulate<T, false, QT>(static_cast<const T*>(p.a), p.lda, row0, end, b,
-                                 QT ? p.cols : p.depth, j0, p.cols, 0, group < 0 ? 0 : p.depth,
-                                 acc, false, false, none);
-    const int64_t r = row0 + (wave >> 1) * 32 + (lane & 31);
-    if (r >= end) continue;
+    f32x16_t acc[F][F] = {};
+    f32x4_t none[F] = {};
+    any_accumulate<T, false, QT, SIDE>(static_cast<const T*>(p.a), p.lda, row0, end, b,
+                                       QT ? p.cols : p.depth, j0, p.cols, 0,
+                                       group < 0 ? 0 : p.depth, acc, 0, none);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t c = j0 + (wave & 1) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
-      if (c >= p.cols) continue;
-      finish_element<T>(p, group, r, c, acc[i]);
+    for (int m = 0; m < F; ++m) {
+      const int64_t r = row0 + ((wave >> 1) * F + m) * 32 + (lane & 31);
+      if (r >= end) continue;
+#pragma unroll
+      for (int n = 0; n < F; ++n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int64_t c =
+              j0 + ((wave & 1) * F + n) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+          if (c < p.cols) finish_element<T>(p, group, r, c, acc[m][n][i]);
+        }
+      }
     }
   }
 }
@@ -133,9 +205,10 @@ __global__ __launch_bounds__(256) void any_rows_kernel(RowsProduct p, int tiles_
 // Weight product, tile by tile of [groups][splits][tiles]: split s of a group takes the s-th part
 // of its rows (a multiple of kAnyDepth).  With one split the tile goes to dw and db; with more, as
 // fp32 to plane s of the workspace, [splits][groups * pi * qj] and then [splits][groups * width].
-template <typename T>
-__global__ __launch_bounds__(256) void any_weight_kernel(WeightProduct p, float* ws, int splits,
-                                                         int tiles_i, int tiles_j) {
+template <typename T, int SIDE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void any_weight_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int tiles_j) {
+  constexpr int F = SIDE / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t tiles = (int64_t)tiles_i * tiles_j;
   const int groups = p.groups.count;
@@ -145,36 +218,47 @@ __global__ __launch_bounds__(256) void any_weight_kernel(WeightProduct p, float*
     const int64_t t = w % tiles;
     const int s = (int)(w / tiles % splits);
     const int e = (int)(w / tiles / splits);
-    const int64_t i0 = t / tiles_j * kAnyTile, j0 = t % tiles_j * kAnyTile;
+    const int64_t i0 = t / tiles_j * SIDE, j0 = t % tiles_j * SIDE;
     int64_t begin, end;
     group_rows(p.groups, p.rows, e, &begin, &end);
     const int64_t part =
         ((end - begin + splits - 1) / splits + kAnyDepth - 1) / kAnyDepth * kAnyDepth;
     const int64_t k0 = std::min(begin + s * part, end), k1 = std::min(k0 + part, end);
-    const bool sum = p.db && (p.dz_is_q ? i0 == 0 && wave < 2 : j0 == 0 && (wave & 1) == 0);
-    f32x16_t acc = {};
-    f32x4_t sums = {};
-    any_accumulate<T, true, true>(static_cast<const T*>(p.p), p.ldp, i0, p.pi,
-                                  static_cast<const T*>(p.q), p.ldq, j0, p.qj, k0, k1, acc, sum,
-                                  !p.dz_is_q, sums);
+    const int sum = !p.db ? 0
+                    : p.dz_is_q ? (i0 == 0 && wave < 2 ? 2 : 0)
+                                : (j0 == 0 && (wave & 1) == 0 ? 1 : 0);
+    f32x16_t acc[F][F] = {};
+    f32x4_t sums[F] = {};
+    any_accumulate<T, true, true, SIDE>(static_cast<const T*>(p.p), p.ldp, i0, p.pi,
+                                        static_cast<const T*>(p.q), p.ldq, j0, p.qj, k0, k1, acc,
+                                        sum, sums);
     if (sum && lane < 16) {
-      const int64_t c = p.dz_is_q ? j0 + (wave & 1) * 32 + lane : i0 + (wave >> 1) * 32 + lane;
-      if (c < width) {
-        float* db = splits > 1 ? ws + splits * plane + (int64_t)s * groups * width : p.db;
-        db[(int64_t)e * width + c] = sums[0];
-        if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[1];
+      float* db = splits > 1 ? ws + splits * plane + (int64_t)s * groups * width : p.db;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int64_t c = (p.dz_is_q ? j0 + ((wave & 1) * F + f) * 32
+                                     : i0 + ((wave >> 1) * F + f) * 32) + lane;
+        if (c < width) db[(int64_t)e * width + c] = sums[f][0];
+        if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[f][1];
       }
     }
-    const int64_t i = i0 + (wave >> 1) * 32 + (lane & 31);
-    if (i >= p.pi) continue;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int64_t j = j0 + (wave & 1) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-      if (j >= p.qj) continue;
-      const int64_t at = ((int64_t)e * p.pi + i) * p.qj + j;
-      if (splits > 1) ws[s * plane + at] = acc[r];
-      else if (p.dw_f32) static_cast<float*>(p.dw)[at] = acc[r];
-      else static_cast<T*>(p.dw)[at] = from_f32<T>(acc[r]);
+    for (int m = 0; m < F; ++m) {
+      const int64_t i = i0 + ((wave >> 1) * F + m) * 32 + (lane & 31);
+      if (i >= p.pi) continue;
+#pragma unroll
+      for (int n = 0; n < F; ++n) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t j =
+              j0 + ((wave & 1) * F + n) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+          if (j >= p.qj) continue;
+          const int64_t at = ((int64_t)e * p.pi + i) * p.qj + j;
+          if (splits > 1) ws[s * plane + at] = acc[m][n][r];
+          else if (p.dw_f32) static_cast<float*>(p.dw)[at] = acc[m][n][r];
+          else static_cast<T*>(p.dw)[at] = from_f32<T>(acc[m][n][r]);
+        }
+      }
     }
   }
 }
@@ -215,39 +299,64 @@ __global__ __launch_bounds__(256) void join_kernel(const float* ws, int splits, 
 int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, kMaxGrid)); }
 
-template <typename T>
-hipError_t launch_rows_t(const RowsProduct& a, hipStream_t stream) {
-  const int64_t tiles_m = ceil64(a.rows, kAnyTile) + (a.groups.offsets ? a.groups.count + 1 : 0);
-  const int tiles_n = (int)ceil64(a.cols, kAnyTile);
+// 128x128 tiles once they give every CU one.
+constexpr int64_t kManyTiles = 256;
+
+template <typename T, int SIDE>
+hipError_t launch_rows_side(const RowsProduct& a, hipStream_t stream) {
+  const int64_t tiles_m = ceil64(a.rows, SIDE) + (a.groups.offsets ? a.groups.count + 1 : 0);
+  const int tiles_n = (int)ceil64(a.cols, SIDE);
   if (a.b_kmajor)
-    any_rows_kernel<T, true><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
+    any_rows_kernel<T, true, SIDE><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
   else
-    any_rows_kernel<T, false><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
+    any_rows_kernel<T, false, SIDE><<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
   return hipGetLastError();
 }
 
-// Splits of each group's rows: enough workgroups for two rounds of four a CU while a split keeps
-// at least 512 rows on average.
-int weight_splits(const WeightProduct& a) {
-  const int64_t tiles = ceil64(a.pi, kAnyTile) * ceil64(a.qj, kAnyTile) * a.groups.count;
-  const int64_t want = std::max<int64_t>(1, 2048 / tiles);
+template <typename T>
+hipError_t launch_rows_t(const RowsProduct& a, hipStream_t stream) {
+  const int64_t stack = a.groups.offsets ? std::max(1, a.groups.count) : 1;
+  const int64_t height = ceil64(a.rows, stack);
+  return height > 64 && stack * ceil64(height, 128) * ceil64(a.cols, 128) >= kManyTiles
+             ? launch_rows_side<T, 128>(a, stream)
+             : launch_rows_side<T, 64>(a, stream);
+}
+
+struct AnyPlan {
+  int side, splits;
+};
+
+// Splits of each group's rows: enough workgroups for two rounds of two (128x128) or four (64x64) a
+// CU while a split keeps at least 512 rows on average.
+AnyPlan any_weight_plan(const WeightProduct& a) {
   const int64_t most = std::max<int64_t>(1, a.rows / a.groups.count / 512);
-  return (int)std::min<int64_t>(std::min(want, most), 64);
+  auto splits = [&](int side, int64_t slots) {
+    const int64_t tiles = ceil64(a.pi, side) * ceil64(a.qj, side) * a.groups.count;
+    return std::min({std::max<int64_t>(1, slots / tiles), most, int64_t(64)});
+  };
+  const int64_t wide = splits(128, 1024);
+  if (wide * ceil64(a.pi, 128) * ceil64(a.qj, 128) * a.groups.count >= kManyTiles)
+    return {128, (int)wide};
+  return {64, (int)splits(64, 2048)};
+}
+
+template <typename T, int SIDE>
+hipError_t launch_weight_side(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
+  const int tiles_i = (int)ceil64(a.pi, SIDE), tiles_j = (int)ceil64(a.qj, SIDE);
+  const int64_t work = (int64_t)tiles_i * tiles_j * splits * a.groups.count;
+  any_weight_kernel<T, SIDE><<<grid_for(work), 256, 0, stream>>>(a, ws, splits, tiles_i, tiles_j);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_weight_t(const WeightProduct& a, float* ws, hipStream_t stream) {
   const bool tiled = tiles_take_weight(a);
-  const int splits = tiled ? weight_tile_splits(a) : weight_splits(a);
+  const AnyPlan plan = any_weight_plan(a);
+  const int splits = tiled ? weight_tile_splits(a) : plan.splits;
   hipError_t e;
-  if (tiled) {
-    e = launch_weight_tiles(a, ws, splits, stream);
-  } else {
-    const int tiles_i = (int)ceil64(a.pi, kAnyTile), tiles_j = (int)ceil64(a.qj, kAnyTile);
-    const int64_t work = (int64_t)tiles_i * tiles_j * splits * a.groups.count;
-    any_weight_kernel<T><<<grid_for(work), 256, 0, stream>>>(a, ws, splits, tiles_i, tiles_j);
-    e = hipGetLastError();
-  }
+  if (tiled) e = launch_weight_tiles(a, ws, splits, stream);
+  else if (plan.side == 128) e = launch_weight_side<T, 128>(a, ws, splits, stream);
+  else e = launch_weight_side<T, 64>(a, ws, splits, stream);
   if (e != hipSuccess || splits == 1) return e;
   const int64_t n = (int64_t)a.groups.count * a.pi * a.qj;
   const int64_t nb = a.db ? (int64_t)a.groups.count * (a.dz_is_q ? a.qj : a.pi) : 0;
@@ -292,7 +401,7 @@ hipError_t launch_rows_product(const RowsProduct& a, hipStream_t stream) {
 
 // The larger of what the two kinds of kernels need: which of them runs depends on alignment too.
 size_t weight_product_words(const WeightProduct& a) {
-  int splits = weight_splits(a);
+  int splits = any_weight_plan(a).splits;
   if (a.pi % 8 == 0 && a.qj % 8 == 0) splits = std::max(splits, weight_tile_splits(a));
   if (splits == 1) return 0;
   return (size_t)splits * a.groups.count *

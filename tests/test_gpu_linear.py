@@ -118,6 +118,24 @@ def test_linear_large_tiles(gpu_lib, rows, n, k, w_kn, kind):
     H.assert_within(dx, want, err + H.half_step(want, t), "dx")
 
 
+# widths that are no multiples of eight, with tiles for every CU and without
+@pytest.mark.parametrize("rows,n,k", [(2100, 2003, 77), (4400, 1027, 130), (1500, 1285, 1601), (9000, 131, 203)])
+@pytest.mark.parametrize("w_kn", [False, True])
+def test_linear_large_odd(gpu_lib, rows, n, k, w_kn):
+    t = torch.bfloat16
+    x, dz = _mat(rows, k, t, 1), _mat(rows, n, t, 4, 0.1)
+    w = _stack(1, n, k, t, 2, w_kn)[0]
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(3)).cuda()
+    _check_forward(gpu_lib, x, w, bias, _mat(rows, n, t, 5), "gelu", w_kn, True, t)
+    _check_backward(gpu_lib, dz, x, w, _mat(rows, k, t, 6), None, "relu2", w_kn, t)
+
+
+@pytest.mark.parametrize("w_kn", [False, True])
+def test_expert_large_odd(gpu_lib, w_kn):
+    _expert_case(gpu_lib, 4900, [0, 700, 700, 1399, 1800, 2900, 3333, 4000, 4890], 1031, 131, w_kn, torch.bfloat16,
+                 "silu", True)
+
+
 @pytest.mark.parametrize("act", H.ACTS)
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("rows", [3, 300])
