@@ -57,8 +57,8 @@ extern "C" {
 enum anvil_status {
   ANVIL_OK = 0,
   ANVIL_ERR_INVALID_ARG = 1, /* NULL pointer for a non-empty call, negative size, bad flag */
-  ANVIL_ERR_UNSUPPORTED = 2, /* shape outside the supported set, or workspace too small */
-  ANVIL_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
+  ANVIL_ERR_UNSUPPORTED = 2, /* shape or type outside the supported set, or workspace too small */
+  ANVIL_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned (training operators: element) */
   ANVIL_ERR_ALIAS = 4,       /* an output overlaps an input it may not overlap */
   ANVIL_ERR_OOM = 5,         /* the workspace allocation failed */
   ANVIL_ERR_HIP = 6,         /* a HIP API or launch error; see anvil_last_hip_error() */

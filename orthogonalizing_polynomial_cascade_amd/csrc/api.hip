@@ -333,8 +333,10 @@ const char* anvil_status_string(int status) {
     case ANVIL_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size or bad flag)";
     case ANVIL_ERR_UNSUPPORTED:
       return "unsupported shape (m and n must be multiples of 8, m*n <= 2^30, g <= 65535, "
-             "g*m*n <= 2^35) or workspace too small";
-    case ANVIL_ERR_MISALIGNED: return "pointer not 16-byte aligned (workspace: 256-byte)";
+             "g*m*n <= 2^35; training operators: rows < 2^31, widths and pitches <= 2^22, pitch at "
+             "least the width, 16-bit types in the linear layers) or workspace too small";
+    case ANVIL_ERR_MISALIGNED:
+      return "pointer not 16-byte aligned (workspace: 256-byte; training operators: to the element)";
     case ANVIL_ERR_ALIAS: return "an output overlaps an input";
     case ANVIL_ERR_OOM: return "workspace allocation failed";
     case ANVIL_ERR_HIP: return "HIP runtime or launch error (see anvil_last_hip_error)";
@@ -350,7 +352,7 @@ const char* anvil_status_string(int status) {
 
 int anvil_last_hip_error(void) { return t_last_hip; }
 
-int anvil_version(void) { return 100; }
+int anvil_version(void) { return 200; }
 
 size_t anvil_workspace_bytes(int64_t g, int64_t m, int64_t n) {
   Shape sh;

@@ -14,6 +14,13 @@
 //  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row.
 //    The rows leave through LDS (the buffer that is free by then), eight columns a lane, whole lines
 //    an access, with bias, activation, derivative and residual applied on the way.
+//  * What bounds it: the multiplies need 62% of the cycles at 8192^3 (1250 TFLOP/s with w [n, k],
+//    1340 with w [k, n], 1150 in the weight gradient; the barrier and the waits ahead of it take
+//    most of the rest), LDS is busy for a quarter of them and free of bank conflicts.  A slab of
+//    64 k keeps the K-contiguous copies at whole 128-byte lines (rings of four 32-deep slabs were 8%
+//    slower), and 256x256 tiles read 7.8 bytes a thousand operations where 128x128 ones read
+//    15.6 (8192^3: 1080 TFLOP/s).  Copies placed between the multiplies of a slab's last k-step, all
+//    without branches, gave 3-7% over copies ahead of them.
 //  * KS > 1: KS sets of waves share a tile, each with its own part of the depth and its own buffers,
 //    and the first set adds the others' sums in order: for calls with fewer tiles than CUs.
 #include <algorithm>
@@ -323,7 +330,7 @@ __device__ __forceinline__ u32x4_t pack8(const float v[8]) {
 // of one row) go to LDS as fp32 and come back with eight consecutive columns a lane, lanes
 // side by side along the rows, so that every access to memory is whole 128-byte lines.  (Stored
 // from the accumulators' layout, 32 bytes of 32 rows an instruction, the lines left L2 half
-// written: 392 us against 232 for the 32768 x 2816 product of depth 768 with two outputs.)  Slots
+// written: 392 us against 273 for the 32768 x 2816 product of depth 768 with two outputs.)  Slots
 // of 16 bytes are swizzled by row: both sides are free of bank conflicts.
 template <int WTN>
 struct OutStage {

@@ -16,6 +16,8 @@
 // works on this one.  In the backward pass it also keeps its columns' sums of dy h and dy; the
 // workgroup (one to a CU) joins its waves' sums in LDS and leaves one partial row, and a second
 // launch adds the partial rows in a fixed order (no atomics: the same bits on every run).
+// 65536 x 768 bf16: forward 36 us (5.6 TB/s), backward 59 us (5.1 TB/s; 78 us with a row to each
+// wave at a time and 1024 partial rows); 4096 x 8192: 24 and 53 us.
 #include <algorithm>
 
 #include "device_common.h"
