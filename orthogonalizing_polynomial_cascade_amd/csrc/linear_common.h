@@ -188,10 +188,14 @@ struct RowTiles {
 };
 
 // The group at place j when the groups are taken from the one with the most rows down (in their own
-// order from 65 groups on).  Work on the long groups starts first, so that the short ones fill up
-// the end.
-__device__ __forceinline__ int longest_first(const Groups& g, int64_t rows, int j) {
-  if (!g.offsets || g.count > 64) return j;
+// order from 65 groups on), and its rows.  Work on the long groups starts first, so that the short
+// ones fill up the end.
+__device__ __forceinline__ int longest_first(const Groups& g, int64_t rows, int j, int64_t* begin,
+                                             int64_t* end) {
+  if (!g.offsets || g.count > 64) {
+    group_rows(g, rows, j, begin, end);
+    return j;
+  }
   const int lane = threadIdx.x & 63;
   const int mine = lane <= g.count ? (int)raw_offset(g, lane, rows) : 0;
   const int bound = scan_max(mine, lane);
@@ -206,7 +210,10 @@ __device__ __forceinline__ int longest_first(const Groups& g, int64_t rows, int 
     const int other = __builtin_amdgcn_readlane(size, f);
     rank += other > size || (other == size && f < lane) ? 1 : 0;
   }
-  return __ffsll((unsigned long long)__ballot(lane < g.count && rank == j)) - 1;
+  const int e = __ffsll((unsigned long long)__ballot(lane < g.count && rank == j)) - 1;
+  *begin = __shfl(bound, e);
+  *end = __shfl(next, e);
+  return e;
 }
 
 // Epilogue of one element: sum over the depth in, output (and kept preactivation) out.

@@ -567,13 +567,12 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
   const int unit = xcd * share + at % share;
   if (unit >= tiles) return;
-  const int e = longest_first(p.groups, p.rows, at / share);
+  int64_t begin, end;
+  const int e = longest_first(p.groups, p.rows, at / share, &begin, &end);
   const int s = unit / (tiles_i * tiles_j);
   int ti, tj;
   banded(unit % (tiles_i * tiles_j), tiles_i, tiles_j, &ti, &tj);
   const int i0 = ti * BM, j0 = tj * BN;
-  int64_t begin, end;
-  group_rows(p.groups, p.rows, e, &begin, &end);
   const int64_t part = ((end - begin + kBK - 1) / kBK + splits - 1) / splits * kBK;
   const int64_t k0 = min(begin + s * part, end), k1 = min(k0 + part, end);
 
