@@ -68,36 +68,4 @@ __device__ __forceinline__ float act_slope(int act, float z) {
   }
 }
 
-// N values at once, the choice of the activation outside the loop.
-template <int N>
-__device__ __forceinline__ void activate(int act, float v[N]) {
-  auto all = [&](auto f) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = f(v[e]);
-  };
-  switch (act) {
-    case kActRelu: return all([](float z) { return act_value(kActRelu, z); });
-    case kActRelu2: return all([](float z) { return act_value(kActRelu2, z); });
-    case kActGelu: return all([](float z) { return act_value(kActGelu, z); });
-    case kActSilu: return all([](float z) { return act_value(kActSilu, z); });
-    default: return;
-  }
-}
-
-// v[e] *= act'(z[e])
-template <int N>
-__device__ __forceinline__ void scale_by_slope(int act, const float z[N], float v[N]) {
-  auto all = [&](auto f) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] *= f(z[e]);
-  };
-  switch (act) {
-    case kActRelu: return all([](float x) { return act_slope(kActRelu, x); });
-    case kActRelu2: return all([](float x) { return act_slope(kActRelu2, x); });
-    case kActGelu: return all([](float x) { return act_slope(kActGelu, x); });
-    case kActSilu: return all([](float x) { return act_slope(kActSilu, x); });
-    default: return;
-  }
-}
-
 }  // namespace anvil

@@ -13,7 +13,6 @@
 // owner and no access leaves the buffers whatever they hold; a row without an owner (before the
 // first offset or past the last) gets an output row of zeros.
 #include <algorithm>
-#include <atomic>
 
 #include "activation.h"
 #include "device_common.h"

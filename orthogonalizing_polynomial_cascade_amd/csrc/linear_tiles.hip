@@ -7,8 +7,8 @@
 //    and k past the depth get an offset outside the buffer's range, which loads zeros.
 //  * A wave reads the fragments of one 16-deep k-step while the matrix cores work on the step
 //    before it.  At the last step of a slab the waves meet: the next slab has landed (it was
-//    requested a whole slab earlier), its first fragments are read and the slab after it is
-//    requested into the buffer just finished, all ahead of that step's multiplies.
+//    requested a whole slab earlier), its first fragments are read, and among that step's
+//    multiplies the slab after it is requested into the buffer just finished.
 //  * K-contiguous operands are one ds_read_b128 per fragment and lane, K-major ones two transposing
 //    reads; both layouts are swizzled against bank conflicts (mfma_slab.h).
 //  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row.
