@@ -75,8 +75,12 @@ __device__ __forceinline__ uint32_t lds_addr(const char* ptr) {
 // One wave-instruction of DMA: lane L's 16 bytes at `voff` of the buffer land in LDS at
 // lds + 16*L.  Issued as inline assembly so that the compiler neither reorders it nor inserts its
 // own (conservative) waits on it; completion is tracked with wait_vmcnt below.
+// Nor does the compiler put wait states inside: one is needed between the write of m0 and the copy,
+// five between a vector instruction's write of a scalar register (the v_readfirstlane of a descriptor
+// word) and a vector memory instruction that reads it.  s_nop 4 is five, whatever stands before the
+// block.
 __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc)
                : "memory", "m0");
@@ -84,7 +88,7 @@ __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t lds, uint32_t voff)
 
 // The same with a uniform byte offset `soff` on top of the lanes'; a lane at kOOB stays out of range.
 __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
