@@ -120,19 +120,18 @@ struct AnySlab {
 
 // acc (the wave's fragments, C transposed: register r of lane l is row l%32, column
 // 8(r/4) + 4(l/32) + r%4 of a fragment) of the tile's k range [k0, k1).  `sum`: 1 the wave also adds
-// up its P fragments over k into `sums`, 2 its Q fragments (see row_sum_selector).
+// up its P fragments over k into `sums`, 2 its Q fragments (see add8).
 template <typename T, bool PT, bool QT, int SIDE>
 __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t i0, int64_t ni,
                                                const T* Q, int64_t ldq, int64_t j0, int64_t nj,
                                                int64_t k0, int64_t k1,
                                                f32x16_t (&acc)[SIDE / 64][SIDE / 64], int sum,
-                                               f32x4_t (&sums)[SIDE / 64]) {
+                                               float (&sums)[SIDE / 64]) {
   __shared__ __attribute__((aligned(16))) T lp[SIDE][kAnyPitch];
   __shared__ __attribute__((aligned(16))) T lq[SIDE][kAnyPitch];
   typedef typename Mfma<T>::vec vec;
   constexpr int F = SIDE / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const vec one = row_sum_selector<T>(lane);
   AnySlab<T, PT, SIDE> sp;
   AnySlab<T, QT, SIDE> sq;
   if (k0 < k1) {
@@ -161,10 +160,14 @@ __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t 
       for (int m = 0; m < F; ++m)
 #pragma unroll
         for (int n = 0; n < F; ++n) acc[m][n] = Mfma<T>::run(fq[n], fp[m], acc[m][n]);
-      if (sum) {
+      if (sum) {   // one branch for the waves that have none
+        if (sum == 1) {
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-          sums[f] = Mfma<T>::run16(one, sum == 1 ? fp[f] : fq[f], sums[f]);
+          for (int f = 0; f < F; ++f) add8_of(f, fp[f], sums[f]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < F; ++f) add8_of(F + f, fq[f], sums[f]);
+        }
       }
     }
   }
@@ -183,7 +186,7 @@ void any_rows_kernel(RowsProduct p, int tiles_n) {
     const int64_t j0 = (tile % tiles_n) * SIDE;
     const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * p.cols * p.depth;
     f32x16_t acc[F][F] = {};
-    f32x4_t none[F] = {};
+    float none[F] = {};
     any_accumulate<T, false, QT, SIDE>(static_cast<const T*>(p.a), p.lda, row0, end, b,
                                        QT ? p.cols : p.depth, j0, p.cols, 0,
                                        group < 0 ? 0 : p.depth, acc, 0, none);
@@ -230,18 +233,18 @@ void any_weight_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int 
                     : p.dz_is_q ? (i0 == 0 && wave < 2 ? 2 : 0)
                                 : (j0 == 0 && (wave & 1) == 0 ? 1 : 0);
     f32x16_t acc[F][F] = {};
-    f32x4_t sums[F] = {};
+    float sums[F] = {};
     any_accumulate<T, true, true, SIDE>(static_cast<const T*>(p.p), p.ldp, i0, p.pi,
                                         static_cast<const T*>(p.q), p.ldq, j0, p.qj, k0, k1, acc,
                                         sum, sums);
-    if (sum && lane < 16) {
+    if (sum) {
       float* db = splits > 1 ? ws + splits * plane + (int64_t)s * groups * width : p.db;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
+        const float both = sums[f] + __shfl_xor(sums[f], 32);
         const int64_t c = (p.dz_is_q ? j0 + ((wave & 1) * F + f) * 32
                                      : i0 + ((wave >> 1) * F + f) * 32) + lane;
-        if (c < width) db[(int64_t)e * width + c] = sums[f][0];
-        if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[f][1];
+        if (lane < 32 && c < width) db[(int64_t)e * width + c] = both;
       }
     }
 #pragma unroll

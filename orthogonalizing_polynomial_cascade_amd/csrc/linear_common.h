@@ -17,9 +17,6 @@ struct Mfma<bf16> {
   __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  __device__ static __forceinline__ f32x4_t run16(vec a, vec b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
 };
 template <>
 struct Mfma<f16> {
@@ -27,23 +24,37 @@ struct Mfma<f16> {
   __device__ static __forceinline__ f32x16_t run(vec a, vec b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  __device__ static __forceinline__ f32x4_t run16(vec a, vec b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
 };
 
-// Sums over k of a 32-row fragment (lane l: row l % 32, k 8 (l / 32) .. + 7) by a 16x16x32 multiply,
-// four registers instead of a fragment's sixteen.  That instruction takes the lane's column as
-// l % 16 and its k group as l / 16, so rows r and r + 16 of the fragment meet in one column, in k
-// groups of different parity: row 0 of the other operand holds ones for the even groups, row 1 for
-// the odd ones.  Sums of rows r and 16 + r arrive in entries 0 and 1 of lane r < 16.
-template <typename T>
-__device__ __forceinline__ typename Mfma<T>::vec row_sum_selector(int lane) {
-  typename Mfma<T>::vec v;
-  const float x = lane % 16 == (lane / 16) % 2 ? 1.0f : 0.0f;
+// s plus a lane's eight elements of a 32-row fragment (lane l: row l % 32, k 8 (l / 32) .. + 7), by the
+// two-element dot products of the vector unit with ones: lanes l and l + 32 together hold the row's
+// sum over k.  Every lane adds its own row only.  A matrix instruction that sums two rows at once has
+// to tell them apart by zeros, and 0 * inf is NaN: one infinite gradient would spoil another column.
+// Weight gradients in us with that instruction and with these: 517 x 512 x 4096 fp16 13.8 and 13.6,
+// 32768 x 768 x 2816 163 and 163, 4096^3 131 and 128, 4096 x 4097 x 4095 623 and 622.
+__device__ __forceinline__ float add8(Mfma<bf16>::vec v, float s) {
+  typedef bf16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t one = {from_f32<bf16>(1.0f), from_f32<bf16>(1.0f)};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(x);
-  return v;
+  for (int e = 0; e < 8; e += 2) s = __builtin_amdgcn_fdot2_f32_bf16(pair_t{v[e], v[e + 1]}, one, s, false);
+  return s;
+}
+__device__ __forceinline__ float add8(Mfma<f16>::vec v, float s) {
+  typedef f16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t one = {from_f32<f16>(1.0f), from_f32<f16>(1.0f)};
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) s = __builtin_amdgcn_fdot2(pair_t{v[e], v[e + 1]}, one, s, false);
+  return s;
+}
+
+// add8 of one of several fragments between which a wave chooses; `which` is a constant (an unrolled
+// loop's), another one for each.  The empty block keeps the choices apart: merged into one sum, the
+// compiler moves the chosen fragment through other registers first, behind the multiplies that still
+// read them.
+template <typename V>
+__device__ __forceinline__ void add8_of(int which, V v, float& s) {
+  s = add8(v, s);
+  asm volatile("" : "+v"(s) : "n"(which));
 }
 
 // Offset j of the groups, clamped to [0, rows] (not yet a running maximum).

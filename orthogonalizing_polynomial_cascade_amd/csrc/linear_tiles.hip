@@ -181,9 +181,9 @@ struct Pipe {
   __device__ __forceinline__ char* spare() const { return smem + (KT & 1) * C::kStage; }
 
   // All slabs.  `sum`: 0 none, 1 also the sums over k of the wave's P fragment `wn`, 2 of its Q
-  // fragment `wm` into `sums`.
+  // fragment `wm` into `sums` (see add8).
   template <bool SUMS>
-  __device__ __forceinline__ void run(f32x16_t (&acc)[C::kFM][C::kFN], int sum, f32x4_t& sums) {
+  __device__ __forceinline__ void run(f32x16_t (&acc)[C::kFM][C::kFN], int sum, float& sums) {
     if (KT == 0) return;
     vec fa[2][C::kFM], fb[2][C::kFN];
     auto read = [&](int stage, int ks, int buf) {
@@ -198,7 +198,6 @@ struct Pipe {
         fb[buf][f] = __builtin_bit_cast(
             vec, (read_frag<QT, BN, kBK>(tq, wn * C::kWTN + f * 32, ks, lane)));
     };
-    const vec one = row_sum_selector<T>(lane);
 
     // Slab kt from buffer `stage`.  MORE: there is a slab after it; REQUEST: and one after that,
     // whose copies go out among the last step's multiplies.
@@ -235,11 +234,11 @@ struct Pipe {
           if (sum == 1) {
 #pragma unroll
             for (int f = 0; f < C::kFM; ++f)
-              if (f == wn) sums = Mfma<T>::run16(one, fa[ks & 1][f], sums);
+              if (f == wn) add8_of(f, fa[ks & 1][f], sums);
           } else if (sum == 2) {
 #pragma unroll
             for (int f = 0; f < C::kFN; ++f)
-              if (f == wm) sums = Mfma<T>::run16(one, fb[ks & 1][f], sums);
+              if (f == wm) add8_of(C::kFM + f, fb[ks & 1][f], sums);
           }
         }
         if (last && REQUEST) advance();
@@ -531,7 +530,7 @@ void rows_tile_kernel(RowsProduct p, int tiles_n) {
   for (int fm = 0; fm < C::kFM; ++fm)
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
-  f32x4_t none;
+  float none;
   Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
   pipe.begin(static_cast<const uint16_t*>(p.a) + row0 * p.lda, p.lda, end - row0, b,
              QT ? p.cols : p.depth, p.cols - j0, group < 0 ? 0 : p.depth, kg);
@@ -581,7 +580,7 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   for (int fm = 0; fm < C::kFM; ++fm)
 #pragma unroll
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
-  f32x4_t sums{};
+  float sums = 0.0f;
   const int sum = !p.db ? 0 : p.dz_is_q ? (ti == 0 ? 2 : 0) : (tj == 0 ? 1 : 0);
   Pipe<T, true, true, BM, BN, WM, WN, 1> pipe(smem, wave);
   pipe.begin(static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.pi - i0,
@@ -591,11 +590,11 @@ void weight_tile_kernel(WeightProduct p, float* ws, int splits, int tiles_i, int
   const int wm = wave / WN, wn = wave % WN;
   const int width = p.dz_is_q ? p.qj : p.pi;
   const int64_t plane = (int64_t)p.groups.count * p.pi * p.qj;
-  if (sum && lane < 16 && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
+  if (sum && (sum == 1 ? wn < C::kFM : wm < C::kFN)) {
     const int c = (sum == 1 ? i0 + wm * C::kWTM + wn * 32 : j0 + wn * C::kWTN + wm * 32) + lane;
     float* db = splits > 1 ? ws + splits * plane + (int64_t)s * p.groups.count * width : p.db;
-    if (c < width) db[(int64_t)e * width + c] = sums[0];
-    if (c + 16 < width) db[(int64_t)e * width + c + 16] = sums[1];
+    const float both = sums + __shfl_xor(sums, 32);
+    if (lane < 32 && c < width) db[(int64_t)e * width + c] = both;
   }
   using S = OutStage<C::kWTN>;
   char* stage = pipe.spare() + wave * S::kBytes;

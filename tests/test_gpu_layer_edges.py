@@ -1,0 +1,69 @@
+"""The training operators at the edges of their arguments."""
+import pytest
+import torch
+
+from tests import layer_helpers as H
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _normal(*shape, t, seed, scale=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(t).cuda()
+
+
+# 128x128 and 256x256 tiles from copies, 64x64 and 128x128 tiles of any width
+SUM_SHAPES = [(200, 96, 72), (6000, 776, 1032), (2048, 4104, 2056), (200, 97, 71), (2100, 1031, 1033), (40, 33, 7)]
+
+
+@pytest.mark.parametrize("rows,n,k", SUM_SHAPES)
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_nonfinite_gradient_stays_in_its_column(gpu_lib, rows, n, k, w_kn, kind):
+    """Infinities and NaN in some columns of dz reach the sums of those columns and no others."""
+    t = TYPES[kind]
+    dz, x = _normal(rows, n, t=t, seed=1, scale=0.1), _normal(rows, k, t=t, seed=2)
+    clean = gpu_lib.anvil_linear_grad_weight(dz, x, w_kn=w_kn)
+    inf = float("inf")
+    marks = {0: (inf,), 5: (-inf,), 18: (float("nan"),), n - 1: (inf,), n - 9: (inf, -inf)}
+    for c, values in marks.items():
+        for i, v in enumerate(values):
+            dz[(7 * c + 11 * i) % rows, c] = v
+    dw, db = gpu_lib.anvil_linear_grad_weight(dz, x, w_kn=w_kn)
+    (ww, ew), (bw, eb) = H.grad_weight(dz.cpu(), x.cpu(), w_kn)
+    H.assert_within(db, bw, eb, "db")
+    H.assert_within(dw, ww, ew + H.half_step(ww, torch.float32), "dw")
+    rest = [c for c in range(n) if c not in marks]
+    assert torch.equal(db[rest], clean[1][rest])
+
+
+@pytest.mark.parametrize("n,k", [(264, 136), (67, 33)])
+@pytest.mark.parametrize("w_kn", [False, True])
+def test_nonfinite_gradient_stays_with_its_expert(gpu_lib, n, k, w_kn):
+    t = torch.bfloat16
+    ends = [0, 300, 300, 800, 1000]
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    dz, x = _normal(1000, n, t=t, seed=3, scale=0.1), _normal(1000, k, t=t, seed=4)
+    dz[299, 3], dz[300, 20], dz[999, 40] = float("inf"), float("nan"), -float("inf")
+    dw, db = gpu_lib.anvil_expert_grad_weight(dz, x, off, w_kn=w_kn)
+    for e in range(4):
+        s = slice(ends[e], ends[e + 1])
+        (ww, ew), (bw, eb) = H.grad_weight(dz[s].cpu(), x[s].cpu(), w_kn)
+        H.assert_within(db[e], bw, eb + 1e-45, f"db {e}")
+        H.assert_within(dw[e], ww, ew + H.half_step(ww, torch.float32), f"dw {e}")
+
+
+@pytest.mark.parametrize("n,k", [(96, 72), (97, 71)])
+def test_subnormal_values_count(gpu_lib, n, k):
+    """fp16 gradients below the smallest normal value are not taken as zero."""
+    t = torch.float16
+    dz, x = _normal(300, n, t=t, seed=12, scale=2e-6), _normal(300, k, t=t, seed=13)
+    assert float(dz.abs().max()) < 2.0 ** -14
+    dw, db = gpu_lib.anvil_linear_grad_weight(dz, x)
+    (ww, ew), (bw, eb) = H.grad_weight(dz.cpu(), x.cpu(), False)
+    H.assert_within(dw, ww, ew + H.half_step(ww, torch.float32), "dw")
+    H.assert_within(db, bw, eb, "db")
+    dx = gpu_lib.anvil_linear_grad_input(dz, x[:n].contiguous()[:, :k])
+    want, err = H.grad_input(dz.cpu(), x[:n].cpu(), None, "none", None, False)
+    H.assert_within(dx, want, err + H.half_step(want, t), "dx")
