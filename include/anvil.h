@@ -335,7 +335,9 @@ int anvil_linear_grad_input(const void* dz, int64_t lddz, const void* w, int w_k
 
 /* Gradient of its weight and bias: dw = dz^T x [n][k] (w_kn = 0) or x^T dz [k][n] (w_kn = 1), of
  * dw_dtype (ANVIL_F32 or dtype): a bank's gradient.  dbias = sum over rows of dz, fp32 [n], or
- * NULL.  Both are zeros when there are no rows. */
+ * NULL.  Both are zeros when there are no rows.  Where dw is empty (n, k or experts is 0) the call
+ * returns ANVIL_OK and writes nothing, dbias neither: for the bias gradient of a layer without inputs,
+ * which depends on dz alone, pass k = 1 and any column as x. */
 int anvil_linear_grad_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, int w_kn,
                              void* dw, int dw_dtype, float* dbias, int dtype, int64_t rows,
                              int64_t n, int64_t k, void* workspace, size_t workspace_bytes,

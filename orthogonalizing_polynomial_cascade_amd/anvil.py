@@ -730,6 +730,10 @@ def _grad_weight(fn, dz, x, offsets, w_kn, out, out_dtype, want_bias, workspace,
     if out is None:
         out = _empty(shape, out_dtype or _torch.float32, dz.device, stream)
     dw, out_code = _parameter(out, "out", code, dz, device, shape)
+    if want_bias and k == 0 and n:
+        # nothing of a weight, and the library returns at once; its bias has a gradient all the same,
+        # which does not depend on x: one column of dz stands in for it
+        return out, _grad_weight(fn, dz, dz[:, :1], offsets, w_kn, None, None, True, None, stream)[1]
     dbias = _empty(stack + (n,), _torch.float32, dz.device, stream) if want_bias else None
     lib = load()
     need = lib.anvil_linear_grad_weight_workspace(1 if w_kn else 0, rows, n, k,

@@ -54,6 +54,28 @@ def test_nonfinite_gradient_stays_with_its_expert(gpu_lib, n, k, w_kn):
         H.assert_within(dw[e], ww, ew + H.half_step(ww, torch.float32), f"dw {e}")
 
 
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("rows,n", [(1, 1), (40, 64), (5000, 33)])
+def test_bias_gradient_of_a_layer_without_inputs(gpu_lib, rows, n, w_kn):
+    """k = 0: the output is the bias alone, whose gradient is the sum of dz all the same."""
+    t = torch.bfloat16
+    dz = _normal(rows, n, t=t, seed=5)
+    x = torch.empty(rows, 0, dtype=t, device="cuda")
+    _, (want, err) = H.grad_weight(dz.cpu(), x.cpu(), w_kn)
+    torch.full((1 << 18,), float("nan"), device="cuda")   # memory that the result may come from
+    dw, db = gpu_lib.anvil_linear_grad_weight(dz, x, w_kn=w_kn)
+    assert dw.numel() == 0
+    H.assert_within(db, want, err, "db")
+    assert gpu_lib.anvil_linear_grad_weight(dz, x, w_kn=w_kn, want_bias=False)[1] is None
+    ends = [0, rows // 2, rows // 2, rows]
+    off = torch.tensor(ends, dtype=torch.int64, device="cuda")
+    dw, db = gpu_lib.anvil_expert_grad_weight(dz, x, off, w_kn=w_kn)
+    assert dw.shape == ((3, 0, n) if w_kn else (3, n, 0)) and db.shape == (3, n)
+    for e in range(3):
+        _, (want, err) = H.grad_weight(dz[ends[e]:ends[e + 1]].cpu(), x[ends[e]:ends[e + 1]].cpu(), w_kn)
+        H.assert_within(db[e], want, err + 1e-45, f"db {e}")
+
+
 @pytest.mark.parametrize("n,k", [(96, 72), (97, 71)])
 def test_subnormal_values_count(gpu_lib, n, k):
     """fp16 gradients below the smallest normal value are not taken as zero."""
