@@ -565,7 +565,7 @@ def _empty(shape, dtype, device, stream):
     t = _torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
         s = stream if isinstance(stream, _torch.cuda.Stream) else \
-            _torch.cuda.ExternalStream(int(stream))
+            _torch.cuda.ExternalStream(_raw_stream(stream, device))
         if s != _torch.cuda.current_stream():
             t.record_stream(s)
     return t

@@ -76,6 +76,25 @@ def test_bias_gradient_of_a_layer_without_inputs(gpu_lib, rows, n, w_kn):
         H.assert_within(db[e], want, err + 1e-45, f"db {e}")
 
 
+class _Borrowed:
+    """A stream of another library: its handle under the name that torch's streams have."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+def test_streams_of_other_kinds(gpu_lib):
+    """A handle, and an object that holds one, work as a torch stream does."""
+    t = torch.bfloat16
+    x, w = _normal(70, 64, t=t, seed=10), _normal(96, 64, t=t, seed=11)
+    want = gpu_lib.anvil_linear(x, w, act="relu")[0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [gpu_lib.anvil_linear(x, w, act="relu", stream=k)[0] for k in (s, s.cuda_stream, _Borrowed(s))]
+    s.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
 @pytest.mark.parametrize("n,k", [(96, 72), (97, 71)])
 def test_subnormal_values_count(gpu_lib, n, k):
     """fp16 gradients below the smallest normal value are not taken as zero."""
