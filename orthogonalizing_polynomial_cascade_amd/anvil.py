@@ -174,7 +174,7 @@ def anvil_bank_step(grad, velocity, momentum, fast_beta, fast_weight, out=None, 
     g, m, n = _gmn(grad)
     _need(velocity, "velocity", torch.float32, (2, g, m, n))
     if out is None:
-        out = torch.empty((g, m, n), dtype=torch.bfloat16, device=grad.device)
+        out = _empty((g, m, n), torch.bfloat16, grad.device, stream)
     _need(out, "out", torch.bfloat16, (g, m, n))
     if workspace is None:
         st = lib.anvil_bank_step(_ptr(grad), _ptr(velocity), momentum, fast_beta, fast_weight,
@@ -218,7 +218,7 @@ def anvil_bank_step_maps(grad, velocity, momentum, fast_beta, fast_weight, maps,
         raise ValueError("maps must be (a, b, c) triples")
     host = (ctypes.c_float * max(1, len(table)))(*table)
     if out is None:
-        out = torch.empty((g, m, n), dtype=torch.bfloat16, device=grad.device)
+        out = _empty((g, m, n), torch.bfloat16, grad.device, stream)
     _need(out, "out", torch.bfloat16, (g, m, n))
     ws, wsb = None, 0
     if workspace is not None:
@@ -297,7 +297,7 @@ def anvil_momentum(grad, velocity, momentum, fast_beta, fast_weight, x_out=None,
     g, m, n = _gmn(grad)
     _need(velocity, "velocity", torch.float32, (2, g, m, n))
     if x_out is None:
-        x_out = torch.empty((g, m, n), dtype=torch.bfloat16, device=grad.device)
+        x_out = _empty((g, m, n), torch.bfloat16, grad.device, stream)
     _need(x_out, "x_out", torch.bfloat16, (g, m, n))
     _check("anvil_momentum", lib.anvil_momentum(_ptr(grad), _ptr(velocity), momentum, fast_beta,
                                                 fast_weight, _ptr(x_out), g, m, n, _stream(stream)))
@@ -312,10 +312,10 @@ def anvil_gram(x, a_out=None, trace_partials=None, want_trace=False, stream=None
     g, m, n = _gmn(x)
     s = min(m, n)
     if a_out is None:
-        a_out = torch.empty((g, s, s), dtype=torch.bfloat16, device=x.device)
+        a_out = _empty((g, s, s), torch.bfloat16, x.device, stream)
     _need(a_out, "a_out", torch.bfloat16, (g, s, s))
     if want_trace and trace_partials is None:
-        trace_partials = torch.empty((g, trace_slots(m, n)), dtype=torch.float32, device=x.device)
+        trace_partials = _empty((g, trace_slots(m, n)), torch.float32, x.device, stream)
     if trace_partials is not None:
         _need(trace_partials, "trace_partials", torch.float32, (g, trace_slots(m, n)))
     _check("anvil_gram", lib.anvil_gram(_ptr(x), _ptr(a_out), _ptr(trace_partials), g, m, n,
@@ -333,7 +333,7 @@ def anvil_normalize(x, a, trace_partials, d_out=None, stream=None):
     _need(a, "a", torch.bfloat16, (g, s, s))
     _need(trace_partials, "trace_partials", torch.float32, (g, trace_slots(m, n)))
     if d_out is None:
-        d_out = torch.empty((g,), dtype=torch.float32, device=x.device)
+        d_out = _empty((g,), torch.float32, x.device, stream)
     _need(d_out, "d_out", torch.float32, (g,))
     _check("anvil_normalize", lib.anvil_normalize(_ptr(x), _ptr(a), _ptr(trace_partials),
                                                   _ptr(d_out), g, m, n, _stream(stream)))
@@ -348,7 +348,7 @@ def anvil_poly(a, coef_b, coef_c, b_out=None, stream=None):
     if s != s2:
         raise ValueError("a must be a stack of square matrices")
     if b_out is None:
-        b_out = torch.empty_like(a)
+        b_out = _empty(a.shape, a.dtype, a.device, stream)
     _need(b_out, "b_out", torch.bfloat16, (g, s, s))
     _check("anvil_poly", lib.anvil_poly(_ptr(a), _ptr(b_out), coef_b, coef_c, g, s, _stream(stream)))
     return b_out
@@ -362,7 +362,7 @@ def anvil_apply(x, b, coef_a, split, c_out=None, stream=None):
     s = min(m, n)
     _need(b, "b", torch.bfloat16, (g, s, s))
     if c_out is None:
-        c_out = torch.empty_like(x)
+        c_out = _empty(x.shape, x.dtype, x.device, stream)
     _need(c_out, "c_out", torch.bfloat16, (g, m, n))
     _check("anvil_apply", lib.anvil_apply(_ptr(x), _ptr(b), _ptr(c_out), coef_a, int(bool(split)),
                                           g, m, n, _stream(stream)))
@@ -394,7 +394,7 @@ def anvil_bank_update(grad, velocity, momentum, fast_beta, fast_weight, lane_ene
     _need(mantissa, "mantissa", mantissa.dtype, (g, m, n))
     _need(eff_lr, "eff_lr", torch.float32, (g,))
     if update is None:
-        update = torch.empty((g, m, n), dtype=torch.bfloat16, device=grad.device)
+        update = _empty((g, m, n), torch.bfloat16, grad.device, stream)
     _need(update, "update", torch.bfloat16, (g, m, n))
     args = [_ptr(grad), _ptr(velocity), momentum, fast_beta, fast_weight, _ptr(update),
             _ptr(lane_energy), beta2, _ptr(param), _ptr(mantissa), eff_wd, _ptr(eff_lr), g, m, n]
@@ -418,7 +418,7 @@ def anvil_equalize(update, lane_energy, beta2, lane_scratch=None, stream=None):
     if lane_energy.numel() != g * lanes:
         raise ValueError("lane_energy must hold g * lanes values")
     if lane_scratch is None:
-        lane_scratch = torch.empty(2 * g * lanes, dtype=torch.float32, device=update.device)
+        lane_scratch = _empty(2 * g * lanes, torch.float32, update.device, stream)
     _need(lane_scratch, "lane_scratch", torch.float32)
     if lane_scratch.numel() < 2 * g * lanes:
         raise ValueError("lane_scratch must hold 2 * g * lanes values")
@@ -559,15 +559,27 @@ def _parameter(t, name, code, like, device, shape):
     return _dense(t, name, t.dtype, device, shape), own
 
 
+def _other_stream(stream):
+    """`stream` as a torch stream where it is not the current one, else None."""
+    torch = _module()
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)
+
+
 def _empty(shape, dtype, device, stream):
-    """torch.empty for a call on `stream`: memory of another stream than the current one is kept
-    from reuse until that stream is done with it."""
-    t = _torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        s = stream if isinstance(stream, _torch.cuda.Stream) else \
-            _torch.cuda.ExternalStream(_raw_stream(stream, device))
-        if s != _torch.cuda.current_stream():
-            t.record_stream(s)
+    """torch.empty for a call on `stream`.  For another stream than the current one the memory is that
+    stream's own: whatever used it before was queued there too, ahead of this call (memory of the
+    current stream may still be in use by what is queued on it).  The current stream, where the
+    caller goes on with the tensor, is recorded as its second user."""
+    torch = _torch or _module()
+    other = None if stream is None else _other_stream(stream)
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 

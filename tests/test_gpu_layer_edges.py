@@ -108,3 +108,29 @@ def test_subnormal_values_count(gpu_lib, n, k):
     dx = gpu_lib.anvil_linear_grad_input(dz, x[:n].contiguous()[:, :k])
     want, err = H.grad_input(dz.cpu(), x[:n].cpu(), None, "none", None, False)
     H.assert_within(dx, want, err + H.half_step(want, t), "dx")
+
+
+def test_outputs_on_another_stream_come_from_its_memory(gpu_lib):
+    """A block that the current stream has just freed is not handed to a call on another stream."""
+    t = torch.bfloat16
+    x, w = _normal(1024, 64, t=t, seed=14), _normal(2048, 64, t=t, seed=15)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = torch.empty(1024, 2048, dtype=t, device="cuda")
+    at = freed.data_ptr()
+    del freed
+    y = gpu_lib.anvil_linear(x, w, stream=s)[0]
+    assert y.data_ptr() != at
+    s.synchronize()
+    assert torch.equal(y, gpu_lib.anvil_linear(x, w)[0])
+    # a bank call likewise
+    grad = torch.randn(2, 64, 128, device="cuda")
+    rails = [torch.zeros(2, 2, 64, 128, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    freed = torch.empty(2, 64, 128, dtype=t, device="cuda")
+    at = freed.data_ptr()
+    del freed
+    other = gpu_lib.anvil_bank_step(grad, rails[0], 0.95, 0.85, 1.0, stream=s)
+    assert other.data_ptr() != at
+    s.synchronize()
+    assert torch.equal(other, gpu_lib.anvil_bank_step(grad, rails[1], 0.95, 0.85, 1.0))
