@@ -296,7 +296,8 @@ enum anvil_act {
  * y = (x - mean) rstd weight + bias.
  *   x, y         dtype [rows][cols] at pitches ldx, ldy
  *   weight, bias [cols] of param_dtype (ANVIL_F32 or dtype), each may be NULL (1 and 0)
- *   mean, rstd   fp32 [rows], for the backward pass; each may be NULL */
+ *   mean, rstd   fp32 [rows], for the backward pass; each may be NULL
+ * Without columns the call returns ANVIL_OK and writes nothing, mean and rstd neither. */
 int anvil_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias,
                      int param_dtype, float eps, void* y, int64_t ldy, float* mean, float* rstd,
                      int dtype, int64_t rows, int64_t cols, void* stream);

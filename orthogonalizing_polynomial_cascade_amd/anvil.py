@@ -603,7 +603,8 @@ def _scratch(workspace, need, device, stream):
 def anvil_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """Layer norm of each row of x (bf16, fp16 or fp32 [rows, cols]); weight and bias [cols] are
     fp32 or of x's dtype.  Returns (y, mean, rstd), the last two fp32 [rows] for the backward
-    pass."""
+    pass (NaN where there are no columns)."""
+    torch = _module()
     device = _device(x, "x")
     code = _code(x, "x", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
     rows, cols, ldx = _rows(x, "x")
@@ -622,6 +623,9 @@ def anvil_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None)
                                      _raw_stream(stream, device))
     if status:
         _check("anvil_layer_norm", status)
+    if cols == 0:   # the library returns at once; the mean of nothing is 0 / 0
+        with torch.cuda.stream(None if stream is None else _other_stream(stream)):
+            stats.fill_(float("nan"))
     return out, mean, rstd
 
 

@@ -76,6 +76,15 @@ def test_bias_gradient_of_a_layer_without_inputs(gpu_lib, rows, n, w_kn):
         H.assert_within(db[e], want, err + 1e-45, f"db {e}")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_norm_statistics_without_columns(gpu_lib, kind):
+    """No columns: the mean of nothing, 0 / 0, and what follows from it."""
+    torch.zeros(1 << 18, device="cuda")   # memory that the statistics may come from
+    y, mean, rstd = gpu_lib.anvil_layer_norm(torch.empty(300, 0, dtype=TYPES[kind], device="cuda"))
+    assert y.shape == (300, 0) and mean.shape == rstd.shape == (300,)
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+
+
 class _Borrowed:
     """A stream of another library: its handle under the name that torch's streams have."""
 
