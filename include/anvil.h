@@ -267,8 +267,8 @@ int anvil_bank_update_dev(const void* grad, int grad_dtype, float* velocity,
  * Training operators around a bank: the layers whose gradients the bank step takes.
  *
  * Conventions on top of those above:
- *   - Matrices of activations are [rows][width] with a pitch (ld*, in elements, >= width; any
- *     value for a single row; at most 2^22) between rows; weights are contiguous.  Any widths,
+ *   - Matrices of activations are [rows][width] with a pitch (ld*, in elements, >= width and at most
+ *     2^22; any value for a single row, which has none) between rows; weights are contiguous.  Any widths,
  *     pitches and element-aligned pointers are taken (rows < 2^31, widths <= 2^22, one weight
  *     matrix <= 2^30 elements); the linear layers run fastest when widths and pitches are
  *     multiples of 8 and pointers 16-byte aligned.  An output may not share memory with another

@@ -58,9 +58,11 @@ int check_views(std::initializer_list<View> views) {
   return ANVIL_OK;
 }
 
-// A pitch in elements: at least the row, within bounds (a single row needs none).
-bool pitch_ok(const void* p, int64_t ld, int64_t width, int64_t rows) {
-  return !p || ((ld >= width || rows <= 1) && ld <= kMaxPitch && ld >= 0);
+// A pitch in elements: at least the row, within bounds.  A single row has none: its is taken as the
+// row's width, whatever the caller's value (the last token of a long sequence has the sequence's).
+bool take_pitch(const void* p, int64_t* ld, int64_t width, int64_t rows) {
+  if (rows <= 1) *ld = width;
+  return !p || (*ld >= width && *ld <= kMaxPitch);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -108,8 +110,8 @@ int rows_forward(const void* x, int64_t ldx, const void* w, int w_kn, const Grou
   const int64_t count = grouped ? g.count : 1;
   if (grouped && !g.offsets) return ANVIL_ERR_INVALID_ARG;
   if (!y || (k > 0 && !x) || (k > 0 && count > 0 && !w)) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(x, ldx, k, rows) || !pitch_ok(y, ldy, n, rows) ||
-      !pitch_ok(preact, ldz, n, rows) || !pitch_ok(residual, ldr, n, rows))
+  if (!take_pitch(x, &ldx, k, rows) || !take_pitch(y, &ldy, n, rows) ||
+      !take_pitch(preact, &ldz, n, rows) || !take_pitch(residual, &ldr, n, rows))
     return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype);
   if (!aligned(x, eb) || !aligned(w, eb) || !aligned(y, eb) || !aligned(preact, eb) ||
@@ -148,8 +150,8 @@ int rows_backward(const void* dz, int64_t lddz, const void* w, int w_kn, const G
   if (grouped && !g.offsets) return ANVIL_ERR_INVALID_ARG;
   if (!dx || (n > 0 && !dz) || (n > 0 && count > 0 && !w)) return ANVIL_ERR_INVALID_ARG;
   if (act != ANVIL_ACT_NONE && !preact) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(dz, lddz, n, rows) || !pitch_ok(dx, lddx, k, rows) ||
-      !pitch_ok(preact, ldz, k, rows) || !pitch_ok(add, ldadd, k, rows))
+  if (!take_pitch(dz, &lddz, n, rows) || !take_pitch(dx, &lddx, k, rows) ||
+      !take_pitch(preact, &ldz, k, rows) || !take_pitch(add, &ldadd, k, rows))
     return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype);
   if (!aligned(dz, eb) || !aligned(w, eb) || !aligned(dx, eb) || !aligned(preact, eb) ||
@@ -216,7 +218,7 @@ int weight_backward(const void* dz, int64_t lddz, const void* x, int64_t ldx, in
   if (n == 0 || k == 0 || count == 0) return ANVIL_OK;
   if (grouped && !g.offsets) return ANVIL_ERR_INVALID_ARG;
   if (!dw || (rows > 0 && (!dz || !x))) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(dz, lddz, n, rows) || !pitch_ok(x, ldx, k, rows)) return ANVIL_ERR_UNSUPPORTED;
+  if (!take_pitch(dz, &lddz, n, rows) || !take_pitch(x, &ldx, k, rows)) return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype), wb = elem_bytes(dw_dtype);
   if (!aligned(dz, eb) || !aligned(x, eb) || !aligned(dw, wb) || !aligned(dbias, 4))
     return ANVIL_ERR_MISALIGNED;
@@ -267,7 +269,7 @@ int anvil_layer_norm(const void* x, int64_t ldx, const void* weight, const void*
   if (st != ANVIL_OK) return st;
   if (rows == 0 || cols == 0) return ANVIL_OK;
   if (!x || !y) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(x, ldx, cols, rows) || !pitch_ok(y, ldy, cols, rows)) return ANVIL_ERR_UNSUPPORTED;
+  if (!take_pitch(x, &ldx, cols, rows) || !take_pitch(y, &ldy, cols, rows)) return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype), pb = weight || bias ? elem_bytes(param_dtype) : 1;
   if (!aligned(x, eb) || !aligned(y, eb) || !aligned(weight, pb) || !aligned(bias, pb) ||
       !aligned(mean, 4) || !aligned(rstd, 4))
@@ -303,8 +305,8 @@ int anvil_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t l
   const bool sums = dweight || dbias;
   if (rows == 0 && !sums) return ANVIL_OK;
   if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(dy, lddy, cols, rows) || !pitch_ok(x, ldx, cols, rows) ||
-      !pitch_ok(dx, lddx, cols, rows))
+  if (!take_pitch(dy, &lddy, cols, rows) || !take_pitch(x, &ldx, cols, rows) ||
+      !take_pitch(dx, &lddx, cols, rows))
     return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype), pb = weight ? elem_bytes(param_dtype) : 1;
   if (!aligned(dy, eb) || !aligned(x, eb) || !aligned(dx, eb) || !aligned(weight, pb) ||
@@ -398,8 +400,8 @@ int anvil_activation_grad(const void* dy, int64_t lddy, const void* preact, int6
   if (!act_known(act)) return ANVIL_ERR_INVALID_ARG;
   if (rows == 0 || n == 0) return ANVIL_OK;
   if (!dy || !preact || !dz) return ANVIL_ERR_INVALID_ARG;
-  if (!pitch_ok(dy, lddy, n, rows) || !pitch_ok(preact, ldz, n, rows) ||
-      !pitch_ok(dz, lddz, n, rows))
+  if (!take_pitch(dy, &lddy, n, rows) || !take_pitch(preact, &ldz, n, rows) ||
+      !take_pitch(dz, &lddz, n, rows))
     return ANVIL_ERR_UNSUPPORTED;
   const int eb = elem_bytes(dtype);
   if (!aligned(dy, eb) || !aligned(preact, eb) || !aligned(dz, eb)) return ANVIL_ERR_MISALIGNED;

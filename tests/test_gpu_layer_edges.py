@@ -85,6 +85,34 @@ def test_norm_statistics_without_columns(gpu_lib, kind):
     assert torch.isnan(mean).all() and torch.isnan(rstd).all()
 
 
+@pytest.mark.parametrize("pitch", [1 << 24, (1 << 23) + 1])
+@pytest.mark.parametrize("width", [768, 77])
+def test_single_row_at_any_pitch(gpu_lib, pitch, width):
+    """The last token of a long sequence: one row, whose stride is never taken."""
+    t = torch.bfloat16
+    n = 64
+    x = _normal(1, width, t=t, seed=6).as_strided((1, width), (pitch, 1))
+    dz = _normal(1, n, t=t, seed=7).as_strided((1, n), (pitch, 1))
+    assert x.stride(0) == pitch
+    flat, dflat = x.clone(memory_format=torch.contiguous_format).reshape(1, width), dz.reshape(-1).clone().reshape(1, n)
+    w = _normal(n, width, t=t, seed=8)
+    y, mean, rstd = gpu_lib.anvil_layer_norm(x)
+    ref = gpu_lib.anvil_layer_norm(flat)
+    assert all(torch.equal(p, q) for p, q in zip((y, mean, rstd), ref))
+    got = gpu_lib.anvil_layer_norm_grad(x, x, None, mean, rstd)
+    ref = gpu_lib.anvil_layer_norm_grad(flat, flat, None, mean, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    out = torch.empty(1, n, dtype=t, device="cuda").as_strided((1, n), (pitch, 1))
+    got = gpu_lib.anvil_linear(x, w, residual=dz, act="silu", keep_preact=True, out=out)
+    ref = gpu_lib.anvil_linear(flat, w, residual=dflat, act="silu", keep_preact=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    got = gpu_lib.anvil_linear_grad_input(dz, w, preact=x, act="gelu", add=x)
+    assert torch.equal(got, gpu_lib.anvil_linear_grad_input(dflat, w, preact=flat, act="gelu", add=flat))
+    got, ref = gpu_lib.anvil_linear_grad_weight(dz, x), gpu_lib.anvil_linear_grad_weight(dflat, flat)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    assert torch.equal(gpu_lib.anvil_activation_grad(x, x, "relu2"), gpu_lib.anvil_activation_grad(flat, flat, "relu2"))
+
+
 class _Borrowed:
     """A stream of another library: its handle under the name that torch's streams have."""
 
