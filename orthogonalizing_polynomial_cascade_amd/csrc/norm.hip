@@ -299,8 +299,11 @@ void norm_grad_kernel(NormParams p) {
     for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        // a column past the end has dy = 0: it adds nothing to any sum
-        const float hv = (h[k][e] - mean) * rstd;
+        // a column past the end has dy = 0 and adds nothing to any sum, if its h is finite:
+        // (0 - mean) rstd need not be.  Pieces of the first half are whole at every width of the
+        // layout.
+        const bool there = k < CHUNKS / 2 || R::col(k) + (EVEN ? 0 : e) < p.cols;
+        const float hv = (h[k][e] - mean) * (there ? rstd : 0.0f);
         const float d = g[k][e];
         sb[k][e] += d;
         sw[k][e] = fmaf(d, hv, sw[k][e]);
@@ -369,9 +372,11 @@ __global__ __launch_bounds__(256) void norm_grad_long_kernel(NormParams p) {
       load_param<T>(p.w, p.param_f32, c, p.cols, 1.0f, w);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        const float gv = c + e < p.cols ? g[e] * w[e] : 0.0f;
-        s1 += gv;
-        s2 = fmaf(gv, (xv[e] - mean) * rstd, s2);
+        if (c + e < p.cols) {
+          const float gv = g[e] * w[e];
+          s1 += gv;
+          s2 = fmaf(gv, (xv[e] - mean) * rstd, s2);
+        }
       }
     }
     s1 = row_sum<256>(s1, red[0]) / (float)p.cols;

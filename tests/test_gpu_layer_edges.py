@@ -113,6 +113,24 @@ def test_single_row_at_any_pitch(gpu_lib, pitch, width):
     assert torch.equal(gpu_lib.anvil_activation_grad(x, x, "relu2"), gpu_lib.anvil_activation_grad(flat, flat, "relu2"))
 
 
+@pytest.mark.parametrize("cols", [12, 40, 600, 1100, 1601, 2100, 5000, 9001])
+def test_norm_gradient_of_rows_near_the_end_of_the_range(gpu_lib, cols):
+    """Rows of one value 2^120 with rstd 512: (0 - mean) rstd, as a column past the end would have it,
+    is no fp32 value, while every column that is there has h = 0 and so dx = rstd (dy - mean(dy))."""
+    x = torch.full((3, cols), 2.0 ** 120, device="cuda")
+    dy = _normal(3, cols, t=torch.float32, seed=9)
+    mean, rstd = torch.full((3,), 2.0 ** 120, device="cuda"), torch.full((3,), 512.0, device="cuda")
+    dx, dw, db = gpu_lib.anvil_layer_norm_grad(dy, x, None, mean, rstd)
+    d = dy.double().cpu()
+    a = d.mean(1, keepdim=True)
+    # the mean is a sum of cols products and two roundings, the rest four more
+    ea = (H.SIGMA * H.U32 * cols ** 0.5 * d.square().sum(1, keepdim=True).sqrt()) / cols + 4 * H.U32 * a.abs()
+    want = 512 * (d - a)
+    H.assert_within(dx, want, 512 * (ea + 8 * H.U32 * (d.abs() + a.abs())), "dx")
+    assert torch.count_nonzero(dw) == 0
+    H.assert_within(db, d.sum(0), 4 * H.U32 * d.abs().sum(0), "db")
+
+
 class _Borrowed:
     """A stream of another library: its handle under the name that torch's streams have."""
 
