@@ -17,8 +17,11 @@ __device__ __forceinline__ float gauss(float z) {
 
 // Standard normal distribution function, given g = gauss(z).  With x = |z| / sqrt(2) and
 // t = 1 / (1 + 0.4 x), exp(x^2) erfc(x) / t is smooth on 0 < t <= 1; the polynomial is its
-// least-maximum fit of degree 8 (relative error 6e-8, 4e-7 as evaluated in fp32, in the tail as
-// well: a sixteen-bit result rounds as the exact one but for the nearest ties).  A third of the
+// least-maximum fit of degree 8 (relative error 6e-8).  Evaluated in fp32 the tail erfc(x) / 2 is off by
+// at most 5e-7 + 6e-8 z^2 of itself: the exponent -z^2 / 2 is rounded before the power is taken, so
+// the error grows with it (4e-7 below |z| = 2, 2e-6 at 6, 8e-6 at 13), and the hardware's power and
+// reciprocal add a step each.  A sixteen-bit result, whose half step is 4.9e-4 or more, rounds as the
+// exact one but for the nearest ties.  A third of the
 // instructions of the library's erfcf, which kept the epilogue of a 256x256 tile busy for longer
 // than the multiplies of depth 768.
 __device__ __forceinline__ float normal_cdf(float z, float g) {
