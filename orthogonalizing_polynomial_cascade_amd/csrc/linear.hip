@@ -28,9 +28,9 @@ constexpr int64_t kMaxGrid = 1 << 22;   // a launch counts its work-items in 32 
 // The kernels for any width, pitch and alignment: tiles of SIDE x SIDE (64, or 128 where there are
 // enough of them), four waves of F x F 32x32 fragments, operands through registers into LDS (the
 // copies of linear_tiles.hip need 16-byte alignment).  Bound by the two barriers a slab, by the
-// two-byte LDS writes of K-major operands and by an epilogue of single elements: 444 TFLOP/s at 4096 x
-// 4097 x 4095 with w [n, k], 367 with w [k, n], 218 in the weight gradient, 265 where 2817 columns
-// have a depth of 769.  Slabs of 32 k, which wait for memory twice as often, and guarded loads of
+// two-byte LDS writes of K-major operands and by an epilogue of single elements: 441 TFLOP/s at 4096 x
+// 4097 x 4095 with w [n, k] and 365 with w [k, n], 220 and 275 in their weight gradients.  128x128 tiles
+// of a K-major weight spill 8 registers, those of the weight gradient 4.  Slabs of 32 k, which wait for memory twice as often, and guarded loads of
 // single elements at the edges took 1247 us for the first of these instead of 310.
 // ---------------------------------------------------------------------------------------------
 
@@ -305,7 +305,16 @@ __global__ __launch_bounds__(256) void join_kernel(const float* ws, int splits, 
 int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, kMaxGrid)); }
 
-// 128x128 tiles once they give every CU one.
+// 128x128 tiles once they give every CU one.  Us of the forward product with 64x64 and 128x128 tiles, by
+// the number of the latter:
+//    72 tiles, depth 769   20.1   39.5      288 tiles, depth 769    38.7   41.7
+//   144 tiles, depth 769   23.7   37.0      544 tiles, depth 769    64.2   73.2
+//   272 tiles, depth 513   31.8   33.3     1056 tiles, depth 4095  439.9  308.9
+// and of the weight gradient with its best splits, by rows x columns of the weight:
+//    600 rows,  131 x 333   12.9  21.4      2048 rows, 1031 x 769   37.4   35.9
+//   4096 rows, 2049 x 769   92.4  73.3      4096 rows, 4097 x 4095 732.2  584.0
+// The larger tiles pay with the depth: short of about a thousand, 64x64 would be 5 to 15% faster past
+// the threshold too.
 constexpr int64_t kManyTiles = 256;
 
 template <typename T, int SIDE>
@@ -333,7 +342,14 @@ struct AnyPlan {
 };
 
 // Splits of each group's rows: enough workgroups for two rounds of two (128x128) or four (64x64) a
-// CU while a split keeps at least 512 rows on average.
+// CU while a split keeps at least 512 rows on average.  Us by side/splits, the choice first:
+//    600 rows,  131 x 333    64/1   17.3   64/2  12.9   128/2 21.4
+//   2048 rows, 1031 x 769    64/4   38.0   64/1  45.9   64/2  37.4   128/4 35.9
+//   4096 rows, 1031 x 769   128/8   56.2   128/4 49.8   128/1 140.1   64/4 59.3
+//   4096 rows, 2049 x 769   128/8   93.2   128/4 73.3   128/2 80.7    64/4 92.4
+//  32768 rows,  131 x 333   128/64  81.1   64/32 67.0   64/64 83.2   128/32 77.5
+//   4096 rows, 4097 x 4095 128/1  643.9   128/2 584.0   64/1 732.2
+// Half as many splits would serve most of these better, by a tenth to a quarter.
 AnyPlan any_weight_plan(const WeightProduct& a) {
   const int64_t most = std::max<int64_t>(1, a.rows / a.groups.count / 512);
   auto splits = [&](int side, int64_t slots) {

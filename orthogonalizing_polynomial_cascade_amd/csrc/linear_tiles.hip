@@ -14,9 +14,10 @@
 //  * The multiplies take (Q, P), so a lane holds runs of four consecutive columns of one output row.
 //    The rows leave through LDS (the buffer that is free by then), eight columns a lane, whole lines
 //    an access, with bias, activation, derivative and residual applied on the way.
-//  * What bounds it: the multiplies need 62% of the cycles at 8192^3 (1250 TFLOP/s with w [n, k],
-//    1340 with w [k, n], 1150 in the weight gradient; the barrier and the waits ahead of it take
-//    most of the rest), LDS is busy for a quarter of them and free of bank conflicts.  A slab of
+//  * What bounds it: the matrix cores are busy in 76% of the cycles at 8192^3 forward, 55% in the
+//    weight gradient (1260 TFLOP/s with w [n, k], 1300 with w [k, n], 1100 in the weight gradient;
+//    the barrier and the waits ahead of it take most of the rest, waves wait in 32% of their cycles),
+//    LDS is busy in 29% and 21% of them and free of bank conflicts.  A slab of
 //    64 k keeps the K-contiguous copies at whole 128-byte lines (rings of four 32-deep slabs were 8%
 //    slower), and 256x256 tiles read 7.8 bytes a thousand operations where 128x128 ones read
 //    15.6 (8192^3: 1080 TFLOP/s).  Copies placed between the multiplies of a slab's last k-step, all
@@ -692,7 +693,15 @@ double tile_cost(int side, double tiles, double slabs, bool heavy) {
 RowsTile rows_tile(const RowsProduct& a) {
   const int64_t stack = a.groups.offsets ? std::max(1, a.groups.count) : 1;
   const int64_t height = ceil64(a.rows, stack);   // rows of a typical group
-  // up to 32 rows a taller tile only adds work on rows that are not there
+  // Up to 32 rows a taller tile only adds work on rows that are not there: us with 32x32 / 32x128 /
+  // 64x64 tiles, the first or second taken by the same kind of fit (rounds of workgroups, slabs of
+  // one set of waves):
+  //   1 row, 768 columns, depth 2816   7.2 / 12.8 / 10.3    64 rows over 8, 2816, depth 768    17.1 /  9.8 / 13.8
+  //   1 row, 4096, depth 4096         10.4 / 24.7 / 16.7    64 over 8, 512, depth 4096         12.9 / 27.1 / 19.0
+  //   32 rows, 4096, depth 512         4.7 /  5.4 /  5.3    1000 over 32, 2816, depth 768      90.6 / 39.7 / 49.3
+  //   32 rows, 512, depth 4096         8.7 / 17.7 / 13.5    768 over 24, 512, depth 4096       38.3 / 32.1 / 28.4
+  // The last is one of two measured calls where 64x64 tiles, which share the depth among four sets,
+  // are faster (by a tenth).
   if (height <= 32) {
     const double tiles_m = a.groups.offsets ? (double)a.rows / 32 + 0.5 * (double)stack : 1.0;
     const double slabs = (double)ceil64(a.depth, kBK);
@@ -708,8 +717,18 @@ RowsTile rows_tile(const RowsProduct& a) {
     const int side = kTileRows[t];
     double cost;
     if (a.groups.offsets) {
-      // a group's last tile is half full on average, takes two thirds of a whole one's time and
-      // comes at the end, where it fills up what a round leaves over
+      // A group's last tile is half full on average and comes at the end, where it fills up what a
+      // round leaves over: 0.2 of a tile for each group, no whole rounds.  Us with 64 / 128 / 256 rows
+      // and columns, equal groups and then groups as a router leaves them, the rule's choice last:
+      //   4096 rows over  8,  512, depth 4096   43 /  45 /  76    59 /  47 /  77   64
+      //   4096 rows over  8, 2816, depth  768   76 /  30 /  26    79 /  37 /  29   128
+      //   4096 rows over 32, 2816, depth  768   80 /  36 /  46    99 /  52 /  46   256
+      //   8192 rows over 32,  512, depth 4096   83 /  51 /  78   104 /  58 /  79   128
+      //  32768 rows over 24,  768, depth 2816  397 / 194 / 163   403 / 198 / 174   256
+      //  32768 rows over 32,  512, depth 4096  414 / 173 / 138   434 / 211 / 221   256
+      // The host does not see the groups, so the choice is the average group's.  All 1024 rows at one
+      // of 32 experts (2816, depth 768) run on 32x128 tiles in 18.1 us, where 128x128 takes 11.8; half
+      // of 32768 rows at one of 32 (512, depth 4096) in 201 (equal groups 138).
       const double tiles_m = (double)a.rows / side + 0.2 * (double)stack;
       const double slots = side == 128 ? 512 : 256;
       const double share = std::max(1.0, tiles_m * (double)ceil64(a.cols, side) / slots);
@@ -751,7 +770,19 @@ bool multiple8(int64_t v) { return v % 8 == 0; }
 bool wide_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Tile side and splits of each group's rows: the least of the tiles' time (as above; the K-major
-// operands' slabs take 1.25 and 0.95 us) and the join's, which writes and reads each split's sums.
+// operands' slabs take 1.25 and 0.95 us, 0.62 where a CU has one 128x128 tile) and the join's, which
+// writes and reads each split's sums.  Us by side/splits, bias gradient included, the choice first:
+//     517 rows,  512 x 4096         128/1   13.3   256/1  22.8   128/2  18.1
+//    4096 rows,  768 x 2816         128/3   40.8   128/1  59.8   128/2  43.3   256/4 46.9   256/7 44.1
+//    4096 rows, 4096 x 4096         256/1  140.8   128/1 165.9   256/2 174.9
+//   32768 rows,  256 x 768          128/21  39.6   128/8  64.3   128/32 39.7   256/32 50.2
+//   32768 rows,  768 x 2816         256/7  167.3   128/7 201.2   256/4 224.8   256/8 229.1
+//   32768 rows,  512 x 4096         256/8  164.8   128/4 178.0   256/7 174.6   256/16 183.2
+//   32768 over 24, 768 x 2816       256/1  206.0   128/1 223.3   256/2 355.4
+//   32768 over 32, 512 x 4096       256/1  201.9   128/1 233.5   256/2 414.9
+//   32768 over  8, 256 x 768        128/5   39.2   128/1 113.5   128/4 42.1   256/4 67.7
+// Experts are split alike, by the average group's rows: with half of the 32768 rows at one expert the
+// two cases of 24 and 32 take 459 and 471, with all of them there 859 and 878.
 struct WeightPlan {
   int side, splits;
 };

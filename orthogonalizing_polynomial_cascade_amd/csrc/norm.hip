@@ -14,10 +14,23 @@
 // one workgroup of 256 lanes (up to 8192); longer rows are read again from memory for each step.
 // A wave walks over rows with weight and bias in registers and the next row on its way while it
 // works on this one.  In the backward pass it also keeps its columns' sums of dy h and dy; the
-// workgroup (one to a CU) joins its waves' sums in LDS and leaves one partial row, and a second
-// launch adds the partial rows in a fixed order (no atomics: the same bits on every run).
-// 65536 x 768 bf16: forward 36 us (5.6 TB/s), backward 59 us (5.1 TB/s; 78 us with a row to each
-// wave at a time and 1024 partial rows); 4096 x 8192: 24 and 53 us.
+// workgroup (one or two to a CU, see norm_grad_blocks) joins its waves' sums in LDS and leaves one
+// partial row, and a second launch adds the partial rows in a fixed order (no atomics: the same bits on
+// every run).  Times with that launch, us:
+//                     forward                backward
+//   65536 x 768  bf16  35.5 (5.7 TB/s)         58 (5.2 TB/s; 78 with a row to each wave at a time and
+//                                              1024 partial rows)
+//   65536 x 768  fp32  81   (5.0)             120 (5.0)
+//   16384 x 2048 bf16  23.4 (5.7)              42 (4.8)
+//   16384 x 2048 fp32  43.5 (6.2)             107 (3.8)
+//    4099 x 1601 fp16  13.1 (2.0)              31 (1.3)
+//    4096 x 8192 bf16  23.7 (5.7)              56 (3.6)
+//    4096 x 8192 fp32  43.7 (6.1)             138 (2.9)
+//    1000 x 20000 bf16 44   (1.8)              80 (1.5)
+// Four pieces of a row a lane (1025 to 2048 and 4097 to 8192 columns) are too many for the backward
+// pass: x, dy, h, g, the weight, two sums and the next row do not fit 256 registers, and the compiler
+// spills 22 to 167 of them with 16-bit types and 283 to 347 with fp32, which is what keeps these widths
+// further from the memory's rate than the others.
 #include <algorithm>
 
 #include "device_common.h"
@@ -256,7 +269,7 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormParams p) {
 // Backward pass in workgroups of LANES lanes, LANES / THREADS rows at a time; each workgroup leaves
 // its column sums in its partial row.
 // At least two waves a SIMD: with the 290 registers that the compiler takes for 2048 uneven columns
-// only one fits, and the 4099 x 1601 pass took 34 us instead of 24.
+// only one fits, and the 4099 x 1601 fp16 pass took 34 us instead of 24 with 111 of them spilled.
 template <typename T, int LANES, int THREADS, int CHUNKS, bool EVEN>
 __global__ __launch_bounds__(LANES) __attribute__((amdgpu_waves_per_eu(2)))
 void norm_grad_kernel(NormParams p) {

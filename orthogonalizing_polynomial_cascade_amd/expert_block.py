@@ -6,7 +6,8 @@ Forward, for rows sorted by expert:  h = norm(x);  y = x + relu2(h up_e^T + b_e)
 The weight gradients leave the backward pass as the [experts, hidden, width] gradient stacks of two
 banks, which anvil_bank_update orthogonalises and applies; the norm's weight and bias and the experts'
 biases take plain gradient steps.  The command fits a fixed random block of the same shape on random
-inputs and prints the loss.
+inputs.  What it minimises is the squared error summed over the columns and averaged over the rows; what
+it prints is the mean over both, smaller by the width.
 """
 from __future__ import annotations
 
@@ -80,7 +81,8 @@ def groups(rows, experts, seed):
 
 
 def train(steps=20, rows=4096, experts=8, width=256, hidden=768, seed=0):
-    """Fits a fixed random block; returns the mean squared error before each step."""
+    """Fits a fixed random block; returns the squared error before each step, averaged over rows and
+    columns (the gradients are those of its sum over the columns, which the vectors' plain steps see)."""
     import torch
     teacher, block = ExpertBlock(experts, width, hidden, seed + 1), ExpertBlock(experts, width, hidden, seed)
     losses = []
