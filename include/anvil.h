@@ -376,6 +376,43 @@ int anvil_expert_grad_weight(const void* dz, int64_t lddz, const void* x, int64_
                              int dw_dtype, float* dbias, int dtype, int64_t rows, int64_t n,
                              int64_t k, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated linear layer: z = x w^T + bias with w [2 n][k] (w_kn = 1: x w, w [k][2 n]),
+ *   y = act(z_gate) * z_up,  z_gate the first n columns of z and z_up the last n, in one kernel.
+ *   bias       [2 n] of bias_dtype (ANVIL_F32 or dtype), or NULL
+ *   y          [rows][n]
+ *   preact     receives z [rows][2 n] (rounded to dtype; y is formed from the unrounded z), or NULL
+ * w is a bank stack of two [n][k] matrices; its gradient and x's are those of a linear layer of width
+ * 2 n, from dz. */
+int anvil_gated_linear(const void* x, int64_t ldx, const void* w, int w_kn, const void* bias,
+                       int bias_dtype, int act, void* y, int64_t ldy, void* preact, int64_t ldz,
+                       int dtype, int64_t rows, int64_t n, int64_t k, void* stream);
+
+/* Its backward pass up to z, through the linear layer that y feeds: with h the gated layer's output
+ * [rows][k], input of a layer with weight w [n][k] (w_kn = 1: [k][n]) and output gradient dy [rows][n],
+ *   dh = dy w,  dz_gate = dh z_up act'(z_gate),  dz_up = dh act(z_gate).
+ *   preact     z [rows][2 k];  dz [rows][2 k] */
+int anvil_gated_grad_input(const void* dy, int64_t lddy, const void* w, int w_kn,
+                           const void* preact, int64_t ldz, int act, void* dz, int64_t lddz,
+                           int dtype, int64_t rows, int64_t n, int64_t k, void* stream);
+
+/* dz [rows][2 n] from the gradient dh [rows][n] of the gated layer's output itself, elementwise. */
+int anvil_gated_activation_grad(const void* dh, int64_t lddh, const void* preact, int64_t ldz,
+                                int act, void* dz, int64_t lddz, int dtype, int64_t rows, int64_t n,
+                                void* stream);
+
+/* The gated layer and its gradient for a stack of experts (w [experts][2 n][k], or [experts][k][2 n],
+ * and [experts][n][k] or [experts][k][n]; bias [experts][2 n]), offsets as above.  Rows without an
+ * expert get zeros in y, preact and dz. */
+int anvil_expert_gated_linear(const void* x, int64_t ldx, const void* w, int w_kn,
+                              const void* offsets, int offset_bits, int64_t experts,
+                              const void* bias, int bias_dtype, int act, void* y, int64_t ldy,
+                              void* preact, int64_t ldz, int dtype, int64_t rows, int64_t n,
+                              int64_t k, void* stream);
+int anvil_expert_gated_grad_input(const void* dy, int64_t lddy, const void* w, int w_kn,
+                                  const void* offsets, int offset_bits, int64_t experts,
+                                  const void* preact, int64_t ldz, int act, void* dz, int64_t lddz,
+                                  int dtype, int64_t rows, int64_t n, int64_t k, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -76,6 +76,16 @@ SIGNATURES = {
                                      _vp, _i64, _i, _i64, _i64, _i64, _vp]),
     "anvil_expert_grad_weight": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i, _i64, _vp, _i, _vp, _i,
                                       _i64, _i64, _i64, _vp, _sz, _vp]),
+    "anvil_gated_linear": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _i, _i64,
+                                _i64, _i64, _vp]),
+    "anvil_gated_grad_input": (_i, [_vp, _i64, _vp, _i, _vp, _i64, _i, _vp, _i64, _i, _i64, _i64,
+                                    _i64, _vp]),
+    "anvil_gated_activation_grad": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i64, _i, _i64, _i64,
+                                         _vp]),
+    "anvil_expert_gated_linear": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _i, _i, _vp, _i64,
+                                       _vp, _i64, _i, _i64, _i64, _i64, _vp]),
+    "anvil_expert_gated_grad_input": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _i64, _i, _vp,
+                                           _i64, _i, _i64, _i64, _i64, _vp]),
 }
 
 _lib = None
@@ -829,3 +839,102 @@ def anvil_expert_grad_weight(dz, x, offsets, w_kn=False, out=None, out_dtype=Non
     stack of the experts' bank, and dbias [experts, n]."""
     return _grad_weight("anvil_expert_grad_weight", dz, x, offsets, w_kn, out, out_dtype, want_bias,
                         workspace, stream)
+
+
+def _gated(fn, x, w, offsets, bias, act, w_kn, keep_preact, preact, out, stream):
+    device = _device(x, "x")
+    code = _code(x, "x", _SIXTEEN)
+    dtype = x.dtype
+    rows, k, ldx = _rows(x, "x")
+    group = () if offsets is None else _offsets(offsets, device)
+    experts = group[2] if group else None
+    wp, both, wk = _weight(w, dtype, device, w_kn, experts)
+    if k != wk:
+        raise ValueError(f"x has width {k}, w takes {wk}")
+    if both % 2:
+        raise ValueError(f"w gives {both} columns: a gated layer has two halves of equal width")
+    n = both // 2
+    b, b_code = _parameter(bias, "bias", code, x, device,
+                           (both,) if experts is None else (experts, both))
+    if out is None:
+        out = _empty((rows, n), dtype, x.device, stream)
+    y, ldy = _operand(out, "out", dtype, device, rows, n)
+    if preact is None and keep_preact:
+        preact = _empty((rows, both), dtype, x.device, stream)
+    z, ldz = _operand(preact, "preact", dtype, device, rows, both)
+    status = getattr(load(), fn)(x.data_ptr(), ldx, wp, 1 if w_kn else 0, *group, b, b_code,
+                                 _act(act), y, ldy, z, ldz, code, rows, n, k,
+                                 _raw_stream(stream, device))
+    if status:
+        _check(fn, status)
+    return out, preact
+
+
+def _gated_grad(fn, dy, w, offsets, preact, act, w_kn, out, stream):
+    device = _device(dy, "dy")
+    code = _code(dy, "dy", _SIXTEEN)
+    dtype = dy.dtype
+    rows, n, lddy = _rows(dy, "dy")
+    group = () if offsets is None else _offsets(offsets, device)
+    wp, wn, k = _weight(w, dtype, device, w_kn, group[2] if group else None)
+    if n != wn:
+        raise ValueError(f"dy has width {n}, w gives {wn}")
+    z, ldz = _operand(preact, "preact", dtype, device, rows, 2 * k)
+    if z is None:
+        raise ValueError("preact must be given")
+    if out is None:
+        out = _empty((rows, 2 * k), dtype, dy.device, stream)
+    dz, lddz = _operand(out, "out", dtype, device, rows, 2 * k)
+    status = getattr(load(), fn)(dy.data_ptr(), lddy, wp, 1 if w_kn else 0, *group, z, ldz, _act(act),
+                                 dz, lddz, code, rows, n, k, _raw_stream(stream, device))
+    if status:
+        _check(fn, status)
+    return out
+
+
+def anvil_gated_linear(x, w, bias=None, act="silu", w_kn=False, keep_preact=False, preact=None,
+                       out=None, stream=None):
+    """Gated linear layer y = act(z_gate) * z_up, where z = x w^T + bias has z_gate in its first n columns
+    and z_up in its last n: w [2n, k] (w_kn: x w, w [k, 2n]), x bf16 or fp16 [rows, k], bias [2n] fp32 or
+    of x's dtype.  Returns (y [rows, n], z), z [rows, 2n] where keep_preact asks for it or `preact`
+    receives it, else None.  The gradients of x and w are anvil_linear_grad_input's and
+    anvil_linear_grad_weight's, from dz."""
+    return _gated("anvil_gated_linear", x, w, None, bias, act, w_kn, keep_preact, preact, out, stream)
+
+
+def anvil_gated_grad_input(dy, w, preact, act="silu", w_kn=False, out=None, stream=None):
+    """dz [rows, 2k] of a gated layer's z (`preact`) from the gradient dy [rows, n] of the linear layer that
+    its output h feeds, y = h w^T with w [n, k] (w_kn: y = h w, w [k, n])."""
+    return _gated_grad("anvil_gated_grad_input", dy, w, None, preact, act, w_kn, out, stream)
+
+
+def anvil_gated_activation_grad(dh, preact, act="silu", out=None, stream=None):
+    """dz [rows, 2n] of a gated layer's z (`preact`) from the gradient dh [rows, n] of its output."""
+    device = _device(dh, "dh")
+    code = _code(dh, "dh", _SIXTEEN)
+    rows, n, lddh = _rows(dh, "dh")
+    z, ldz = _operand(preact, "preact", dh.dtype, device, rows, 2 * n)
+    if z is None:
+        raise ValueError("preact must be given")
+    if out is None:
+        out = _empty((rows, 2 * n), dh.dtype, dh.device, stream)
+    dz, lddz = _operand(out, "out", dh.dtype, device, rows, 2 * n)
+    status = load().anvil_gated_activation_grad(dh.data_ptr(), lddh, z, ldz, _act(act), dz, lddz, code,
+                                                rows, n, _raw_stream(stream, device))
+    if status:
+        _check("anvil_gated_activation_grad", status)
+    return out
+
+
+def anvil_expert_gated_linear(x, w, offsets, bias=None, act="silu", w_kn=False, keep_preact=False,
+                              preact=None, out=None, stream=None):
+    """anvil_gated_linear for a stack of experts (w [experts, 2n, k], bias [experts, 2n]) over the groups of
+    rows that offsets give, as in anvil_expert_linear."""
+    return _gated("anvil_expert_gated_linear", x, w, offsets, bias, act, w_kn, keep_preact, preact, out,
+                  stream)
+
+
+def anvil_expert_gated_grad_input(dy, w, offsets, preact, act="silu", w_kn=False, out=None,
+                                  stream=None):
+    """anvil_gated_grad_input over the experts' groups of rows (w [experts, n, k])."""
+    return _gated_grad("anvil_expert_gated_grad_input", dy, w, offsets, preact, act, w_kn, out, stream)

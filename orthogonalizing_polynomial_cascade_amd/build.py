@@ -11,13 +11,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libanvil.so")
 SOURCES = ["momentum.hip", "gemm.hip", "normalize.hip", "update.hip", "api.hip", "norm.hip",
-           "linear.hip", "linear_tiles.hip", "train_api.hip"]
+           "linear.hip", "linear_tiles.hip", "gated.hip", "train_api.hip"]
 ARCH = "gfx950"
 
 
@@ -29,7 +31,7 @@ def hipcc() -> str:
 
 def flags() -> list:
     return [
-        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
         "-ffp-contract=off",
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-I", os.path.join(ROOT, "include"),
@@ -42,19 +44,33 @@ def flags() -> list:
 def build(verbose: bool = False) -> str:
     """Compile every source into libanvil.so (always recompiles).  Returns the library path."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + flags() + [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    with tempfile.TemporaryDirectory() as work:
+        def compile_one(source):
+            out = os.path.join(work, source + ".o")
+            cmd = [hipcc()] + flags() + ["-c", os.path.join(CSRC, source), "-o", out]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            return out, subprocess.run(cmd, capture_output=True, text=True)
+
+        # the sources are independent of each other: one compiler for each, up to the CPUs given
+        jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", 0)) or os.cpu_count() or 1, 16)
+        with ThreadPoolExecutor(jobs) as pool:
+            done = list(pool.map(compile_one, SOURCES))
+        _report([r for _, r in done], verbose)
+        link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC"] + [o for o, _ in done] + ["-o", tmp]
+        _report([subprocess.run(link, capture_output=True, text=True)], verbose)
+    os.replace(tmp, LIB)
+    return LIB
+
+
+def _report(runs, verbose):
     # hipcc's host pass does not know the packed-fp32 feature and says so; that is harmless
     noise = "is not a recognized feature for this target"
-    msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l and l.strip()]
-    if r.returncode != 0:
+    msgs = [l for r in runs for l in (r.stdout + r.stderr).splitlines() if noise not in l and l.strip()]
+    if any(r.returncode != 0 for r in runs):
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
-    os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

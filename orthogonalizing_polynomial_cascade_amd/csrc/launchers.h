@@ -123,6 +123,16 @@ struct RowsProduct {
 };
 hipError_t launch_rows_product(const RowsProduct& a, hipStream_t stream);
 
+// Gated linear layer: the product has 2 cols columns, z = sum + bias, of which column c and column
+// cols + c give out[r][c] = act(z[r][c]) * z[r][cols + c]; keep receives z [rows][2 cols].  (b is
+// [groups][2 cols][depth], or [groups][depth][2 cols]; aux, add and gradient are not used.)
+hipError_t launch_gated_product(const RowsProduct& a, hipStream_t stream);
+// Its gradient through the layer that follows: with s = sum_d a[r][d] b(c, d) and z = aux [rows][2 cols],
+// out[r][c] = s * z[r][cols + c] * act'(z[r][c]) and out[r][cols + c] = s * act(z[r][c]).
+hipError_t launch_gated_grad(const RowsProduct& a, hipStream_t stream);
+// The same with s = a [rows][cols].
+hipError_t launch_gated_activation_grad(const RowsProduct& a, hipStream_t stream);
+
 // dw[e][i][j] = sum over the rows r of group e of p[r][i] * q[r][j], and the column sums of
 // whichever of the two is dz.
 struct WeightProduct {

@@ -9,6 +9,8 @@
 
 namespace anvil {
 
+inline int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 template <typename T>
 struct Mfma;
 template <>

@@ -244,6 +244,84 @@ int weight_backward(const void* dz, int64_t lddz, const void* x, int64_t ldx, in
                                                  static_cast<hipStream_t>(stream)));
 }
 
+// Gated linear layers: n columns of h, 2 n of the weight and of z.
+int gated_forward(const void* x, int64_t ldx, const void* w, int w_kn, const GroupIn& g,
+                  bool grouped, const void* bias, int bias_dtype, int act, void* y, int64_t ldy,
+                  void* preact, int64_t ldz, int dtype, int64_t rows, int64_t n, int64_t k,
+                  void* stream) {
+  if (n > kMaxWidth / 2) return ANVIL_ERR_UNSUPPORTED;
+  int st = check_sizes(dtype, g, grouped, rows, n < 0 ? n : 2 * n, k);
+  if (st != ANVIL_OK) return st;
+  if ((w_kn != 0 && w_kn != 1) || !act_known(act)) return ANVIL_ERR_INVALID_ARG;
+  if (bias && bias_dtype != ANVIL_F32 && bias_dtype != dtype) return ANVIL_ERR_INVALID_ARG;
+  if (rows == 0 || n == 0) return ANVIL_OK;
+  const int64_t count = grouped ? g.count : 1;
+  if (grouped && !g.offsets) return ANVIL_ERR_INVALID_ARG;
+  if (!y || (k > 0 && !x) || (k > 0 && count > 0 && !w)) return ANVIL_ERR_INVALID_ARG;
+  if (!take_pitch(x, &ldx, k, rows) || !take_pitch(y, &ldy, n, rows) ||
+      !take_pitch(preact, &ldz, 2 * n, rows))
+    return ANVIL_ERR_UNSUPPORTED;
+  const int eb = elem_bytes(dtype);
+  if (!aligned(x, eb) || !aligned(w, eb) || !aligned(y, eb) || !aligned(preact, eb) ||
+      !aligned(bias, bias ? elem_bytes(bias_dtype) : 1))
+    return ANVIL_ERR_MISALIGNED;
+  st = check_views({{x, rows, k * eb, ldx * eb, false},
+                    dense(w, count * 2 * n * k * eb, false),
+                    dense(bias, bias ? count * 2 * n * elem_bytes(bias_dtype) : 0, false),
+                    {y, rows, n * eb, ldy * eb, true},
+                    {preact, rows, 2 * n * eb, ldz * eb, true},
+                    offsets_view(g)});
+  if (st != ANVIL_OK) return st;
+  anvil::RowsProduct a{};
+  a.a = x; a.lda = ldx; a.b = w; a.b_kmajor = w_kn != 0;
+  a.rows = rows; a.cols = static_cast<int>(n); a.depth = static_cast<int>(k);
+  a.groups = groups_of(g, grouped);
+  a.f16 = dtype == ANVIL_F16;
+  a.act = act;
+  a.bias = bias; a.bias_f32 = bias && bias_dtype == ANVIL_F32;
+  a.keep = preact; a.ldkeep = ldz;
+  a.out = y; a.ldout = ldy;
+  return hip_status(anvil::launch_gated_product(a, static_cast<hipStream_t>(stream)));
+}
+
+// dz [rows][2 k] from dy [rows][n] of the layer w that h [rows][k] feeds, or (no w) from dh itself.
+int gated_backward(const void* dy, int64_t lddy, const void* w, bool has_w, int w_kn,
+                   const GroupIn& g, bool grouped, const void* preact, int64_t ldz, int act,
+                   void* dz, int64_t lddz, int dtype, int64_t rows, int64_t n, int64_t k,
+                   void* stream) {
+  if (k > kMaxWidth / 2) return ANVIL_ERR_UNSUPPORTED;
+  int st = check_sizes(dtype, g, grouped, rows, has_w ? n : 0, k);
+  if (st != ANVIL_OK) return st;
+  if ((w_kn != 0 && w_kn != 1) || !act_known(act)) return ANVIL_ERR_INVALID_ARG;
+  if (rows == 0 || k == 0) return ANVIL_OK;
+  const int64_t count = grouped ? g.count : 1;
+  if (grouped && !g.offsets) return ANVIL_ERR_INVALID_ARG;
+  if (!dz || !preact || (n > 0 && !dy) || (has_w && n > 0 && count > 0 && !w))
+    return ANVIL_ERR_INVALID_ARG;
+  if (!take_pitch(dy, &lddy, n, rows) || !take_pitch(dz, &lddz, 2 * k, rows) ||
+      !take_pitch(preact, &ldz, 2 * k, rows))
+    return ANVIL_ERR_UNSUPPORTED;
+  const int eb = elem_bytes(dtype);
+  if (!aligned(dy, eb) || !aligned(w, eb) || !aligned(dz, eb) || !aligned(preact, eb))
+    return ANVIL_ERR_MISALIGNED;
+  st = check_views({{dy, rows, n * eb, lddy * eb, false},
+                    dense(w, w ? count * n * k * eb : 0, false),
+                    {preact, rows, 2 * k * eb, ldz * eb, false},
+                    {dz, rows, 2 * k * eb, lddz * eb, true},
+                    offsets_view(g)});
+  if (st != ANVIL_OK) return st;
+  anvil::RowsProduct a{};
+  a.a = dy; a.lda = lddy; a.b = w; a.b_kmajor = w_kn == 0;   // as rows_backward
+  a.rows = rows; a.cols = static_cast<int>(k); a.depth = static_cast<int>(n);
+  a.groups = groups_of(g, grouped);
+  a.f16 = dtype == ANVIL_F16;
+  a.act = act;
+  a.aux = preact; a.ldaux = ldz;
+  a.out = dz; a.ldout = lddz;
+  return hip_status(has_w ? anvil::launch_gated_grad(a, static_cast<hipStream_t>(stream))
+                          : anvil::launch_gated_activation_grad(a, static_cast<hipStream_t>(stream)));
+}
+
 constexpr GroupIn kNoGroups{nullptr, 32, 1};
 
 // ------------------------------------------------------------------------------------------
@@ -412,6 +490,44 @@ int anvil_activation_grad(const void* dy, int64_t lddy, const void* preact, int6
   return hip_status(anvil::launch_activation_grad(dy, lddy, preact, ldz, act, dz, lddz,
                                                   dtype == ANVIL_F16, rows, static_cast<int>(n),
                                                   static_cast<hipStream_t>(stream)));
+}
+
+int anvil_gated_linear(const void* x, int64_t ldx, const void* w, int w_kn, const void* bias,
+                       int bias_dtype, int act, void* y, int64_t ldy, void* preact, int64_t ldz,
+                       int dtype, int64_t rows, int64_t n, int64_t k, void* stream) {
+  return gated_forward(x, ldx, w, w_kn, kNoGroups, false, bias, bias_dtype, act, y, ldy, preact,
+                       ldz, dtype, rows, n, k, stream);
+}
+
+int anvil_gated_grad_input(const void* dy, int64_t lddy, const void* w, int w_kn,
+                           const void* preact, int64_t ldz, int act, void* dz, int64_t lddz,
+                           int dtype, int64_t rows, int64_t n, int64_t k, void* stream) {
+  return gated_backward(dy, lddy, w, true, w_kn, kNoGroups, false, preact, ldz, act, dz, lddz, dtype,
+                        rows, n, k, stream);
+}
+
+int anvil_gated_activation_grad(const void* dh, int64_t lddh, const void* preact, int64_t ldz,
+                                int act, void* dz, int64_t lddz, int dtype, int64_t rows, int64_t n,
+                                void* stream) {
+  return gated_backward(dh, lddh, nullptr, false, 0, kNoGroups, false, preact, ldz, act, dz, lddz,
+                        dtype, rows, n, n, stream);
+}
+
+int anvil_expert_gated_linear(const void* x, int64_t ldx, const void* w, int w_kn,
+                              const void* offsets, int offset_bits, int64_t experts,
+                              const void* bias, int bias_dtype, int act, void* y, int64_t ldy,
+                              void* preact, int64_t ldz, int dtype, int64_t rows, int64_t n,
+                              int64_t k, void* stream) {
+  return gated_forward(x, ldx, w, w_kn, {offsets, offset_bits, experts}, true, bias, bias_dtype, act,
+                       y, ldy, preact, ldz, dtype, rows, n, k, stream);
+}
+
+int anvil_expert_gated_grad_input(const void* dy, int64_t lddy, const void* w, int w_kn,
+                                  const void* offsets, int offset_bits, int64_t experts,
+                                  const void* preact, int64_t ldz, int act, void* dz, int64_t lddz,
+                                  int dtype, int64_t rows, int64_t n, int64_t k, void* stream) {
+  return gated_backward(dy, lddy, w, true, w_kn, {offsets, offset_bits, experts}, true, preact, ldz,
+                        act, dz, lddz, dtype, rows, n, k, stream);
 }
 
 }  // extern "C"
