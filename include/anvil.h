@@ -413,6 +413,43 @@ int anvil_expert_gated_grad_input(const void* dy, int64_t lddy, const void* w, i
                                   const void* preact, int64_t ldz, int act, void* dz, int64_t lddz,
                                   int dtype, int64_t rows, int64_t n, int64_t k, void* stream);
 
+/* Cross entropy of a linear head over a vocabulary, the logits s = x w^T never stored:
+ *   lse[r] = log(sum over v of exp(s[r][v])),  loss[r] = lse[r] - s[r][targets[r]].
+ *   x          dtype (ANVIL_BF16 or ANVIL_F16) [rows][k] at pitch ldx
+ *   w          dtype [vocab][k] (w_kn = 0) or [k][vocab] (w_kn = 1)
+ *   targets    DEVICE integers [rows] of target_bits (32 or 64); a row whose target is outside
+ *              0 .. vocab - 1 is ignored: its loss is 0 and it has no gradient, whatever its x and
+ *              dloss hold (but where dw is taken its x has to be finite: its P is 0, and 0 * inf is NaN)
+ *   loss, lse  fp32 [rows]
+ *   workspace  anvil_cross_entropy_workspace bytes; in_place: ANVIL_X_IN_PLACE where x is 16-byte
+ *              aligned and ldx (k for a single row) a multiple of 8, plus ANVIL_W_IN_PLACE where w is
+ *              16-byte aligned.  What is not, or has a row of another length than a multiple of 8, is
+ *              copied there first, and it is larger.
+ * rows <= 2^24, 1 <= vocab <= 2^22, vocab * k <= 2^30, rows * vocab and rows * k <= 2^37. */
+enum anvil_in_place { ANVIL_X_IN_PLACE = 1, ANVIL_W_IN_PLACE = 2 };
+int anvil_cross_entropy(const void* x, int64_t ldx, const void* w, int w_kn, const void* targets,
+                        int target_bits, float* loss, float* lse, int dtype, int64_t rows,
+                        int64_t vocab, int64_t k, void* workspace, size_t workspace_bytes,
+                        void* stream);
+size_t anvil_cross_entropy_workspace(int w_kn, int in_place, int64_t rows, int64_t vocab, int64_t k);
+
+/* Its gradients, with P[r][v] = (exp(s[r][v] - lse[r]) - [v = targets[r]]) dloss[r]:
+ *   dx = P w,  dw = P^T x (w_kn = 1: x^T P).
+ *   lse        fp32 [rows], from anvil_cross_entropy
+ *   dloss      fp32 [rows]: the gradient that reaches each row's loss (1 / rows for their mean)
+ *   dx         dtype [rows][k], dw of dw_dtype (ANVIL_F32 or dtype) as w; each may be NULL
+ *   workspace  anvil_cross_entropy_grad_workspace bytes (want_dx, want_dw: whether dx, dw are given)
+ * P is formed by pieces of the vocabulary and rounded to dtype (fp16: scaled by a power of two first) for
+ * the two products, whose sums are fp32: dw in fp32 holds the sums of the rounded P.  dw is zeros when
+ * there are no rows. */
+int anvil_cross_entropy_grad(const void* x, int64_t ldx, const void* w, int w_kn, const void* targets,
+                             int target_bits, const float* lse, const float* dloss, void* dx,
+                             int64_t lddx, void* dw, int dw_dtype, int dtype, int64_t rows,
+                             int64_t vocab, int64_t k, void* workspace, size_t workspace_bytes,
+                             void* stream);
+size_t anvil_cross_entropy_grad_workspace(int want_dx, int want_dw, int w_kn, int in_place, int dtype,
+                                          int64_t rows, int64_t vocab, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

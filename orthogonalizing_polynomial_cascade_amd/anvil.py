@@ -86,6 +86,12 @@ SIGNATURES = {
                                        _vp, _i64, _i, _i64, _i64, _i64, _vp]),
     "anvil_expert_gated_grad_input": (_i, [_vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _i64, _i, _vp,
                                            _i64, _i, _i64, _i64, _i64, _vp]),
+    "anvil_cross_entropy": (_i, [_vp, _i64, _vp, _i, _vp, _i, _vp, _vp, _i, _i64, _i64, _i64, _vp,
+                                 _sz, _vp]),
+    "anvil_cross_entropy_workspace": (_sz, [_i, _i, _i64, _i64, _i64]),
+    "anvil_cross_entropy_grad": (_i, [_vp, _i64, _vp, _i, _vp, _i, _vp, _vp, _vp, _i64, _vp, _i, _i,
+                                      _i64, _i64, _i64, _vp, _sz, _vp]),
+    "anvil_cross_entropy_grad_workspace": (_sz, [_i, _i, _i, _i, _i, _i64, _i64, _i64]),
 }
 
 _lib = None
@@ -938,3 +944,79 @@ def anvil_expert_gated_grad_input(dy, w, offsets, preact, act="silu", w_kn=False
                                   stream=None):
     """anvil_gated_grad_input over the experts' groups of rows (w [experts, n, k])."""
     return _gated_grad("anvil_expert_gated_grad_input", dy, w, offsets, preact, act, w_kn, out, stream)
+
+
+def _head(x, w, targets, w_kn):
+    """Checked operands of the head: (device, dtype code, rows, k, ldx, w, vocab, targets, target bits, which of
+    x (1) and w (2) are read where they lie)."""
+    device = _device(x, "x")
+    code = _code(x, "x", _SIXTEEN)
+    rows, k, ldx = _rows(x, "x")
+    wp, vocab, wk = _weight(w, x.dtype, device, w_kn, None)
+    if k != wk:
+        raise ValueError(f"x has width {k}, w takes {wk}")
+    if vocab == 0:
+        raise ValueError("w must have an entry")
+    if not isinstance(targets, _torch.Tensor):
+        raise TypeError("targets must be a torch.Tensor")
+    if targets.dtype not in (_torch.int32, _torch.int64):
+        raise TypeError("targets must be int32 or int64")
+    tp = _dense(targets, "targets", targets.dtype, device, (rows,))
+    pitch = k if rows <= 1 else ldx
+    in_place = (1 if x.data_ptr() % 16 == 0 and pitch % 8 == 0 else 0) | (2 if wp % 16 == 0 else 0)
+    return (device, code, rows, k, ldx, wp, vocab, tp, 32 if targets.dtype == _torch.int32 else 64,
+            in_place)
+
+
+def anvil_cross_entropy(x, w, targets, w_kn=False, workspace=None, stream=None):
+    """Cross entropy of the linear head s = x w^T (w [vocab, k]; w_kn: s = x w, w [k, vocab]) for each row of
+    x (bf16 or fp16 [rows, k]) and its target (int32 or int64 [rows]).  Returns (loss, lse), both fp32 [rows];
+    the logits are never stored.  A row whose target is outside 0 .. vocab - 1 is ignored: loss 0, no
+    gradient (for dw its x has to be finite all the same)."""
+    device, code, rows, k, ldx, wp, vocab, tp, bits, in_place = _head(x, w, targets, w_kn)
+    both = _empty((2, rows), _torch.float32, x.device, stream)
+    loss, lse = both.unbind()
+    at = both.data_ptr()
+    lib = load()
+    ws = _scratch(workspace, lib.anvil_cross_entropy_workspace(1 if w_kn else 0, in_place, rows, vocab, k),
+                  device, stream)
+    status = lib.anvil_cross_entropy(
+        x.data_ptr(), ldx, wp, 1 if w_kn else 0, tp, bits, at, at + 4 * rows, code, rows, vocab, k,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _raw_stream(stream, device))
+    if status:
+        _check("anvil_cross_entropy", status)
+    return loss, lse
+
+
+def anvil_cross_entropy_grad(x, w, targets, lse, dloss, w_kn=False, out=None, dw_out=None, out_dtype=None,
+                             want_input=True, want_weight=True, workspace=None, stream=None):
+    """(dx, dw) of anvil_cross_entropy from its lse and the gradient dloss (fp32 [rows]) of each row's loss.
+    dx has x's dtype, dw w's shape and out_dtype (by default x's dtype; fp32 holds the sums of probabilities
+    that were rounded to x's dtype).  Without want_input or want_weight that one is None."""
+    device, code, rows, k, ldx, wp, vocab, tp, bits, in_place = _head(x, w, targets, w_kn)
+    lp = _dense(lse, "lse", _torch.float32, device, (rows,))
+    gp = _dense(dloss, "dloss", _torch.float32, device, (rows,))
+    if want_input:
+        if out is None:
+            out = _empty((rows, k), x.dtype, x.device, stream)
+        dx, lddx = _operand(out, "out", x.dtype, device, rows, k)
+    else:
+        out, dx, lddx = None, None, 0
+    if want_weight:
+        if dw_out is None:
+            dw_out = _empty(tuple(w.shape), out_dtype or x.dtype, x.device, stream)
+        dw, dw_code = _parameter(dw_out, "dw_out", code, x, device, tuple(w.shape))
+    else:
+        dw_out, dw, dw_code = None, None, code
+    lib = load()
+    need = lib.anvil_cross_entropy_grad_workspace(int(want_input), int(want_weight), 1 if w_kn else 0,
+                                                  in_place, code, rows, vocab, k)
+    ws = _scratch(workspace, need, device, stream)
+    status = lib.anvil_cross_entropy_grad(
+        x.data_ptr(), ldx, wp, 1 if w_kn else 0, tp, bits, lp, gp, dx, lddx, dw, dw_code, code, rows, vocab,
+        k, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _raw_stream(stream, device))
+    if status:
+        _check("anvil_cross_entropy_grad", status)
+    return out, dw_out

@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libanvil.so")
 SOURCES = ["momentum.hip", "gemm.hip", "normalize.hip", "update.hip", "api.hip", "norm.hip",
-           "linear.hip", "linear_tiles.hip", "gated.hip", "train_api.hip"]
+           "linear.hip", "linear_tiles.hip", "gated.hip", "cross_entropy.hip",
+           "cross_entropy_grad.hip", "train_api.hip", "head_api.hip"]
 ARCH = "gfx950"
 
 

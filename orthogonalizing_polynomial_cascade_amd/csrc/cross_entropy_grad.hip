@@ -1,0 +1,480 @@
+// Gradients of the linear head's cross entropy, and the calls of both directions.
+//
+// With P = (softmax(x W^T) - onehot) dloss:  dx = P W,  dW = P^T x.  P is formed for a piece of the
+// vocabulary at a time (cross_entropy.hip), rounded to the operands' type as the matrix cores take it, and
+// both products read it: dW of the piece is complete, dx is summed over the pieces in fp32.  An fp16 P is
+// scaled by a power of two so that the largest |dloss| comes to 2^14 (a mean over 16384 rows alone would push
+// probabilities below 2^-10 under fp16's range); the products are scaled back in fp32, exactly.  The
+// rounding of P is each element's own, at most half a step of its type: it adds to a sum of many of them
+// what the roundings of the inputs already did.
+//
+// Operands whose widths or addresses the copies into LDS cannot take (multiples of 8, 16 bytes) are packed
+// into the workspace once, with zeros to the next multiple of 8.
+#include <algorithm>
+#include <atomic>
+
+#include "cross_entropy.h"
+#include "tile_pipe.h"
+
+namespace anvil {
+
+namespace {
+
+int64_t ceil8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// to [rows][pitch] = from [rows][width] at ld, zeros from width to pitch.  16-bit elements.
+__global__ __launch_bounds__(256) void head_pack_kernel(const uint16_t* from, int64_t ld,
+                                                        int64_t rows, int64_t width, uint16_t* to,
+                                                        int64_t pitch) {
+  const int64_t pieces = pitch / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pieces;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / pieces, c = i % pieces * 8;
+    const uint16_t* at = from + r * ld + c;
+    uint16_t v[8];
+    if (c + 8 <= width) {
+      __builtin_memcpy(v, at, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = c + e < width ? at[e] : (uint16_t)0;
+    }
+    __builtin_memcpy(to + r * pitch + c, v, 16);
+  }
+}
+
+// scale = {S, 1 / S}: S the power of two that takes the largest finite |dloss| to [2^14, 2^15).
+__global__ __launch_bounds__(1024) void head_scale_kernel(const float* dloss, int64_t rows,
+                                                          float* scale) {
+  __shared__ float wave_top[16];
+  float top = 0.0f;
+  for (int64_t r = threadIdx.x; r < rows; r += 1024) {
+    const float v = fabsf(dloss[r]);
+    if (v > top && v < INFINITY) top = v;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, wave_top[i]);
+    int power = 0;
+    if (top > 0.0f) {
+      frexpf(top, &power);                       // top in [2^(power - 1), 2^power)
+      power = min(max(15 - power, -120), 120);   // S and 1 / S stay normal numbers
+    }
+    scale[0] = ldexpf(1.0f, power);
+    scale[1] = ldexpf(1.0f, -power);
+  }
+}
+
+// One piece's part of dx.
+struct InputGrad {
+  const void* p;         // [rows][ldp], columns up to `depth`
+  int64_t ldp;
+  const void* w;         // of the piece's first entry
+  int64_t ldw;
+  int64_t rows;
+  int cols, depth;       // width of x, entries of the piece
+  float* sum;            // [rows][ldsum] fp32, when there are several pieces
+  int64_t ldsum;
+  bool first, last;
+  const float* scale;    // or null
+  void* out;
+  int64_t ldout;
+};
+
+template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
+__global__ __launch_bounds__(WM * WN * KS * 64)
+__attribute__((amdgpu_waves_per_eu(OCC)))
+void head_input_kernel(InputGrad p, int tiles_n) {
+  using C = Tile<BM, BN, WM, WN, KS>;
+  using S = OutStage<C::kWTN>;
+  static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
+  extern __shared__ __attribute__((aligned(1024))) char smem_all[];
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int kg = wave_all / C::kWaves;
+  const int wave = wave_all % C::kWaves;
+  char* smem = smem_all + kg * C::kRing;
+  int64_t row0, end;
+  int group, tj;
+  if (!rows_place<BM>(Groups{nullptr, false, 1}, p.rows, tiles_n, &row0, &end, &group, &tj)) return;
+  const int j0 = tj * BN;
+  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (QT ? (int64_t)j0 : j0 * p.ldw);
+  f32x16_t acc[C::kFM][C::kFN];
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+  float none;
+  Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
+  pipe.begin(static_cast<const uint16_t*>(p.p) + row0 * p.ldp, p.ldp, end - row0, w, p.ldw,
+             p.cols - j0, p.depth, kg);
+  const int wm = wave / WN, wn = wave % WN;
+  const bool idle = row0 + wm * C::kWTM >= end;
+  if (idle) pipe.attend();
+  else pipe.template run<false>(acc, 0, none);
+  if constexpr (KS > 1) {
+    pipe.merge(kg, acc);
+    if (kg > 0) return;
+  }
+  if (idle) return;
+  char* stage = pipe.spare() + wave * S::kBytes;
+  const int c = j0 + wn * C::kWTN + S::col(lane);
+  const int64_t first = row0 + wm * C::kWTM + S::row(0, lane);
+  const int rows = c < p.cols ? (int)min(end - first, (int64_t)C::kWTM) : 0;
+  float* sum = p.sum + first * p.ldsum + c;
+  T* out = static_cast<T*>(p.out) + first * p.ldout + c;
+  const float back = p.scale ? p.scale[1] : 1.0f;
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm) {
+    S::put(stage, acc[fm], lane);
+#pragma unroll
+    for (int i = 0; i < S::kPasses; ++i) {
+      const int r = fm * 32 + i * S::kRows;
+      float v[8];
+      S::get(stage, i, lane, v);
+      if (r >= rows) continue;
+      if (!p.first) {
+        float before[8];
+        load_vec<float, 8>(sum + r * p.ldsum, before);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += before[e];
+      }
+      if (!p.last) {
+        store_vec<float, 8>(sum + r * p.ldsum, v);   // the pitch is a multiple of 8
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= back;
+      if (c + 8 <= p.cols) {
+        store_vec<T, 8>(out + r * p.ldout, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < p.cols) out[r * p.ldout + e] = from_f32<T>(v[e]);
+      }
+    }
+  }
+}
+
+// dW of one piece: out[i][j] = sum_r p[r][i] q[r][j], one of the two P and the other x.
+struct WeightGrad {
+  const void* p;
+  int64_t ldp;
+  const void* q;
+  int64_t ldq;
+  int64_t rows;
+  int ni, nj;
+  int splits;            // parts of the rows; with several, sums go to planes [splits][ni][ceil8(nj)]
+  float* planes;
+  const float* scale;
+  void* out;
+  int64_t ldout;
+  bool out_f32;
+};
+
+// Eight sums (columns j .. j + 7) to the output, scaled back.
+template <typename T>
+__device__ __forceinline__ void weight_out(const WeightGrad& p, int64_t i, int j, float back,
+                                           float v[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= back;
+  const int64_t at = i * p.ldout + j;
+  if (j + 8 <= p.nj) {
+    if (p.out_f32) store_vec<float, 8>(static_cast<float*>(p.out) + at, v);
+    else store_vec<T, 8>(static_cast<T*>(p.out) + at, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (j + e >= p.nj) break;
+    if (p.out_f32) static_cast<float*>(p.out)[at + e] = v[e];
+    else static_cast<T*>(p.out)[at + e] = from_f32<T>(v[e]);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(WM * WN * 64)
+__attribute__((amdgpu_waves_per_eu(OCC)))
+void head_weight_kernel(WeightGrad p, int tiles_i, int tiles_j) {
+  using C = Tile<BM, BN, WM, WN, 1>;
+  using S = OutStage<C::kWTN>;
+  static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int unit = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int s = unit / (tiles_i * tiles_j);
+  int ti, tj;
+  banded(unit % (tiles_i * tiles_j), tiles_i, tiles_j, &ti, &tj);
+  const int i0 = ti * BM, j0 = tj * BN;
+  const int64_t part = ((p.rows + kBK - 1) / kBK + p.splits - 1) / p.splits * kBK;
+  const int64_t k0 = min(s * part, p.rows), k1 = min(k0 + part, p.rows);
+  f32x16_t acc[C::kFM][C::kFN];
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+  float none;
+  Pipe<T, true, true, BM, BN, WM, WN, 1> pipe(smem, wave);
+  pipe.begin(static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.ni - i0,
+             static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.nj - j0, k1 - k0, 0);
+  pipe.template run<false>(acc, 0, none);
+  const int wm = wave / WN, wn = wave % WN;
+  char* stage = pipe.spare() + wave * S::kBytes;
+  const int j = j0 + wn * C::kWTN + S::col(lane);
+  const int64_t pitch = (p.nj + 7) / 8 * 8;
+  const float back = p.scale ? p.scale[1] : 1.0f;
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm) {
+    S::put(stage, acc[fm], lane);
+#pragma unroll
+    for (int k = 0; k < S::kPasses; ++k) {
+      const int i = i0 + wm * C::kWTM + fm * 32 + S::row(k, lane);
+      float v[8];
+      S::get(stage, k, lane, v);
+      if (i >= p.ni || j >= p.nj) continue;
+      if (p.splits > 1) store_vec<float, 8>(p.planes + ((int64_t)s * p.ni + i) * pitch + j, v);
+      else weight_out<T>(p, i, j, back, v);
+    }
+  }
+}
+
+// Adds the planes in order.
+template <typename T>
+__global__ __launch_bounds__(256) void head_planes_kernel(WeightGrad p) {
+  const int64_t pieces = (p.nj + 7) / 8, plane = p.ni * pieces * 8;
+  const float back = p.scale ? p.scale[1] : 1.0f;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < p.ni * pieces;
+       u += (int64_t)gridDim.x * 256) {
+    float v[8];
+    load_vec<float, 8>(p.planes + u * 8, v);
+    for (int s = 1; s < p.splits; ++s) {
+      float more[8];
+      load_vec<float, 8>(p.planes + s * plane + u * 8, more);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += more[e];
+    }
+    weight_out<T>(p, u / pieces, (int)(u % pieces) * 8, back, v);
+  }
+}
+
+// Zeros of dW where there are no rows.
+__global__ __launch_bounds__(256) void head_zero_kernel(uint16_t* to, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    to[i] = 0;
+}
+
+template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
+hipError_t input_tiles(const InputGrad& a, hipStream_t stream) {
+  using C = Tile<BM, BN, WM, WN, KS>;
+  static std::atomic<uint64_t> configured{0};
+  const int64_t tiles_m = ceil64(a.rows, BM), tiles_n = ceil64(a.cols, BN);
+  return launch_lds(head_input_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured,
+                    ceil64(tiles_m * tiles_n, 8) * 8 + 8, C::kThreads, C::kLds, stream, a,
+                    (int)tiles_n);
+}
+
+template <typename T, bool QT>
+hipError_t input_variant(const InputGrad& a, hipStream_t stream) {
+  RowsProduct r{};
+  r.rows = a.rows;
+  r.cols = a.cols;
+  r.depth = a.depth;
+  r.groups = Groups{nullptr, false, 1};
+  switch (rows_tile_that_fits(r)) {
+    case kRows32: return input_tiles<T, QT, 32, 32, 1, 1, 8, 2>(a, stream);
+    case kRows32x128: return input_tiles<T, QT, 32, 128, 1, 4, 2, 4>(a, stream);
+    case kRows64: return input_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
+    case kRows128: return input_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
+    default: return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int OCC>
+hipError_t weight_side(const WeightGrad& a, hipStream_t stream) {
+  using C = Tile<BM, BN, WM, WN, 1>;
+  static std::atomic<uint64_t> configured{0};
+  const int64_t tiles_i = ceil64(a.ni, BM), tiles_j = ceil64(a.nj, BN);
+  hipError_t e = launch_lds(head_weight_kernel<T, BM, BN, WM, WN, OCC>, configured,
+                            tiles_i * tiles_j * a.splits, C::kThreads, C::kLds, stream, a,
+                            (int)tiles_i, (int)tiles_j);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t pieces = a.ni * ceil64(a.nj, 8);
+  head_planes_kernel<T><<<dim3((unsigned)std::min<int64_t>(ceil64(pieces, 256), 8192)), 256, 0,
+                          stream>>>(a);
+  return hipGetLastError();
+}
+
+// The splits and tiles of a weight gradient of the same size.
+WeightPlan plan_of(int64_t rows, int64_t vocab, int64_t depth, bool w_kn) {
+  WeightProduct a{};
+  a.rows = rows;
+  a.pi = (int)(w_kn ? depth : vocab);
+  a.qj = (int)(w_kn ? vocab : depth);
+  a.groups = Groups{nullptr, false, 1};
+  return weight_plan(a);
+}
+
+// Columns of the vocabulary at a time: P of a piece takes up to 2^28 elements.
+int64_t piece_of(int64_t rows, int64_t vocab) {
+  const int64_t most = std::max<int64_t>(1024, (int64_t(1) << 28) / std::max<int64_t>(rows, 1) / 256 * 256);
+  return std::min(most, ceil8(vocab));
+}
+
+hipError_t pack(const void* from, int64_t ld, int64_t rows, int64_t width, void* to, int64_t pitch,
+                hipStream_t stream) {
+  const int64_t pieces = rows * (pitch / 8);
+  if (pieces == 0) return hipSuccess;
+  head_pack_kernel<<<dim3((unsigned)std::min<int64_t>(ceil64(pieces, 256), 16384)), 256, 0, stream>>>(
+      static_cast<const uint16_t*>(from), ld, rows, width, static_cast<uint16_t*>(to), pitch);
+  return hipGetLastError();
+}
+
+// The call's operands as the tiles read them, packed where that is needed.
+hipError_t ready(const HeadCall& a, const HeadPlan& plan, char* ws, HeadProduct* p,
+                 hipStream_t stream) {
+  *p = HeadProduct{};
+  p->x = a.x; p->ldx = a.ldx;
+  p->w = a.w; p->ldw = a.w_kn ? a.vocab : a.depth;
+  p->w_kn = a.w_kn; p->f16 = a.f16;
+  p->rows = a.rows; p->depth = a.depth; p->vocab = a.vocab;
+  p->targets = a.targets; p->wide = a.wide;
+  if (plan.x >= 0) {
+    const hipError_t e = pack(a.x, a.ldx, a.rows, a.depth, ws + plan.x, plan.ldx, stream);
+    if (e != hipSuccess) return e;
+    p->x = ws + plan.x;
+    p->ldx = plan.ldx;
+  }
+  if (plan.w >= 0) {
+    const hipError_t e = pack(a.w, p->ldw, a.w_kn ? a.depth : a.vocab, p->ldw, ws + plan.w, plan.ldw,
+                              stream);
+    if (e != hipSuccess) return e;
+    p->w = ws + plan.w;
+    p->ldw = plan.ldw;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStream_t stream) {
+  HeadProduct p;
+  hipError_t e = ready(a, plan, ws, &p, stream);
+  if (e != hipSuccess) return e;
+  p.lse = a.lse;
+  p.dloss = a.dloss;
+  p.p = ws + plan.p;
+  if (plan.scale >= 0) {
+    float* scale = reinterpret_cast<float*>(ws + plan.scale);
+    head_scale_kernel<<<1, 1024, 0, stream>>>(a.dloss, a.rows, scale);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.scale = scale;
+  }
+  for (int64_t v = 0; v < a.vocab; v += plan.piece) {
+    const int64_t cols = std::min(plan.piece, a.vocab - v);
+    p.first = v;
+    p.cols = cols;
+    p.ldp = ceil8(cols);
+    e = launch_head_probabilities(p, stream);
+    if (e != hipSuccess) return e;
+    if (a.dx) {
+      InputGrad g{};
+      g.p = p.p; g.ldp = p.ldp;
+      g.w = static_cast<const uint16_t*>(p.w) + (a.w_kn ? v : v * p.ldw);
+      g.ldw = p.ldw;
+      g.rows = a.rows; g.cols = a.depth; g.depth = (int)cols;
+      g.sum = plan.dx >= 0 ? reinterpret_cast<float*>(ws + plan.dx) : nullptr;
+      g.ldsum = ceil8(a.depth);
+      g.first = v == 0; g.last = v + cols == a.vocab;
+      g.scale = p.scale;
+      g.out = a.dx; g.ldout = a.lddx;
+      e = a.w_kn ? input_variant<T, false>(g, stream) : input_variant<T, true>(g, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (a.dw) {
+      WeightGrad g{};
+      const WeightPlan tiles = plan_of(a.rows, cols, a.depth, a.w_kn);
+      const int64_t at = a.w_kn ? v : v * a.depth;
+      if (a.w_kn) {
+        g.p = p.x; g.ldp = p.ldx; g.ni = a.depth;
+        g.q = p.p; g.ldq = p.ldp; g.nj = (int)cols;
+      } else {
+        g.p = p.p; g.ldp = p.ldp; g.ni = (int)cols;
+        g.q = p.x; g.ldq = p.ldx; g.nj = a.depth;
+      }
+      g.rows = a.rows;
+      g.splits = tiles.splits;
+      g.planes = plan.planes >= 0 ? reinterpret_cast<float*>(ws + plan.planes) : nullptr;
+      g.scale = p.scale;
+      g.out = static_cast<char*>(a.dw) + at * (a.dw_f32 ? 4 : 2);
+      g.ldout = a.w_kn ? a.vocab : a.depth;
+      g.out_f32 = a.dw_f32;
+      e = tiles.side == 256 ? weight_side<T, 256, 256, 2, 4, 2>(g, stream)
+                            : weight_side<T, 128, 128, 2, 2, 2>(g, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f16, int in_place,
+                   int64_t rows, int64_t vocab, int64_t depth) {
+  HeadPlan plan{-1, -1, -1, -1, -1, -1, -1, ceil8(depth), ceil8(w_kn ? vocab : depth), 0, 0};
+  auto take = [&](int64_t bytes) {
+    const int64_t at = (int64_t)plan.bytes;
+    plan.bytes += (size_t)((bytes + 255) / 256 * 256);
+    return at;
+  };
+  if (!(in_place & 1) || depth % 8) plan.x = take(rows * plan.ldx * 2);
+  if (!(in_place & 2) || (w_kn ? vocab : depth) % 8) plan.w = take((w_kn ? depth : vocab) * plan.ldw * 2);
+  if (!gradient) {
+    plan.part = take(rows * head_stat_tiles(rows, vocab, (int)depth) * 8);
+    return plan;
+  }
+  plan.piece = piece_of(rows, vocab);
+  if (f16) plan.scale = take(8);
+  plan.p = take(rows * plan.piece * 2);
+  if (want_dx && plan.piece < vocab) plan.dx = take(rows * ceil8(depth) * 4);
+  if (want_dw) {
+    int64_t words = 0;
+    for (int64_t cols : {std::min(plan.piece, vocab), vocab % plan.piece}) {   // and the last piece
+      if (cols == 0) continue;
+      const WeightPlan t = plan_of(rows, cols, depth, w_kn);
+      if (t.splits > 1)
+        words = std::max(words, t.splits * (w_kn ? depth * ceil8(cols) : cols * ceil8(depth)));
+    }
+    if (words) plan.planes = take(words * 4);
+  }
+  return plan;
+}
+
+hipError_t launch_cross_entropy(const HeadCall& a, char* ws, hipStream_t stream) {
+  const HeadPlan plan =
+      head_plan(false, false, false, a.w_kn, a.f16, a.in_place, a.rows, a.vocab, a.depth);
+  HeadProduct p;
+  const hipError_t e = ready(a, plan, ws, &p, stream);
+  if (e != hipSuccess) return e;
+  p.cols = a.vocab;
+  p.part = reinterpret_cast<float2*>(ws + plan.part);
+  p.loss = a.loss;
+  return launch_head_stats(p, a.lse, stream);
+}
+
+hipError_t launch_cross_entropy_grad(const HeadCall& a, char* ws, hipStream_t stream) {
+  if (a.rows == 0) {
+    const int64_t n = a.dw ? a.vocab * a.depth * (a.dw_f32 ? 2 : 1) : 0;   // in 16-bit words
+    if (n == 0) return hipSuccess;
+    head_zero_kernel<<<dim3((unsigned)std::min<int64_t>(ceil64(n, 256), 4096)), 256, 0, stream>>>(
+        static_cast<uint16_t*>(a.dw), n);
+    return hipGetLastError();
+  }
+  const HeadPlan plan = head_plan(true, a.dx != nullptr, a.dw != nullptr, a.w_kn, a.f16, a.in_place,
+                                  a.rows, a.vocab, a.depth);
+  return a.f16 ? gradients<f16>(a, plan, ws, stream) : gradients<bf16>(a, plan, ws, stream);
+}
+
+}  // namespace anvil

@@ -279,49 +279,6 @@ hipError_t rows_variant(const RowsProduct& a, hipStream_t stream) {
   }
 }
 
-// Tile side and splits of each group's rows: the least of the tiles' time (as above; the K-major
-// operands' slabs take 1.25 and 0.95 us, 0.62 where a CU has one 128x128 tile) and the join's, which
-// writes and reads each split's sums.  Us by side/splits, bias gradient included, the choice first:
-//     517 rows,  512 x 4096         128/1   13.3   256/1  22.8   128/2  18.1
-//    4096 rows,  768 x 2816         128/3   40.8   128/1  59.8   128/2  43.3   256/4 46.9   256/7 44.1
-//    4096 rows, 4096 x 4096         256/1  140.8   128/1 165.9   256/2 174.9
-//   32768 rows,  256 x 768          128/21  39.6   128/8  64.3   128/32 39.7   256/32 50.2
-//   32768 rows,  768 x 2816         256/7  167.3   128/7 201.2   256/4 224.8   256/8 229.1
-//   32768 rows,  512 x 4096         256/8  164.8   128/4 178.0   256/7 174.6   256/16 183.2
-//   32768 over 24, 768 x 2816       256/1  206.0   128/1 223.3   256/2 355.4
-//   32768 over 32, 512 x 4096       256/1  201.9   128/1 233.5   256/2 414.9
-//   32768 over  8, 256 x 768        128/5   39.2   128/1 113.5   128/4 42.1   256/4 67.7
-// Experts are split alike, by the average group's rows: with half of the 32768 rows at one expert the
-// two cases of 24 and 32 take 459 and 471, with all of them there 859 and 878.
-struct WeightPlan {
-  int side, splits;
-};
-
-WeightPlan weight_plan(const WeightProduct& a) {
-  const double slabs = std::max(1.0, (double)a.rows / a.groups.count / kBK);
-  const double bytes = 4.0 * a.groups.count * a.pi * a.qj;
-  WeightPlan best{128, 1};
-  double least = 0;
-  for (int side : {128, 256}) {
-    const double tiles =
-        (double)ceil64(a.pi, side) * (double)ceil64(a.qj, side) * (double)a.groups.count;
-    for (int splits = 1; splits <= 64; ++splits) {
-      const double each = std::ceil(slabs / splits);
-      if (splits > 1 && each < 4) break;   // at least 256 rows a split
-      const double workgroups = tiles * splits;
-      double cost = side == 256 ? rounds(workgroups, 256) * (10.0 + 1.25 * each)
-                                : rounds(workgroups, 512) * (4.0 + 0.95 * each);
-      if (side == 128 && workgroups <= 256) cost = 5.0 + 0.62 * each;
-      if (splits > 1) cost += 5.0 + (2 * splits + 1) * bytes / 5e6;
-      if ((side == 128 && splits == 1) || cost < least) {
-        best = {side, splits};
-        least = cost;
-      }
-    }
-  }
-  return best;
-}
-
 template <typename T, int BM, int BN, int WM, int WN, int OCC>
 hipError_t weight_tiles(const WeightProduct& a, float* ws, int splits, hipStream_t stream) {
   using C = Tile<BM, BN, WM, WN, 1>;
