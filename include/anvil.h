@@ -450,6 +450,50 @@ int anvil_cross_entropy_grad(const void* x, int64_t ldx, const void* w, int w_kn
 size_t anvil_cross_entropy_grad_workspace(int want_dx, int want_dw, int w_kn, int in_place, int dtype,
                                           int64_t rows, int64_t vocab, int64_t k);
 
+/* ------------------------------------------------------------------------------------------
+ * AdamW over a list of tensors in one launch, for what is no bank (embedding, head, norms, biases).
+ * Per element in fp32, every operation rounded on its own:
+ *   g = grad * grad_scale;  m = m beta1 + g (1 - beta1);  v = v beta2 + (g g) (1 - beta2);
+ *   p = p (1 - lr wd) - lr ((m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps))
+ * with lr * lr_mul and weight_decay * wd_mul of the tensor as lr and wd (both corrections are formed in
+ * double and applied as fp32 factors).
+ * ------------------------------------------------------------------------------------------ */
+typedef struct anvil_adamw_tensor {
+  void* param;          /* [count] of param_dtype: rounded to it once, to nearest even, ... */
+  uint16_t* mantissa;   /* ... or, with ANVIL_BF16, the low halves of fp32 masters whose high halves are
+                         * param (as in anvil_bank_update), or NULL */
+  const void* grad;     /* [count] of grad_dtype */
+  void *m, *v;          /* state_bits 32: fp32 [count].  8: e4m3 bytes [count] times a scale for each 256
+                         * elements, of m and of sqrt(v) */
+  float *m_scale, *v_scale; /* state_bits 8: fp32 [ceil(count / 256)] */
+  int64_t count;        /* <= 2^40 */
+  int param_dtype, grad_dtype;   /* enum anvil_dtype */
+  float lr_mul, wd_mul;
+  int state_bits;       /* 32 or 8 */
+} anvil_adamw_tensor;
+
+/* The plan of a list: written to HOST memory (8-byte aligned) of anvil_adamw_plan_bytes bytes (0 for an
+ * empty list or counts out of range); the caller copies it to the device (16-byte aligned) and keeps it
+ * for as many steps as the pointers are the same.  All device pointers, element-aligned; what a step writes may not
+ * share memory with anything else in the list (ANVIL_ERR_ALIAS; gradients may be shared).  count <= 2^20,
+ * at most 2^31 pieces of 2048 elements.  No HIP call is made. */
+size_t anvil_adamw_plan_bytes(const anvil_adamw_tensor* tensors, int64_t count);
+int anvil_adamw_plan(const anvil_adamw_tensor* tensors, int64_t count, void* plan, size_t plan_bytes);
+
+/* One step of every tensor of a plan in DEVICE memory.  step counts from 1; grad_scale is a DEVICE fp32 (a
+ * clipping coefficient) or NULL.  8-bit states are rounded up or down at random with the probability
+ * that keeps the mean; the dither is a hash of (seed, tensor, element), so pass another seed each step
+ * and the same one to repeat a step bit for bit.  (A non-zero sqrt(v) keeps the least code; a block whose largest
+ * magnitude is under 2^-100 is taken as zero; an infinity makes its block of 256 NaN.) */
+int anvil_adamw(const void* plan, size_t plan_bytes, int64_t tensors, float lr, double beta1,
+                double beta2, double eps, float weight_decay, int64_t step, uint32_t seed,
+                const float* grad_scale, void* stream);
+
+/* The same with the per-step values read from the device when the kernel runs (graph-capturable): fp32
+ * scalars[5] = lr, weight_decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24). */
+int anvil_adamw_dev(const void* plan, size_t plan_bytes, int64_t tensors, const float* scalars,
+                    double beta1, double beta2, double eps, const float* grad_scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,6 +92,10 @@ SIGNATURES = {
     "anvil_cross_entropy_grad": (_i, [_vp, _i64, _vp, _i, _vp, _i, _vp, _vp, _vp, _i64, _vp, _i, _i,
                                       _i64, _i64, _i64, _vp, _sz, _vp]),
     "anvil_cross_entropy_grad_workspace": (_sz, [_i, _i, _i, _i, _i, _i64, _i64, _i64]),
+    "anvil_adamw_plan_bytes": (_sz, [_vp, _i64]),
+    "anvil_adamw_plan": (_i, [_vp, _i64, _vp, _sz]),
+    "anvil_adamw": (_i, [_vp, _sz, _i64, _f, _d, _d, _d, _f, _i64, ctypes.c_uint32, _vp, _vp]),
+    "anvil_adamw_dev": (_i, [_vp, _sz, _i64, _vp, _d, _d, _d, _vp, _vp]),
 }
 
 _lib = None
@@ -1020,3 +1024,143 @@ def anvil_cross_entropy_grad(x, w, targets, lse, dloss, w_kn=False, out=None, dw
     if status:
         _check("anvil_cross_entropy_grad", status)
     return out, dw_out
+
+
+class AdamwTensor(ctypes.Structure):
+    """anvil_adamw_tensor of include/anvil.h."""
+    _fields_ = [("param", _vp), ("mantissa", _vp), ("grad", _vp), ("m", _vp), ("v", _vp),
+                ("m_scale", _vp), ("v_scale", _vp), ("count", _i64), ("param_dtype", _i),
+                ("grad_dtype", _i), ("lr_mul", _f), ("wd_mul", _f), ("state_bits", _i)]
+
+
+class AdamW:
+    """The tensors of an AdamW step, their states and the plan of the launch that updates them all.
+
+    params and grads are lists of contiguous GPU tensors of equal shapes, each fp32, bf16 or fp16.  With
+    `mantissas` a bf16 parameter may have an int16 or uint16 tensor (None for others): the low half of an
+    fp32 master whose high half it is, as in anvil_bank_update.  state_bits is 32 (m and v in fp32) or 8 (m
+    and sqrt(v) as float8_e4m3fn with an fp32 scale for each 256 elements), one for all or one each; states
+    that are not given start at zero.  lr_mul and wd_mul multiply a step's lr and weight decay, one for each
+    tensor.  The plan holds the tensors' addresses (and references to them): gradients that move to other
+    tensors are given to bind()."""
+
+    def __init__(self, params, grads, mantissas=None, state_bits=32, m=None, v=None, m_scale=None,
+                 v_scale=None, lr_mul=None, wd_mul=None):
+        torch = _module()
+        self.params = list(params)
+        count = len(self.params)
+
+        def each(values, name, default):
+            values = [default] * count if values is None else list(values)
+            if len(values) != count:
+                raise ValueError(f"{name} must have one entry for each of {count} parameters")
+            return values
+
+        bits = each([state_bits] * count if isinstance(state_bits, int) else state_bits, "state_bits", 32)
+        if any(b not in (8, 32) for b in bits):
+            raise ValueError("state_bits must be 8 or 32")
+        self.mantissas = each(mantissas, "mantissas", None)
+        lr_mul, wd_mul = each(lr_mul, "lr_mul", 1.0), each(wd_mul, "wd_mul", 1.0)
+        given = [each(s, name, None) for s, name in ((m, "m"), (v, "v"), (m_scale, "m_scale"), (v_scale, "v_scale"))]
+        self.m, self.v, self.m_scale, self.v_scale = [], [], [], []
+        self._table = (AdamwTensor * max(1, count))()
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else 0
+        for i, p in enumerate(self.params):
+            self.device = device = _device(p, f"params[{i}]")
+            code = _code(p, f"params[{i}]", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
+            shape, n = tuple(p.shape), p.numel()
+            low = self.mantissas[i]
+            if low is not None:
+                if code != ANVIL_BF16:
+                    raise TypeError(f"params[{i}] must be bfloat16 to have a mantissa")
+                if not isinstance(low, torch.Tensor) or low.dtype not in (torch.int16, torch.uint16):
+                    raise TypeError(f"mantissas[{i}] must be a 16-bit integer tensor")
+                low = _dense(low, f"mantissas[{i}]", low.dtype, device, shape)
+            at = {}
+            blocks = -(-n // 256)
+            for name, value, own in zip(("m", "v", "m_scale", "v_scale"), given, (self.m, self.v, self.m_scale, self.v_scale)):
+                scale = name.endswith("scale")
+                if scale and bits[i] == 32:
+                    own.append(None)
+                    at[name] = None
+                    continue
+                dtype = torch.float32 if scale or bits[i] == 32 else torch.float8_e4m3fn
+                want = (blocks,) if scale else shape
+                t = value[i]
+                if t is None:
+                    # as bytes: those of zero are zeros in either type
+                    t = _empty(want, dtype, p.device, None)
+                    t.view(torch.uint8).zero_()
+                at[name] = _dense(t, f"{name}[{i}]", dtype, device, want)
+                own.append(t)
+            _dense(p, f"params[{i}]", p.dtype, device, shape)
+            row = self._table[i]
+            row.param, row.mantissa, row.count, row.param_dtype = p.data_ptr(), low, n, code
+            row.m, row.v, row.m_scale, row.v_scale = at["m"], at["v"], at["m_scale"], at["v_scale"]
+            row.lr_mul, row.wd_mul, row.state_bits = lr_mul[i], wd_mul[i], bits[i]
+        self.bind(grads)
+
+    def bind(self, grads):
+        """Takes the gradients from other tensors from the next step on."""
+        torch = _module()
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"grads must have one entry for each of {len(self.params)} parameters")
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if not isinstance(g, torch.Tensor):
+                raise TypeError(f"grads[{i}] must be a torch.Tensor")
+            code = _code(g, f"grads[{i}]", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
+            self._table[i].grad = _dense(g, f"grads[{i}]", g.dtype, self.device, tuple(p.shape))
+            self._table[i].grad_dtype = code
+        self.grads = grads
+        lib, count = load(), len(self.params)
+        table = ctypes.cast(self._table, _vp)
+        self.plan_bytes = int(lib.anvil_adamw_plan_bytes(table, count))
+        host = (ctypes.c_int64 * max(1, self.plan_bytes // 8))()
+        _check("anvil_adamw_plan", lib.anvil_adamw_plan(table, count, ctypes.cast(host, _vp), self.plan_bytes))
+        # the copy from pageable memory has ended when this returns, whatever stream a step runs on
+        self._plan = torch.frombuffer(host, dtype=torch.int64).to(f"cuda:{self.device}") if count else None
+
+    def _arguments(self, grad_scale, stream):
+        """(plan, its bytes, tensors), the grad_scale pointer and the stream's handle of a step."""
+        torch = _module()
+        if torch.cuda.current_device() != self.device:
+            raise ValueError(f"the parameters are on cuda:{self.device}, not on the current device "
+                             f"cuda:{torch.cuda.current_device()} (use torch.cuda.set_device)")
+        scale = None
+        if grad_scale is not None:
+            _same(grad_scale, "grad_scale", torch.float32, self.device)
+            if grad_scale.numel() != 1:
+                raise ValueError("grad_scale must hold one value")
+            scale = grad_scale.data_ptr()
+        if stream is not None and self._plan is not None:
+            other = _other_stream(stream)
+            if other is not None:
+                self._plan.record_stream(other)
+        plan = self._plan.data_ptr() if self._plan is not None else None
+        return (plan, self.plan_bytes, len(self.params)), scale, _raw_stream(stream, self.device)
+
+
+def anvil_adamw(plan, lr, step, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, grad_scale=None, seed=None,
+                stream=None):
+    """One AdamW step (number `step`, from 1) of every tensor of an AdamW plan, in place.  grad_scale, a
+    device fp32 tensor of one value, multiplies the gradients (a clipping coefficient).  seed dithers the
+    rounding of 8-bit states; by default it is the step."""
+    head, scale, handle = plan._arguments(grad_scale, stream)
+    seed = step if seed is None else seed
+    status = load().anvil_adamw(*head, lr, betas[0], betas[1], eps, weight_decay, step, seed & 0xFFFFFFFF,
+                                scale, handle)
+    if status:
+        _check("anvil_adamw", status)
+
+
+def anvil_adamw_dev(plan, scalars, betas=(0.9, 0.95), eps=1e-8, grad_scale=None, stream=None):
+    """anvil_adamw with the step's values read from the device when it runs (for a captured graph): scalars
+    fp32 [5] = lr, weight decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24)."""
+    head, scale, handle = plan._arguments(grad_scale, stream)
+    _same(scalars, "scalars", _torch.float32, plan.device)
+    if scalars.numel() < 5 or not scalars.is_contiguous():
+        raise ValueError("scalars must hold lr, weight decay, 1 - beta1^t, sqrt(1 - beta2^t) and the seed")
+    status = load().anvil_adamw_dev(*head, scalars.data_ptr(), betas[0], betas[1], eps, scale, handle)
+    if status:
+        _check("anvil_adamw_dev", status)

@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libanvil.so")
 SOURCES = ["momentum.hip", "gemm.hip", "normalize.hip", "update.hip", "api.hip", "norm.hip",
            "linear.hip", "linear_tiles.hip", "gated.hip", "cross_entropy.hip",
-           "cross_entropy_grad.hip", "train_api.hip", "head_api.hip"]
+           "cross_entropy_grad.hip", "train_api.hip", "head_api.hip", "adamw.hip",
+           "adamw_api.hip"]
 ARCH = "gfx950"
 
 
