@@ -37,99 +37,121 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
-// Statistics of a wave's block (rows r0 .., columns c0 .. of the piece) into stat[wn][row of the tile].
-template <typename C, int BM>
-__device__ __forceinline__ void block_stats(const HeadProduct& p,
-                                            const f32x16_t (&acc)[C::kFM][C::kFN], float2* stat,
-                                            int64_t row0, int wm, int64_t c0, int lane) {
-  const int half = 4 * (lane >> 5);
-  const bool edge = c0 + C::kWTN > p.cols;
-  const int left = (int)min(p.cols - c0, (int64_t)C::kWTN) - half;   // the lane's valid columns
+// What the rows of a lane's fragments (row lane % 32 of each) have to do with a tile: read ahead of the
+// tile's end.
+template <int FM>
+struct RowData {
+  int target[FM];      // -1: ignored
+  float ref[FM];       // -lse log2(e)
+  float weight[FM];    // dloss times the scale
+  bool in[FM];
+  template <bool STATS>
+  __device__ __forceinline__ void load(const HeadProduct& p, int64_t r0, int lane) {
+    const float scale = !STATS && p.scale ? p.scale[0] : 1.0f;
 #pragma unroll
-  for (int fm = 0; fm < C::kFM; ++fm) {
-    const int at = wm * C::kWTM + fm * 32 + (lane & 31);
-    const int64_t r = row0 + at;
-    float m = -INFINITY, s = 0.0f;
-#pragma unroll
-    for (int fn = 0; fn < C::kFN; ++fn)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float z = acc[fm][fn][e];
-        const bool in = !edge || fn * 32 + 8 * (e / 4) + e % 4 < left;
-        if (in && z > m) m = z;
-      }
-    const float other = __shfl_xor(m, 32);
-    m = other > m ? other : m;
-    const float ref = m == -INFINITY ? 0.0f : -m * kLog2e;
-#pragma unroll
-    for (int fn = 0; fn < C::kFN; ++fn)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(acc[fm][fn][e], kLog2e, ref));
-        const bool in = !edge || fn * 32 + 8 * (e / 4) + e % 4 < left;
-        s += in ? x : 0.0f;
-      }
-    s += __shfl_xor(s, 32);
-    if (lane < 32) stat[at] = make_float2(m, s);
-    if (r < p.rows) {
-      const int64_t column = target_of(p, r) - c0 - half;   // the lane's own column of the block
-      const int d = column >= 0 && column < C::kWTN ? (int)column : -1;
-      if (d >= 0 && (d & 4) == 0) {
-#pragma unroll
-        for (int fn = 0; fn < C::kFN; ++fn)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (d == fn * 32 + 8 * (e / 4) + e % 4) p.loss[r] = acc[fm][fn][e];
+    for (int fm = 0; fm < FM; ++fm) {
+      const int64_t r = r0 + fm * 32 + (lane & 31);
+      in[fm] = r < p.rows;
+      target[fm] = -1;
+      ref[fm] = weight[fm] = 0.0f;
+      if (!in[fm]) continue;
+      target[fm] = (int)target_of(p, r);
+      if (!STATS) {
+        ref[fm] = -p.lse[r] * kLog2e;
+        weight[fm] = p.dloss[r] * scale;
       }
     }
   }
+};
+
+// Columns past the lane's first `left` of the block count as logits of -inf.
+template <int FM, int FN>
+__device__ __forceinline__ void mask_columns(f32x16_t (&acc)[FM][FN], int left) {
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (fn * 32 + 8 * (e / 4) + e % 4 >= left) acc[fm][fn][e] = -INFINITY;
 }
 
-// P of a wave's block, through LDS into whole lines.
-template <typename T, typename C>
-__device__ __forceinline__ void block_probabilities(const HeadProduct& p,
-                                                    f32x16_t (&acc)[C::kFM][C::kFN], char* stage,
-                                                    int64_t r0, int64_t c0, int lane) {
-  using S = OutStage<C::kWTN>;
-  const int64_t c = c0 + S::col(lane);
-  const int64_t first = r0 + S::row(0, lane);
-  const int rows = c < p.ldp ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
-  T* out = static_cast<T*>(p.p) + first * p.ldp + c;
-  const int half = 4 * (lane >> 5);
-  const bool edge = c0 + C::kWTN > p.cols;
-  const int left = (int)(p.cols - c0) - half;   // vocabularies fit an int
-  const float scale = p.scale ? p.scale[0] : 1.0f;
+// The lane's place (0 .. FN * 32 - 1) of the row's target in a block whose columns begin at c0, -1 where
+// another lane or block has it.
+template <int FN>
+__device__ __forceinline__ int target_place(int target, int64_t c0, int lane) {
+  const int64_t d = target - c0 - 4 * (lane >> 5);
+  return d >= 0 && d < FN * 32 && (d & 4) == 0 ? (int)d : -1;
+}
+
+// Statistics of a wave's block (rows r0 .., columns c0 ..) into stat[row of the block].  The choice of the
+// target's logit is a row of comparisons that only the few blocks with a target run.
+template <int FM, int FN>
+__device__ __forceinline__ void block_stats(const HeadProduct& p, f32x16_t (&acc)[FM][FN],
+                                            const RowData<FM>& rows, float2* stat, int64_t r0,
+                                            int64_t c0, int lane) {
+  if (c0 + FN * 32 > p.cols) mask_columns(acc, (int)(p.cols - c0) - 4 * (lane >> 5));
 #pragma unroll
-  for (int fm = 0; fm < C::kFM; ++fm) {
-    const int64_t r = r0 + fm * 32 + (lane & 31);
-    float ref = 0.0f, weight = 0.0f;
-    int d = -1;
-    bool counts = false;
-    if (r < p.rows) {
-      const int64_t t = target_of(p, r);
-      counts = t >= 0;
-      ref = -p.lse[r] * kLog2e;
-      weight = p.dloss[r] * scale;
-      const int64_t column = t - p.first - c0 - half;   // the lane's own column of the block
-      if (column >= 0 && column < C::kWTN) d = (int)column;
+  for (int fm = 0; fm < FM; ++fm) {
+    const int d = target_place<FN>(rows.target[fm], c0, lane);
+    if (__any(d >= 0)) {
+      float z = 0.0f;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          z = d == fn * 32 + 8 * (e / 4) + e % 4 ? acc[fm][fn][e] : z;
+      if (d >= 0) p.loss[r0 + fm * 32 + (lane & 31)] = z;
     }
+    float m = -INFINITY, s = 0.0f;
 #pragma unroll
-    for (int fn = 0; fn < C::kFN; ++fn)
+    for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int at = fn * 32 + 8 * (e / 4) + e % 4;
-        float x = __builtin_amdgcn_exp2f(fmaf(acc[fm][fn][e], kLog2e, ref));
-        x = (d == at ? x - 1.0f : x) * weight;
-        acc[fm][fn][e] = counts && (!edge || at < left) ? x : 0.0f;
-      }
-    S::put(stage, acc[fm], lane);
+      for (int e = 0; e < 16; ++e) m = __builtin_fmaxf(m, acc[fm][fn][e]);   // NaN stays out
+    m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+    const float ref = m == -INFINITY ? 0.0f : -m * kLog2e;
 #pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) {
-      const int rr = fm * 32 + i * S::kRows;
-      float v[8];
-      S::get(stage, i, lane, v);
-      if (rr < rows) *reinterpret_cast<u32x4_t*>(out + rr * p.ldp) = pack8<T>(v);
-    }
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        s += __builtin_amdgcn_exp2f(fmaf(acc[fm][fn][e], kLog2e, ref));
+    s += __shfl_xor(s, 32);
+    if (lane < 32) stat[fm * 32 + lane] = make_float2(m, s);
+  }
+}
+
+// P of one fragment row of a wave's block in place of the logits; rows without a target are left for
+// the store to clear.
+template <int FN>
+__device__ __forceinline__ void row_probabilities(f32x16_t (&z)[FN], int d, float ref, float weight) {
+  const bool any = __any(d >= 0);
+#pragma unroll
+  for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      z[fn][e] = __builtin_amdgcn_exp2f(fmaf(z[fn][e], kLog2e, ref));
+  if (any) {
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        z[fn][e] -= d == fn * 32 + 8 * (e / 4) + e % 4 ? 1.0f : 0.0f;
+  }
+#pragma unroll
+  for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[fn][e] *= weight;
+}
+
+// The waves' statistics stat[WN][BM] of a tile's rows, joined, to part.
+template <int BM, int WN, int WAVES>
+__device__ __forceinline__ void tile_stats(const HeadProduct& p, const float2* stat, int64_t row0,
+                                           int64_t end, int tj, int tiles_n, int wave, int lane) {
+  for (int at = wave * 64 + lane; at < BM && row0 + at < end; at += WAVES * 64) {
+    float m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WN; ++i) join(m, s, stat[i * BM + at].x, stat[i * BM + at].y);
+    p.part[(row0 + at) * tiles_n + tj] = make_float2(m, s);
   }
 }
 
@@ -168,24 +190,117 @@ void head_kernel(HeadProduct p, int tiles_n) {
   if (idle) pipe.attend();
   else pipe.template run<false>(acc, 0, none);
   if constexpr (KS > 1) pipe.merge(kg, acc);
-  const int64_t c0 = j0 + wn * C::kWTN;
+  const int64_t c0 = j0 + wn * C::kWTN, r0 = row0 + wm * C::kWTM;
+  RowData<C::kFM> rows;
+  if (kg == 0 && !idle) rows.template load<STATS>(p, r0, lane);
   if constexpr (STATS) {
     // the first set's spare buffer; the other sets only meet at the barrier
     float2* stat = reinterpret_cast<float2*>(pipe.spare());
-    if (kg == 0 && !idle) block_stats<C, BM>(p, acc, stat + wn * BM, row0, wm, c0, lane);
+    if (kg == 0 && !idle) block_stats(p, acc, rows, stat + wn * BM + wm * C::kWTM, r0, c0, lane);
     __syncthreads();
-    if (kg == 0) {
-      for (int at = wave * 64 + lane; at < BM && row0 + at < end; at += C::kWaves * 64) {
-        float m = -INFINITY, s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < WN; ++i) join(m, s, stat[i * BM + at].x, stat[i * BM + at].y);
-        p.part[(row0 + at) * tiles_n + tj] = make_float2(m, s);
-      }
-    }
+    if (kg == 0) tile_stats<BM, WN, C::kWaves>(p, stat, row0, end, tj, tiles_n, wave, lane);
   } else {
     if (kg > 0 || idle) return;
-    block_probabilities<T, C>(p, acc, pipe.spare() + wave * S::kBytes, row0 + wm * C::kWTM, c0, lane);
+    char* stage = pipe.spare() + wave * S::kBytes;
+    const int64_t c = c0 + S::col(lane), first = r0 + S::row(0, lane);
+    const int inside = c < p.ldp ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
+    T* out = static_cast<T*>(p.p) + first * p.ldp + c;
+    if (c0 + C::kWTN > p.cols) mask_columns(acc, (int)(p.cols - c0) - 4 * (lane >> 5));
+#pragma unroll
+    for (int fm = 0; fm < C::kFM; ++fm) {
+      row_probabilities(acc[fm], target_place<C::kFN>(rows.target[fm], p.first + c0, lane),
+                        rows.ref[fm], rows.weight[fm]);
+      const uint64_t counts = __ballot(rows.target[fm] >= 0);
+      S::put(stage, acc[fm], lane);
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) {
+        const int r = fm * 32 + i * S::kRows;
+        float v[8];
+        S::get(stage, i, lane, v);
+        if (r < inside)
+          *reinterpret_cast<u32x4_t*>(out + r * p.ldp) =
+              counts >> S::row(i, lane) & 1 ? pack8<T>(v) : u32x4_t{};
+      }
+    }
   }
+}
+
+// The same for large products: 256 workgroups that walk over the 256x256 tiles, the next tile's slabs on
+// their way while a tile is finished (Pipe::walk).  What that needs of LDS, the statistics of the waves or
+// P's outgoing rows in 16 bits, lies beside the two buffers: 32 KB, the rest of the CU's 160.
+template <typename T, bool STATS, bool QT>
+__global__ __launch_bounds__(512)
+__attribute__((amdgpu_waves_per_eu(2)))
+void head_walk_kernel(HeadProduct p, int tiles_n) {
+  constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
+  using C = Tile<BM, BN, WM, WN, 1>;
+  using S = OutStage16<T>;
+  static_assert(C::kWTN == 64, "whole lines");
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave / WN, wn = wave % WN;
+  TileOrder<BM> order(Groups{nullptr, false, 1}, p.rows, tiles_n);
+  const int me = blockIdx.x / 8, step = gridDim.x / 8;
+  const int tiles = (order.count() - me + step - 1) / step;
+  int64_t row0, end;   // of the tile that is being finished
+  int group, tj;
+
+  f32x16_t acc[C::kFM][C::kFN];
+#pragma unroll
+  for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+  Pipe<T, false, QT, BM, BN, WM, WN, 1> pipe(smem, wave);
+  pipe.KT = (p.depth + kBK - 1) / kBK;
+  RowData<C::kFM> rows;
+  pipe.walk(
+      acc, tiles,
+      [&](int i) {
+        int64_t first, last;
+        int none, column;
+        order.place(me + i * step, &first, &last, &none, &column);
+        const int64_t j0 = (int64_t)column * BN;
+        pipe.begin(static_cast<const uint16_t*>(p.x) + first * p.ldx, p.ldx, last - first,
+                   static_cast<const uint16_t*>(p.w) + (QT ? p.first + j0 : (p.first + j0) * p.ldw),
+                   p.ldw, p.cols - j0, p.depth, 0);
+      },
+      [&](int i) {
+        order.place(me + i * step, &row0, &end, &group, &tj);
+        rows.template load<STATS>(p, row0 + wm * C::kWTM, lane);
+      },
+      [&](int) {
+        const int64_t c0 = (int64_t)tj * BN + wn * C::kWTN, r0 = row0 + wm * C::kWTM;
+        if constexpr (STATS) {
+          float2* stat = reinterpret_cast<float2*>(smem + C::kRing);
+          block_stats(p, acc, rows, stat + wn * BM + wm * C::kWTM, r0, c0, lane);
+          wait_vmcnt<0>();
+          __syncthreads();
+          tile_stats<BM, WN, C::kWaves>(p, stat, row0, end, tj, tiles_n, wave, lane);
+        } else {
+          char* stage = smem + C::kRing + wave * S::kBytes;
+          const int64_t c = c0 + S::col(lane), first = r0 + S::row(0, lane);
+          const int inside = c < p.ldp ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
+          T* out = static_cast<T*>(p.p) + first * p.ldp + c;
+          if (c0 + C::kWTN > p.cols) mask_columns(acc, (int)(p.cols - c0) - 4 * (lane >> 5));
+#pragma unroll
+          for (int fm = 0; fm < C::kFM; ++fm) {
+            row_probabilities(acc[fm], target_place<C::kFN>(rows.target[fm], p.first + c0, lane),
+                              rows.ref[fm], rows.weight[fm]);
+            const uint64_t counts = __ballot(rows.target[fm] >= 0);
+            S::put(stage, acc[fm], lane);
+            if (fm == 0) wait_vmcnt<0>();
+#pragma unroll
+            for (int k = 0; k < S::kPasses; ++k) {
+              const int r = fm * 32 + k * S::kRows;
+              const u32x4_t v = S::get(stage, k, lane);
+              if (r < inside)
+                *reinterpret_cast<u32x4_t*>(out + r * p.ldp) =
+                    counts >> S::row(k, lane) & 1 ? v : u32x4_t{};
+            }
+          }
+        }
+      });
 }
 
 // A wave for each row: its tiles' statistics, 64 at a time, then the wave's halves pairwise.
@@ -212,7 +327,8 @@ RowsTile head_tile(int64_t rows, int64_t cols, int depth) {
   a.depth = depth;
   a.groups = Groups{nullptr, false, 1};
   a.act = kActSilu;   // an epilogue of exponentials
-  return rows_tile_that_fits(a);
+  const RowsTile t = rows_tile_that_fits(a);
+  return depth == 0 && t == kRows256 ? kRows128 : t;   // the walk begins with a slab
 }
 
 template <typename T, bool STATS, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
@@ -226,13 +342,21 @@ hipError_t head_tiles(const HeadProduct& a, hipStream_t stream) {
 }
 
 template <typename T, bool STATS, bool QT>
+hipError_t head_walk(const HeadProduct& a, hipStream_t stream) {
+  using C = Tile<256, 256, 2, 4, 1>;
+  static std::atomic<uint64_t> configured{0};
+  return launch_lds(head_walk_kernel<T, STATS, QT>, configured, 256, C::kThreads,
+                    C::kRing + 8 * OutStage16<T>::kBytes, stream, a, (int)ceil64(a.cols, 256));
+}
+
+template <typename T, bool STATS, bool QT>
 hipError_t head_variant(const HeadProduct& a, hipStream_t stream) {
   switch (head_tile(a.rows, a.cols, a.depth)) {
     case kRows32: return head_tiles<T, STATS, QT, 32, 32, 1, 1, 8, 2>(a, stream);
     case kRows32x128: return head_tiles<T, STATS, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return head_tiles<T, STATS, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return head_tiles<T, STATS, QT, 128, 128, 2, 2, 1, 2>(a, stream);
-    default: return head_tiles<T, STATS, QT, 256, 256, 2, 4, 1, 2>(a, stream);
+    default: return head_walk<T, STATS, QT>(a, stream);
   }
 }
 

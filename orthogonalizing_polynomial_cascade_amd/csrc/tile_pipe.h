@@ -171,25 +171,29 @@ struct Pipe {
   // The buffer that no wave reads any more after run(): the one before the last slab's.
   __device__ __forceinline__ char* spare() const { return smem + (KT & 1) * C::kStage; }
 
+  // The wave's fragments of k-step ks of a buffer.
+  __device__ __forceinline__ void read(int stage, int ks, int buf, vec (&fa)[2][C::kFM],
+                                       vec (&fb)[2][C::kFN]) const {
+    const char* tp = smem + stage * C::kStage;
+    const char* tq = tp + C::kQ;
+#pragma unroll
+    for (int f = 0; f < C::kFM; ++f)
+      fa[buf][f] = __builtin_bit_cast(
+          vec, (read_frag<PT, BM, kBK>(tp, wm * C::kWTM + f * 32, ks, lane)));
+#pragma unroll
+    for (int f = 0; f < C::kFN; ++f)
+      fb[buf][f] = __builtin_bit_cast(
+          vec, (read_frag<QT, kRowsQ, kBK>(tq + f / kFQ * (kRowsQ * kBK * 2),
+                                           (wn * kFQ + f % kFQ) * 32, ks, lane)));
+  }
+
   // All slabs.  `sum`: 0 none, 1 also the sums over k of the wave's P fragment `wn`, 2 of its Q
   // fragment `wm` into `sums` (see add8).
   template <bool SUMS>
   __device__ __forceinline__ void run(f32x16_t (&acc)[C::kFM][C::kFN], int sum, float& sums) {
     if (KT == 0) return;
     vec fa[2][C::kFM], fb[2][C::kFN];
-    auto read = [&](int stage, int ks, int buf) {
-      const char* tp = smem + stage * C::kStage;
-      const char* tq = tp + C::kQ;
-#pragma unroll
-      for (int f = 0; f < C::kFM; ++f)
-        fa[buf][f] = __builtin_bit_cast(
-            vec, (read_frag<PT, BM, kBK>(tp, wm * C::kWTM + f * 32, ks, lane)));
-#pragma unroll
-      for (int f = 0; f < C::kFN; ++f)
-        fb[buf][f] = __builtin_bit_cast(
-            vec, (read_frag<QT, kRowsQ, kBK>(tq + f / kFQ * (kRowsQ * kBK * 2),
-                                             (wn * kFQ + f % kFQ) * 32, ks, lane)));
-    };
+    auto read = [&](int stage, int ks, int buf) { this->read(stage, ks, buf, fa, fb); };
 
     // Slab kt from buffer `stage`.  MORE: there is a slab after it; REQUEST: and one after that,
     // whose copies go out among the last step's multiplies.
@@ -248,6 +252,84 @@ struct Pipe {
     for (; kt + 2 < KT; ++kt) slab(kt & 1, yes, yes);
     if (kt + 1 < KT) slab(kt++ & 1, yes, no);
     slab(kt & 1, no, no);
+  }
+
+  // The slabs of `tiles` tiles one after the other, as one stream: while a tile's sums are finished, the
+  // first slabs of the next one are on their way.  place(i) calls begin() for tile i (all of the same
+  // depth, at least 1, which KT is set to before); before(i) runs ahead of the last slab's multiplies, done(i) after them, with
+  // the tile's sums in acc, which are zero again for the next.  done() may use LDS outside the two
+  // buffers; a barrier lies between any two calls of it.  It has to wait for all copies (wait_vmcnt<0>)
+  // ahead of its first store to memory, and the slab after it does not wait again: it would wait for
+  // those stores (the probabilities of 16384 x 16384, depth 768: 584 us, so 4xx).  Past the last tile the
+  // copies load zeros.
+  template <typename Place, typename Before, typename Done>
+  __device__ __forceinline__ void walk(f32x16_t (&acc)[C::kFM][C::kFN], int tiles, Place place,
+                                       Before before, Done done) {
+    static_assert(KS == 1, "one set of waves");
+    if (tiles <= 0) return;
+    vec fa[2][C::kFM], fb[2][C::kFN];
+    place(0);
+    request(0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    int ahead = 0, asked = 1;   // the tile that is being copied, slabs requested of it
+    auto turn = [&] {
+      if (asked == KT) {
+        asked = 0;
+        if (++ahead < tiles) place(ahead);
+        else left = 0;
+      }
+      ++asked;
+    };
+    turn();
+    request(1);
+    read(0, 0, 0, fa, fb);
+    int at = 0, kt = 0;
+    bool landed = false;
+    const int total = tiles * KT;
+    constexpr int kMults = C::kFM * C::kFN;
+    for (int s = 0; s < total; ++s) {
+      const int stage = s & 1;
+      const bool last_slab = kt + 1 == KT;
+      if (last_slab) before(at);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        const bool last = ks + 1 == kSteps;
+        if (!last) {
+          read(stage, ks + 1, (ks + 1) & 1, fa, fb);
+        } else {
+          turn();
+          wait_lds();
+          if (!landed) wait_vmcnt<0>();
+          __syncthreads();
+          read(stage ^ 1, 0, 0, fa, fb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < kMults; ++m) {
+          const int fm = m / C::kFN, fn = m % C::kFN;
+          acc[fm][fn] = Mfma<T>::run(fb[ks & 1][fn], fa[ks & 1][fm], acc[fm][fn]);
+          if (last) {
+#pragma unroll
+            for (int i = m * kCopies / kMults; i < (m + 1) * kCopies / kMults; ++i) copy(i, stage);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      advance();
+      ++kt;
+      landed = last_slab;
+      if (last_slab) {
+        done(at);
+#pragma unroll
+        for (int fm = 0; fm < C::kFM; ++fm)
+#pragma unroll
+          for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
+        kt = 0;
+        ++at;
+      }
+    }
+    wait_vmcnt<0>();   // no copy may land after the workgroup's end
   }
 
   // run() of a wave without multiplies: its share of the copies, and every barrier.
@@ -363,6 +445,40 @@ struct OutStage {
   }
 };
 
+// The same for values that are rounded first: a wave's 32 rows of 64 columns in 16 bits, 4 KB.  A row is
+// 128 bytes = eight slots of 16; slot c of row r lies at c ^ (r / 2 % 8), so that the 16 rows that are read
+// or written together fall on all banks.
+template <typename T>
+struct OutStage16 {
+  static constexpr int kBytes = 32 * 64 * 2;
+  static constexpr int kRows = 8;               // rows of one pass, eight lanes each
+  static constexpr int kPasses = 4;
+  __device__ static __forceinline__ char* at(char* base, int row, int slot) {
+    return base + row * 128 + ((slot ^ ((row >> 1) & 7)) << 4);
+  }
+  __device__ static __forceinline__ void put(char* base, const f32x16_t (&v)[2], int lane) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int fn = 0; fn < 2; ++fn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const T t[4] = {from_f32<T>(v[fn][4 * q]), from_f32<T>(v[fn][4 * q + 1]),
+                        from_f32<T>(v[fn][4 * q + 2]), from_f32<T>(v[fn][4 * q + 3])};
+        u32x2_t w;
+        __builtin_memcpy(&w, t, 8);
+        *reinterpret_cast<u32x2_t*>(at(base, lane & 31, fn * 4 + q) + 8 * (lane >> 5)) = w;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ static __forceinline__ int row(int pass, int lane) { return pass * kRows + lane / 8; }
+  __device__ static __forceinline__ int col(int lane) { return lane % 8 * 8; }
+  __device__ static __forceinline__ u32x4_t get(char* base, int pass, int lane) {
+    return *reinterpret_cast<const u32x4_t*>(at(base, row(pass, lane), lane % 8));
+  }
+};
+
 // Tiles of one launch in an order that lets the workgroups that run together on an XCD share their
 // operands: consecutive ids go down kBand row tiles before they step to the next column tile.
 constexpr int kBand = 4;
@@ -383,33 +499,51 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// The tile of the rows product that this workgroup has: its first row, the end of its group's rows, its
-// group and its column tile.  False where there is none: the launch counts one row tile more for each
-// group than there may be.  The tiles that do exist are dealt out to the XCDs, an eighth of the whole
-// ones to each and then an eighth of the partly filled ones.
+// The tiles of the rows product as the workgroups of one XCD take them: an eighth of the whole tiles
+// and then an eighth of the partly filled ones, numbered from 0 in the order in which neighbours share
+// operands.
+template <int BM>
+struct TileOrder {
+  RowTiles<BM> rows;
+  int tiles_n, xcd;
+  int whole, parts, mine;   // all whole tiles, all partly filled ones, this XCD's whole ones
+
+  __device__ __forceinline__ TileOrder(const Groups& groups, int64_t n_rows, int tiles_n_)
+      : rows(groups, n_rows), tiles_n(tiles_n_), xcd(blockIdx.x % 8) {
+    whole = rows.whole * tiles_n;
+    parts = (rows.total - rows.whole) * tiles_n;
+    mine = whole / 8 + (xcd < whole % 8 ? 1 : 0);
+  }
+  // This XCD's tiles.  The XCDs that have one whole tile less come first among the partly filled ones.
+  __device__ __forceinline__ int count() const { return mine + (parts + xcd) / 8; }
+  // Tile at < count(): its first row, the end of its group's rows, its group, its column tile.
+  __device__ __forceinline__ void place(int at, int64_t* row0, int64_t* end, int* group, int* tj) {
+    int ti;
+    if (at < mine) {
+      banded(xcd * (whole / 8) + min(xcd, whole % 8) + at, rows.whole, tiles_n, &ti, tj);
+    } else {
+      at = (at - mine) * 8 + (7 - xcd);
+      ti = rows.whole + at / tiles_n;
+      *tj = at % tiles_n;
+    }
+    rows.find(ti, row0, end, group);
+    *row0 = uniform(*row0);
+    *end = uniform(*end);
+    *group = __builtin_amdgcn_readfirstlane(*group);
+  }
+};
+
+// The tile of this workgroup, where a workgroup has one.  False where there is none: the launch counts one
+// row tile more for each group than there may be.
 template <int BM>
 __device__ __forceinline__ bool rows_place(const Groups& groups, int64_t n_rows, int tiles_n,
                                            int64_t* row0, int64_t* end, int* group, int* tj) {
-  RowTiles<BM> rows(groups, n_rows);
-  const int xcd = blockIdx.x % 8;
-  int at = blockIdx.x / 8, ti;
-  const int whole = rows.whole * tiles_n, parts = (rows.total - rows.whole) * tiles_n;
-  const int mine = whole / 8 + (xcd < whole % 8 ? 1 : 0);
-  if (at < mine) {
-    banded(xcd * (whole / 8) + min(xcd, whole % 8) + at, rows.whole, tiles_n, &ti, tj);
-  } else {
-    at = (at - mine) * 8 + (7 - xcd);   // the XCDs that have one whole tile less come first
-    if (at >= parts) return false;
-    ti = rows.whole + at / tiles_n;
-    *tj = at % tiles_n;
-  }
-  rows.find(ti, row0, end, group);
-  *row0 = uniform(*row0);
-  *end = uniform(*end);
-  *group = __builtin_amdgcn_readfirstlane(*group);
+  TileOrder<BM> order(groups, n_rows, tiles_n);
+  const int at = blockIdx.x / 8;
+  if (at >= order.count()) return false;
+  order.place(at, row0, end, group, tj);
   return true;
 }
-
 
 // Workgroups of one launch, which counts its work-items (at most 1024 a workgroup) in 32 bits;
 // larger calls take the kernels of linear.hip, whose workgroups walk over tiles.
