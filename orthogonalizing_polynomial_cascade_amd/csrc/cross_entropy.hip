@@ -225,17 +225,18 @@ void head_kernel(HeadProduct p, int tiles_n) {
   }
 }
 
-// The same for large products: 256 workgroups that walk over the 256x256 tiles, the next tile's slabs on
-// their way while a tile is finished (Pipe::walk).  What that needs of LDS, the statistics of the waves or
-// P's outgoing rows in 16 bits, lies beside the two buffers: 32 KB, the rest of the CU's 160.
-template <typename T, bool STATS, bool QT>
+// The statistics of large products: 256 workgroups that walk over the 256x256 tiles, the next tile's
+// slabs on their way while a tile is finished (Pipe::walk); the waves' statistics lie beside the two
+// buffers.  16384 x 50304, depth 768: 1146 us (1100 TFLOP/s), 1320 with a workgroup for each tile.  The
+// probabilities do not gain: vector memory operations end in order, so a walk's copies wait for the
+// last tile's 128 KB of stores, which a workgroup of its own leaves behind when it ends (16384 x 16384: 560 us,
+// 483 with a workgroup for each tile, 484 in a walk whose stores are left out).
+template <typename T, bool QT>
 __global__ __launch_bounds__(512)
 __attribute__((amdgpu_waves_per_eu(2)))
 void head_walk_kernel(HeadProduct p, int tiles_n) {
   constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
   using C = Tile<BM, BN, WM, WN, 1>;
-  using S = OutStage16<T>;
-  static_assert(C::kWTN == 64, "whole lines");
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -262,44 +263,20 @@ void head_walk_kernel(HeadProduct p, int tiles_n) {
         order.place(me + i * step, &first, &last, &none, &column);
         const int64_t j0 = (int64_t)column * BN;
         pipe.begin(static_cast<const uint16_t*>(p.x) + first * p.ldx, p.ldx, last - first,
-                   static_cast<const uint16_t*>(p.w) + (QT ? p.first + j0 : (p.first + j0) * p.ldw),
-                   p.ldw, p.cols - j0, p.depth, 0);
+                   static_cast<const uint16_t*>(p.w) + (QT ? j0 : j0 * p.ldw), p.ldw, p.cols - j0,
+                   p.depth, 0);
       },
       [&](int i) {
         order.place(me + i * step, &row0, &end, &group, &tj);
-        rows.template load<STATS>(p, row0 + wm * C::kWTM, lane);
+        rows.template load<true>(p, row0 + wm * C::kWTM, lane);
       },
       [&](int) {
-        const int64_t c0 = (int64_t)tj * BN + wn * C::kWTN, r0 = row0 + wm * C::kWTM;
-        if constexpr (STATS) {
-          float2* stat = reinterpret_cast<float2*>(smem + C::kRing);
-          block_stats(p, acc, rows, stat + wn * BM + wm * C::kWTM, r0, c0, lane);
-          wait_vmcnt<0>();
-          __syncthreads();
-          tile_stats<BM, WN, C::kWaves>(p, stat, row0, end, tj, tiles_n, wave, lane);
-        } else {
-          char* stage = smem + C::kRing + wave * S::kBytes;
-          const int64_t c = c0 + S::col(lane), first = r0 + S::row(0, lane);
-          const int inside = c < p.ldp ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
-          T* out = static_cast<T*>(p.p) + first * p.ldp + c;
-          if (c0 + C::kWTN > p.cols) mask_columns(acc, (int)(p.cols - c0) - 4 * (lane >> 5));
-#pragma unroll
-          for (int fm = 0; fm < C::kFM; ++fm) {
-            row_probabilities(acc[fm], target_place<C::kFN>(rows.target[fm], p.first + c0, lane),
-                              rows.ref[fm], rows.weight[fm]);
-            const uint64_t counts = __ballot(rows.target[fm] >= 0);
-            S::put(stage, acc[fm], lane);
-            if (fm == 0) wait_vmcnt<0>();
-#pragma unroll
-            for (int k = 0; k < S::kPasses; ++k) {
-              const int r = fm * 32 + k * S::kRows;
-              const u32x4_t v = S::get(stage, k, lane);
-              if (r < inside)
-                *reinterpret_cast<u32x4_t*>(out + r * p.ldp) =
-                    counts >> S::row(k, lane) & 1 ? v : u32x4_t{};
-            }
-          }
-        }
+        float2* stat = reinterpret_cast<float2*>(smem + C::kRing);
+        block_stats(p, acc, rows, stat + wn * BM + wm * C::kWTM, row0 + wm * C::kWTM,
+                    (int64_t)tj * BN + wn * C::kWTN, lane);
+        wait_vmcnt<0>();
+        __syncthreads();
+        tile_stats<BM, WN, C::kWaves>(p, stat, row0, end, tj, tiles_n, wave, lane);
       });
 }
 
@@ -341,12 +318,12 @@ hipError_t head_tiles(const HeadProduct& a, hipStream_t stream) {
                     (int)tiles_n);
 }
 
-template <typename T, bool STATS, bool QT>
+template <typename T, bool QT>
 hipError_t head_walk(const HeadProduct& a, hipStream_t stream) {
   using C = Tile<256, 256, 2, 4, 1>;
   static std::atomic<uint64_t> configured{0};
-  return launch_lds(head_walk_kernel<T, STATS, QT>, configured, 256, C::kThreads,
-                    C::kRing + 8 * OutStage16<T>::kBytes, stream, a, (int)ceil64(a.cols, 256));
+  return launch_lds(head_walk_kernel<T, QT>, configured, 256, C::kThreads, C::kRing + 4 * 256 * 8,
+                    stream, a, (int)ceil64(a.cols, 256));
 }
 
 template <typename T, bool STATS, bool QT>
@@ -356,7 +333,9 @@ hipError_t head_variant(const HeadProduct& a, hipStream_t stream) {
     case kRows32x128: return head_tiles<T, STATS, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return head_tiles<T, STATS, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return head_tiles<T, STATS, QT, 128, 128, 2, 2, 1, 2>(a, stream);
-    default: return head_walk<T, STATS, QT>(a, stream);
+    default:
+      if constexpr (STATS) return head_walk<T, QT>(a, stream);
+      else return head_tiles<T, STATS, QT, 256, 256, 2, 4, 1, 2>(a, stream);
   }
 }
 

@@ -10,6 +10,7 @@
 //
 // Operands whose widths or addresses the copies into LDS cannot take (multiples of 8, 16 bytes) are packed
 // into the workspace once, with zeros to the next multiple of 8.
+#include <stdlib.h>
 #include <algorithm>
 #include <atomic>
 
@@ -88,7 +89,9 @@ __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
 void head_input_kernel(InputGrad p, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
-  using S = OutStage<C::kWTN>;
+  // fragments that leave side by side: 64 columns, or 32 at a time where a wave has 96
+  constexpr int kSide = C::kFN % 2 ? 1 : 2;
+  using S = OutStage<C::kWTN == 32 ? 32 : kSide * 32>;
   static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
   const int lane = threadIdx.x & 63;
@@ -120,39 +123,45 @@ void head_input_kernel(InputGrad p, int tiles_n) {
   }
   if (idle) return;
   char* stage = pipe.spare() + wave * S::kBytes;
-  const int c = j0 + wn * C::kWTN + S::col(lane);
   const int64_t first = row0 + wm * C::kWTM + S::row(0, lane);
-  const int rows = c < p.cols ? (int)min(end - first, (int64_t)C::kWTM) : 0;
-  float* sum = p.sum + first * p.ldsum + c;
-  T* out = static_cast<T*>(p.out) + first * p.ldout + c;
   const float back = p.scale ? p.scale[1] : 1.0f;
 #pragma unroll
-  for (int fm = 0; fm < C::kFM; ++fm) {
-    S::put(stage, acc[fm], lane);
+  for (int fn = 0; fn < C::kFN; fn += kSide) {
+    const int c = j0 + wn * C::kWTN + fn * 32 + S::col(lane);
+    const int rows = c < p.cols ? (int)min(end - first, (int64_t)C::kWTM) : 0;
+    float* sum = p.sum + first * p.ldsum + c;
+    T* out = static_cast<T*>(p.out) + first * p.ldout + c;
 #pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) {
-      const int r = fm * 32 + i * S::kRows;
-      float v[8];
-      S::get(stage, i, lane, v);
-      if (r >= rows) continue;
-      if (!p.first) {
-        float before[8];
-        load_vec<float, 8>(sum + r * p.ldsum, before);
+    for (int fm = 0; fm < C::kFM; ++fm) {
+      f32x16_t leaving[kSide];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += before[e];
-      }
-      if (!p.last) {
-        store_vec<float, 8>(sum + r * p.ldsum, v);   // the pitch is a multiple of 8
-        continue;
-      }
+      for (int f = 0; f < kSide; ++f) leaving[f] = acc[fm][fn + f];
+      S::put(stage, leaving, lane);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= back;
-      if (c + 8 <= p.cols) {
-        store_vec<T, 8>(out + r * p.ldout, v);
-      } else {
+      for (int i = 0; i < S::kPasses; ++i) {
+        const int r = fm * 32 + i * S::kRows;
+        float v[8];
+        S::get(stage, i, lane, v);
+        if (r >= rows) continue;
+        if (!p.first) {
+          float before[8];
+          load_vec<float, 8>(sum + r * p.ldsum, before);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < p.cols) out[r * p.ldout + e] = from_f32<T>(v[e]);
+          for (int e = 0; e < 8; ++e) v[e] += before[e];
+        }
+        if (!p.last) {
+          store_vec<float, 8>(sum + r * p.ldsum, v);   // the pitch is a multiple of 8
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= back;
+        if (c + 8 <= p.cols) {
+          store_vec<T, 8>(out + r * p.ldout, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < p.cols) out[r * p.ldout + e] = from_f32<T>(v[e]);
+        }
       }
     }
   }
@@ -288,7 +297,9 @@ hipError_t input_variant(const InputGrad& a, hipStream_t stream) {
     case kRows32x128: return input_tiles<T, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return input_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return input_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
-    default: return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
+    default:
+      if (getenv("X192")) return input_tiles<T, QT, 256, 192, 4, 2, 1, 2>(a, stream);
+      return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
   }
 }
 
@@ -320,6 +331,7 @@ WeightPlan plan_of(int64_t rows, int64_t vocab, int64_t depth, bool w_kn) {
 // Columns of the vocabulary at a time: P of a piece takes up to 2^28 elements.
 int64_t piece_of(int64_t rows, int64_t vocab) {
   const int64_t most = std::max<int64_t>(1024, (int64_t(1) << 28) / std::max<int64_t>(rows, 1) / 256 * 256);
+  if (getenv("PIECE")) return std::min<int64_t>(atoi(getenv("PIECE")), ceil8(vocab));
   return std::min(most, ceil8(vocab));
 }
 
@@ -376,7 +388,7 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
     const int64_t cols = std::min(plan.piece, a.vocab - v);
     p.first = v;
     p.cols = cols;
-    p.ldp = ceil8(cols);
+    p.ldp = ceil8(cols) + 64;
     e = launch_head_probabilities(p, stream);
     if (e != hipSuccess) return e;
     if (a.dx) {
@@ -437,7 +449,7 @@ HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f1
   }
   plan.piece = piece_of(rows, vocab);
   if (f16) plan.scale = take(8);
-  plan.p = take(rows * plan.piece * 2);
+  plan.p = take(rows * (plan.piece + 64) * 2);
   if (want_dx && plan.piece < vocab) plan.dx = take(rows * ceil8(depth) * 4);
   if (want_dw) {
     int64_t words = 0;

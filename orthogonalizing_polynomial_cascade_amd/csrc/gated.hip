@@ -10,6 +10,7 @@
 // Everything else (slabs, fragments, tile order and choice, groups) is linear_tiles.hip's.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "activation.h"
 #include "any_pipe.h"
@@ -29,13 +30,17 @@ __device__ __forceinline__ void bias4(const RowsProduct& p, int64_t base, int c,
   else load_vec<T, 4>(static_cast<const T*>(p.bias) + base + c, b);
 }
 
+// Values leave rounded where a wave has 64 columns of them, which takes half of the LDS accesses.
+template <typename T, typename C>
+using GatedStage = std::conditional_t<C::kFN == 4, OutStage16<T>, OutStage<32>>;
+
 // The outgoing rows of a wave's block: rows r0 .. of a group that ends at `end`, output columns c0 ..
 template <typename T, typename C, int ACT>
 __device__ __forceinline__ void gated_out(const RowsProduct& p, f32x16_t (&acc)[C::kFM][C::kFN],
                                           char* stage, int64_t r0, int64_t end, int group, int c0,
                                           int lane) {
   constexpr int F = C::kFN / 2;
-  using S = OutStage<C::kWTN / 2>;
+  using S = GatedStage<T, C>;
   const int c = c0 + S::col(lane);
   const int64_t first = r0 + S::row(0, lane);
   const int rows = c < p.cols ? (int)min(end - first, (int64_t)C::kWTM) : 0;   // below: row inside
@@ -46,9 +51,14 @@ __device__ __forceinline__ void gated_out(const RowsProduct& p, f32x16_t (&acc)[
 #pragma unroll
     for (int i = 0; i < S::kPasses; ++i) {
       const int r = fm * 32 + i * S::kRows;
-      float w[8];
-      S::get(stage, i, lane, w);
-      if (r < rows) *reinterpret_cast<u32x4_t*>(to + r * ld) = pack8<T>(w);
+      if constexpr (F == 2) {
+        const u32x4_t w = S::get(stage, i, lane);
+        if (r < rows) *reinterpret_cast<u32x4_t*>(to + r * ld) = w;
+      } else {
+        float w[8];
+        S::get(stage, i, lane, w);
+        if (r < rows) *reinterpret_cast<u32x4_t*>(to + r * ld) = pack8<T>(w);
+      }
     }
   };
 #pragma unroll
@@ -94,7 +104,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
 void gated_tile_kernel(RowsProduct p, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
-  using S = OutStage<C::kWTN / 2>;
+  using S = GatedStage<T, C>;
   static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
   const int lane = threadIdx.x & 63;

@@ -31,11 +31,14 @@ struct SlabStream {
   // K-contiguous one, which exchanges the halves of the slab's k.
   static constexpr int kStep = KMAJOR ? NW * (512 / ROWS) : NW * (512 / kBK);
   static constexpr bool kHalf = !KMAJOR && kStep == 8;
-  static_assert(kInsts == 1 || kHalf || kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
+  static_assert(kInsts == 1 || kHalf || (KMAJOR && 512 % ROWS != 0) ||
+                    kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
   // K-major instructions differ by a uniform offset (soff); K-contiguous ones by rows that have to
-  // be checked against the edge one by one
-  uint32_t off[KMAJOR ? 1 : kInsts];
-  int kin;                 // the lane's k within the slab (of its first instruction)
+  // be checked against the edge one by one; K-major ones of 192 rows begin anywhere in a row
+  static constexpr bool kAny = KMAJOR && 512 % ROWS != 0;
+  static constexpr int kOffs = KMAJOR && !kAny ? 1 : kInsts;
+  uint32_t off[kOffs];
+  int kin[kAny ? kInsts : 1];   // the lane's k within the slab (of its first instruction)
   uint32_t soff;           // K-major: bytes from one instruction to the next
   uint64_t base, step;
 
@@ -45,6 +48,10 @@ struct SlabStream {
       constexpr int kSlots = kBK / 8;
       *row = (64 / kSlots) * u + lane / kSlots;
       *c = (lane % kSlots) ^ KContig<ROWS, kBK>::swz(*row);
+    } else if constexpr (kAny) {
+      constexpr int kSlots = ROWS / 8;
+      *row = (u * 64 + lane) / kSlots;
+      *c = ((u * 64 + lane) % kSlots) ^ KMajor<ROWS>::swz(*row);
     } else {
       constexpr int kSlots = ROWS / 8;
       *row = u * (512 / ROWS) + lane / kSlots;
@@ -57,16 +64,17 @@ struct SlabStream {
                                        int lane) {
     base = reinterpret_cast<uint64_t>(origin);
     step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
-    soff = KMAJOR ? (uint32_t)ld * (2 * kStep) : 0;
+    soff = KMAJOR && !kAny ? (uint32_t)ld * (2 * kStep) : 0;
     int row, c;
     piece(0, wave, lane, &row, &c);
-    kin = KMAJOR ? row : c * 8;
+    kin[0] = KMAJOR ? row : c * 8;
 #pragma unroll
-    for (int i = 0; i < (KMAJOR ? 1 : kInsts); ++i) {
+    for (int i = 0; i < kOffs; ++i) {
       piece(i, wave, lane, &row, &c);
       off[i] = (KMAJOR ? c * 8 : row) < rows
                    ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u
                    : kOOB;
+      if constexpr (kAny) kin[i] = row;
     }
   }
 
@@ -75,11 +83,13 @@ struct SlabStream {
   __device__ __forceinline__ void issue(int i, uint32_t dst, int left, int wave) const {
     const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
     const uint32_t to = dst + (uint32_t)(wave + i * NW) * 1024u;
-    if constexpr (KMAJOR) {
-      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB,
+    if constexpr (kAny) {
+      dma16(rsrc, to, kin[i] < left ? off[i] : kOOB);
+    } else if constexpr (KMAJOR) {
+      dma16(rsrc, to, kin[0] < left - i * kStep ? off[0] : kOOB,
             (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)i * soff)));
     } else {
-      const int k = kHalf && (i & 1) ? kin ^ (kBK / 2) : kin;
+      const int k = kHalf && (i & 1) ? kin[0] ^ (kBK / 2) : kin[0];
       dma16(rsrc, to, k < left ? off[i] : kOOB);
     }
   }
@@ -260,8 +270,7 @@ struct Pipe {
   // the tile's sums in acc, which are zero again for the next.  done() may use LDS outside the two
   // buffers; a barrier lies between any two calls of it.  It has to wait for all copies (wait_vmcnt<0>)
   // ahead of its first store to memory, and the slab after it does not wait again: it would wait for
-  // those stores (the probabilities of 16384 x 16384, depth 768: 584 us, so 4xx).  Past the last tile the
-  // copies load zeros.
+  // those stores.  Past the last tile the copies load zeros.
   template <typename Place, typename Before, typename Done>
   __device__ __forceinline__ void walk(f32x16_t (&acc)[C::kFM][C::kFN], int tiles, Place place,
                                        Before before, Done done) {
