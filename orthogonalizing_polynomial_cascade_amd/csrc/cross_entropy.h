@@ -39,7 +39,7 @@ struct HeadProduct {
 // Parts are 256-byte aligned; an offset of -1 means that the part is not needed.
 struct HeadPlan {
   int64_t x, w, part;                    // packed operands, statistics
-  int64_t scale, p, dx, planes;          // gradients
+  int64_t scale, p, dx, dx_planes, planes;   // gradients
   int64_t ldx, ldw;                      // pitches of the packed operands
   int64_t piece;                         // columns of the vocabulary at a time
   size_t bytes;

@@ -12,6 +12,7 @@
 // written and read.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cross_entropy.h"
 #include "tile_pipe.h"
@@ -160,7 +161,9 @@ __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
 void head_kernel(HeadProduct p, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
-  using S = OutStage<C::kWTN>;
+  // P leaves rounded where a wave has 64 columns, which takes half of the LDS accesses
+  constexpr bool kRounded = C::kWTN == 64;
+  using S = std::conditional_t<kRounded, OutStage16<T>, OutStage<32>>;
   static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
   static_assert(WN * BM * 8 <= C::kStage, "the statistics fit one buffer");
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
@@ -215,11 +218,17 @@ void head_kernel(HeadProduct p, int tiles_n) {
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
         const int r = fm * 32 + i * S::kRows;
-        float v[8];
-        S::get(stage, i, lane, v);
+        u32x4_t w;
+        if constexpr (kRounded) {
+          w = S::get(stage, i, lane);
+        } else {
+          float v[8];
+          S::get(stage, i, lane, v);
+          w = pack8<T>(v);
+        }
         if (r < inside)
           *reinterpret_cast<u32x4_t*>(out + r * p.ldp) =
-              counts >> S::row(i, lane) & 1 ? pack8<T>(v) : u32x4_t{};
+              counts >> S::row(i, lane) & 1 ? w : u32x4_t{};
       }
     }
   }

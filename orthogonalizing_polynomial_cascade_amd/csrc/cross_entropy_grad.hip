@@ -10,7 +10,6 @@
 //
 // Operands whose widths or addresses the copies into LDS cannot take (multiples of 8, 16 bytes) are packed
 // into the workspace once, with zeros to the next multiple of 8.
-#include <stdlib.h>
 #include <algorithm>
 #include <atomic>
 
@@ -76,22 +75,49 @@ struct InputGrad {
   int64_t ldw;
   int64_t rows;
   int cols, depth;       // width of x, entries of the piece
+  int splits;            // parts of the depth; with several, sums go to planes [splits][rows][ldsum]
+  float* planes;
   float* sum;            // [rows][ldsum] fp32, when there are several pieces
-  int64_t ldsum;
+  int64_t ldsum;         // a multiple of 8
   bool first, last;
   const float* scale;    // or null
   void* out;
   int64_t ldout;
 };
 
+// Eight sums (columns c .. c + 7 of row r) joined with those of the pieces before, and on to where they
+// belong.
+template <typename T>
+__device__ __forceinline__ void input_out(const InputGrad& p, int64_t r, int c, float back, float v[8]) {
+  float* sum = p.sum + r * p.ldsum + c;
+  if (!p.first) {
+    float before[8];
+    load_vec<float, 8>(sum, before);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += before[e];
+  }
+  if (!p.last) {
+    store_vec<float, 8>(sum, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= back;
+  T* out = static_cast<T*>(p.out) + r * p.ldout + c;
+  if (c + 8 <= p.cols) {
+    store_vec<T, 8>(out, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < p.cols) out[e] = from_f32<T>(v[e]);
+  }
+}
+
 template <typename T, bool QT, int BM, int BN, int WM, int WN, int KS, int OCC>
 __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
-void head_input_kernel(InputGrad p, int tiles_n) {
+void head_input_kernel(InputGrad p, int tiles_m, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
-  // fragments that leave side by side: 64 columns, or 32 at a time where a wave has 96
-  constexpr int kSide = C::kFN % 2 ? 1 : 2;
-  using S = OutStage<C::kWTN == 32 ? 32 : kSide * 32>;
+  using S = OutStage<C::kWTN>;
   static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
   const int lane = threadIdx.x & 63;
@@ -99,11 +125,15 @@ void head_input_kernel(InputGrad p, int tiles_n) {
   const int kg = wave_all / C::kWaves;
   const int wave = wave_all % C::kWaves;
   char* smem = smem_all + kg * C::kRing;
-  int64_t row0, end;
-  int group, tj;
-  if (!rows_place<BM>(Groups{nullptr, false, 1}, p.rows, tiles_n, &row0, &end, &group, &tj)) return;
+  const int unit = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int s = unit / (tiles_m * tiles_n);
+  int ti, tj;
+  banded(unit % (tiles_m * tiles_n), tiles_m, tiles_n, &ti, &tj);
+  const int64_t row0 = (int64_t)ti * BM;
   const int j0 = tj * BN;
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (QT ? (int64_t)j0 : j0 * p.ldw);
+  const int part = ((p.depth + kBK - 1) / kBK + p.splits - 1) / p.splits * kBK;
+  const int k0 = min(s * part, p.depth), k1 = min(k0 + part, p.depth);
+  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (QT ? j0 + k0 * p.ldw : j0 * p.ldw + k0);
   f32x16_t acc[C::kFM][C::kFN];
 #pragma unroll
   for (int fm = 0; fm < C::kFM; ++fm)
@@ -111,10 +141,10 @@ void head_input_kernel(InputGrad p, int tiles_n) {
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   float none;
   Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
-  pipe.begin(static_cast<const uint16_t*>(p.p) + row0 * p.ldp, p.ldp, end - row0, w, p.ldw,
-             p.cols - j0, p.depth, kg);
+  pipe.begin(static_cast<const uint16_t*>(p.p) + row0 * p.ldp + k0, p.ldp, p.rows - row0, w, p.ldw,
+             p.cols - j0, k1 - k0, kg);
   const int wm = wave / WN, wn = wave % WN;
-  const bool idle = row0 + wm * C::kWTM >= end;
+  const bool idle = row0 + wm * C::kWTM >= p.rows;
   if (idle) pipe.attend();
   else pipe.template run<false>(acc, 0, none);
   if constexpr (KS > 1) {
@@ -123,47 +153,39 @@ void head_input_kernel(InputGrad p, int tiles_n) {
   }
   if (idle) return;
   char* stage = pipe.spare() + wave * S::kBytes;
-  const int64_t first = row0 + wm * C::kWTM + S::row(0, lane);
+  const int c = j0 + wn * C::kWTN + S::col(lane);
   const float back = p.scale ? p.scale[1] : 1.0f;
 #pragma unroll
-  for (int fn = 0; fn < C::kFN; fn += kSide) {
-    const int c = j0 + wn * C::kWTN + fn * 32 + S::col(lane);
-    const int rows = c < p.cols ? (int)min(end - first, (int64_t)C::kWTM) : 0;
-    float* sum = p.sum + first * p.ldsum + c;
-    T* out = static_cast<T*>(p.out) + first * p.ldout + c;
+  for (int fm = 0; fm < C::kFM; ++fm) {
+    S::put(stage, acc[fm], lane);
 #pragma unroll
-    for (int fm = 0; fm < C::kFM; ++fm) {
-      f32x16_t leaving[kSide];
-#pragma unroll
-      for (int f = 0; f < kSide; ++f) leaving[f] = acc[fm][fn + f];
-      S::put(stage, leaving, lane);
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i) {
-        const int r = fm * 32 + i * S::kRows;
-        float v[8];
-        S::get(stage, i, lane, v);
-        if (r >= rows) continue;
-        if (!p.first) {
-          float before[8];
-          load_vec<float, 8>(sum + r * p.ldsum, before);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += before[e];
-        }
-        if (!p.last) {
-          store_vec<float, 8>(sum + r * p.ldsum, v);   // the pitch is a multiple of 8
-          continue;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= back;
-        if (c + 8 <= p.cols) {
-          store_vec<T, 8>(out + r * p.ldout, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < p.cols) out[r * p.ldout + e] = from_f32<T>(v[e]);
-        }
-      }
+    for (int i = 0; i < S::kPasses; ++i) {
+      const int64_t r = row0 + wm * C::kWTM + fm * 32 + S::row(i, lane);
+      float v[8];
+      S::get(stage, i, lane, v);
+      if (r >= p.rows || c >= p.cols) continue;
+      if (p.splits > 1) store_vec<float, 8>(p.planes + (s * p.rows + r) * p.ldsum + c, v);
+      else input_out<T>(p, r, c, back, v);
     }
+  }
+}
+
+// Adds the planes in order.
+template <typename T>
+__global__ __launch_bounds__(256) void input_planes_kernel(InputGrad p) {
+  const int64_t pieces = p.ldsum / 8, plane = p.rows * p.ldsum;
+  const float back = p.scale ? p.scale[1] : 1.0f;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < p.rows * pieces;
+       u += (int64_t)gridDim.x * 256) {
+    float v[8];
+    load_vec<float, 8>(p.planes + u * 8, v);
+    for (int s = 1; s < p.splits; ++s) {
+      float more[8];
+      load_vec<float, 8>(p.planes + s * plane + u * 8, more);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += more[e];
+    }
+    input_out<T>(p, u / pieces, (int)(u % pieces) * 8, back, v);
   }
 }
 
@@ -280,26 +302,59 @@ hipError_t input_tiles(const InputGrad& a, hipStream_t stream) {
   using C = Tile<BM, BN, WM, WN, KS>;
   static std::atomic<uint64_t> configured{0};
   const int64_t tiles_m = ceil64(a.rows, BM), tiles_n = ceil64(a.cols, BN);
-  return launch_lds(head_input_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured,
-                    ceil64(tiles_m * tiles_n, 8) * 8 + 8, C::kThreads, C::kLds, stream, a,
-                    (int)tiles_n);
+  hipError_t e = launch_lds(head_input_kernel<T, QT, BM, BN, WM, WN, KS, OCC>, configured,
+                            tiles_m * tiles_n * a.splits, C::kThreads, C::kLds, stream, a,
+                            (int)tiles_m, (int)tiles_n);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t pieces = a.rows * (a.ldsum / 8);
+  input_planes_kernel<T><<<dim3((unsigned)std::min<int64_t>(ceil64(pieces, 256), 8192)), 256, 0,
+                           stream>>>(a);
+  return hipGetLastError();
+}
+
+// Tile and splits of dx's product: the least of the tiles' time, by the linear layers' fits, and the
+// join's, which writes and reads each split's sums.  The depth is a piece of the vocabulary, so few rows
+// leave most CUs idle for long without splits.
+struct InputPlan {
+  RowsTile tile;
+  int splits;
+};
+
+InputPlan input_plan(int64_t rows, int64_t cols, int64_t depth) {
+  const double slabs = (double)std::max<int64_t>(1, ceil64(depth, kBK));
+  const double bytes = 4.0 * (double)rows * (double)cols;
+  InputPlan best{kRows256, 1};
+  double least = 0;
+  for (RowsTile t : {kRows256, kRows128, kRows64, kRows32x128, kRows32}) {
+    const double tiles = (double)ceil64(rows, kTileRows[t]) * (double)ceil64(cols, kTileCols[t]);
+    if (t != kRows256 && tiles > kMaxTileGrid) continue;
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      const double each = std::ceil(slabs / splits), groups = tiles * splits;
+      if (splits > 1 && (each < 8 || groups > kMaxTileGrid || splits * bytes > 2.7e8)) break;
+      double cost = 0;
+      switch (t) {
+        case kRows32: cost = rounds(groups, 256) * (4.5 + 0.7 * std::ceil(each / 8)); break;
+        case kRows32x128: cost = rounds(groups, 512) * (4.5 + 0.6 * std::ceil(each / 2)); break;
+        default: cost = tile_cost(kTileRows[t], groups, each, false); break;
+      }
+      if (splits > 1) cost += 5.0 + (2 * splits + 1) * bytes / 5e6;
+      if ((t == kRows256 && splits == 1) || cost < least) {
+        best = {t, splits};
+        least = cost;
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T, bool QT>
-hipError_t input_variant(const InputGrad& a, hipStream_t stream) {
-  RowsProduct r{};
-  r.rows = a.rows;
-  r.cols = a.cols;
-  r.depth = a.depth;
-  r.groups = Groups{nullptr, false, 1};
-  switch (rows_tile_that_fits(r)) {
+hipError_t input_variant(const InputGrad& a, RowsTile tile, hipStream_t stream) {
+  switch (tile) {
     case kRows32: return input_tiles<T, QT, 32, 32, 1, 1, 8, 2>(a, stream);
     case kRows32x128: return input_tiles<T, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return input_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return input_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
-    default:
-      if (getenv("X192")) return input_tiles<T, QT, 256, 192, 4, 2, 1, 2>(a, stream);
-      return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
+    default: return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
   }
 }
 
@@ -328,12 +383,24 @@ WeightPlan plan_of(int64_t rows, int64_t vocab, int64_t depth, bool w_kn) {
   return weight_plan(a);
 }
 
-// Columns of the vocabulary at a time: P of a piece takes up to 2^28 elements.
-int64_t piece_of(int64_t rows, int64_t vocab) {
-  const int64_t most = std::max<int64_t>(1024, (int64_t(1) << 28) / std::max<int64_t>(rows, 1) / 256 * 256);
-  if (getenv("PIECE")) return std::min<int64_t>(atoi(getenv("PIECE")), ceil8(vocab));
-  return std::min(most, ceil8(vocab));
+// Columns of the vocabulary at a time: as many as give dW whole rounds of 256x256 tiles on the CUs, with
+// up to 2^29 elements of P.  Loss and gradients of 16384 rows, 768 x 50304: 5610 us by 21760 columns
+// (255 tiles of dW), 5690 by 16384 (192), 5790 by 25344 (297).
+int64_t piece_of(int64_t rows, int64_t vocab, int64_t depth) {
+  const int64_t most =
+      std::max<int64_t>(1024, (int64_t(1) << 29) / std::max<int64_t>(rows, 1) / 256 * 256);
+  if (most >= vocab) return ceil8(vocab);
+  const int64_t across = ceil64(depth, 256);
+  for (int64_t m = most / 256 * across / 256; m >= 1; --m) {
+    const int64_t cols = 256 * m / across * 256;
+    if (cols <= most && cols >= 1024) return cols;
+  }
+  return most;
 }
+
+// Elements from one row of P to the next.  Rows a multiple of 1 KB apart would share the memory channels:
+// dx of 16384 rows, 16384 deep 484 us, 457 with a line more.
+int64_t p_pitch(int64_t cols) { return ceil8(cols) + (ceil8(cols) % 512 == 0 ? 64 : 0); }
 
 hipError_t pack(const void* from, int64_t ld, int64_t rows, int64_t width, void* to, int64_t pitch,
                 hipStream_t stream) {
@@ -388,7 +455,7 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
     const int64_t cols = std::min(plan.piece, a.vocab - v);
     p.first = v;
     p.cols = cols;
-    p.ldp = ceil8(cols) + 64;
+    p.ldp = p_pitch(cols);
     e = launch_head_probabilities(p, stream);
     if (e != hipSuccess) return e;
     if (a.dx) {
@@ -399,10 +466,14 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
       g.rows = a.rows; g.cols = a.depth; g.depth = (int)cols;
       g.sum = plan.dx >= 0 ? reinterpret_cast<float*>(ws + plan.dx) : nullptr;
       g.ldsum = ceil8(a.depth);
+      const InputPlan tiles = input_plan(a.rows, a.depth, cols);
+      g.splits = tiles.splits;
+      g.planes = plan.dx_planes >= 0 ? reinterpret_cast<float*>(ws + plan.dx_planes) : nullptr;
       g.first = v == 0; g.last = v + cols == a.vocab;
       g.scale = p.scale;
       g.out = a.dx; g.ldout = a.lddx;
-      e = a.w_kn ? input_variant<T, false>(g, stream) : input_variant<T, true>(g, stream);
+      e = a.w_kn ? input_variant<T, false>(g, tiles.tile, stream)
+                 : input_variant<T, true>(g, tiles.tile, stream);
       if (e != hipSuccess) return e;
     }
     if (a.dw) {
@@ -435,7 +506,7 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
 
 HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f16, int in_place,
                    int64_t rows, int64_t vocab, int64_t depth) {
-  HeadPlan plan{-1, -1, -1, -1, -1, -1, -1, ceil8(depth), ceil8(w_kn ? vocab : depth), 0, 0};
+  HeadPlan plan{-1, -1, -1, -1, -1, -1, -1, -1, ceil8(depth), ceil8(w_kn ? vocab : depth), 0, 0};
   auto take = [&](int64_t bytes) {
     const int64_t at = (int64_t)plan.bytes;
     plan.bytes += (size_t)((bytes + 255) / 256 * 256);
@@ -447,10 +518,16 @@ HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f1
     plan.part = take(rows * head_stat_tiles(rows, vocab, (int)depth) * 8);
     return plan;
   }
-  plan.piece = piece_of(rows, vocab);
+  plan.piece = piece_of(rows, vocab, depth);
   if (f16) plan.scale = take(8);
   plan.p = take(rows * (plan.piece + 64) * 2);
   if (want_dx && plan.piece < vocab) plan.dx = take(rows * ceil8(depth) * 4);
+  if (want_dx) {
+    int splits = 1;
+    for (int64_t cols : {std::min(plan.piece, vocab), vocab % plan.piece})   // and the last piece
+      if (cols) splits = std::max(splits, input_plan(rows, depth, cols).splits);
+    if (splits > 1) plan.dx_planes = take(splits * rows * ceil8(depth) * 4);
+  }
   if (want_dw) {
     int64_t words = 0;
     for (int64_t cols : {std::min(plan.piece, vocab), vocab % plan.piece}) {   // and the last piece

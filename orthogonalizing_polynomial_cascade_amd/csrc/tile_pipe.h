@@ -31,14 +31,11 @@ struct SlabStream {
   // K-contiguous one, which exchanges the halves of the slab's k.
   static constexpr int kStep = KMAJOR ? NW * (512 / ROWS) : NW * (512 / kBK);
   static constexpr bool kHalf = !KMAJOR && kStep == 8;
-  static_assert(kInsts == 1 || kHalf || (KMAJOR && 512 % ROWS != 0) ||
-                    kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
+  static_assert(kInsts == 1 || kHalf || kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
   // K-major instructions differ by a uniform offset (soff); K-contiguous ones by rows that have to
-  // be checked against the edge one by one; K-major ones of 192 rows begin anywhere in a row
-  static constexpr bool kAny = KMAJOR && 512 % ROWS != 0;
-  static constexpr int kOffs = KMAJOR && !kAny ? 1 : kInsts;
-  uint32_t off[kOffs];
-  int kin[kAny ? kInsts : 1];   // the lane's k within the slab (of its first instruction)
+  // be checked against the edge one by one
+  uint32_t off[KMAJOR ? 1 : kInsts];
+  int kin;                 // the lane's k within the slab (of its first instruction)
   uint32_t soff;           // K-major: bytes from one instruction to the next
   uint64_t base, step;
 
@@ -48,10 +45,6 @@ struct SlabStream {
       constexpr int kSlots = kBK / 8;
       *row = (64 / kSlots) * u + lane / kSlots;
       *c = (lane % kSlots) ^ KContig<ROWS, kBK>::swz(*row);
-    } else if constexpr (kAny) {
-      constexpr int kSlots = ROWS / 8;
-      *row = (u * 64 + lane) / kSlots;
-      *c = ((u * 64 + lane) % kSlots) ^ KMajor<ROWS>::swz(*row);
     } else {
       constexpr int kSlots = ROWS / 8;
       *row = u * (512 / ROWS) + lane / kSlots;
@@ -64,17 +57,16 @@ struct SlabStream {
                                        int lane) {
     base = reinterpret_cast<uint64_t>(origin);
     step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
-    soff = KMAJOR && !kAny ? (uint32_t)ld * (2 * kStep) : 0;
+    soff = KMAJOR ? (uint32_t)ld * (2 * kStep) : 0;
     int row, c;
     piece(0, wave, lane, &row, &c);
-    kin[0] = KMAJOR ? row : c * 8;
+    kin = KMAJOR ? row : c * 8;
 #pragma unroll
-    for (int i = 0; i < kOffs; ++i) {
+    for (int i = 0; i < (KMAJOR ? 1 : kInsts); ++i) {
       piece(i, wave, lane, &row, &c);
       off[i] = (KMAJOR ? c * 8 : row) < rows
                    ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u
                    : kOOB;
-      if constexpr (kAny) kin[i] = row;
     }
   }
 
@@ -83,13 +75,11 @@ struct SlabStream {
   __device__ __forceinline__ void issue(int i, uint32_t dst, int left, int wave) const {
     const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
     const uint32_t to = dst + (uint32_t)(wave + i * NW) * 1024u;
-    if constexpr (kAny) {
-      dma16(rsrc, to, kin[i] < left ? off[i] : kOOB);
-    } else if constexpr (KMAJOR) {
-      dma16(rsrc, to, kin[0] < left - i * kStep ? off[0] : kOOB,
+    if constexpr (KMAJOR) {
+      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB,
             (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)i * soff)));
     } else {
-      const int k = kHalf && (i & 1) ? kin[0] ^ (kBK / 2) : kin[0];
+      const int k = kHalf && (i & 1) ? kin ^ (kBK / 2) : kin;
       dma16(rsrc, to, k < left ? off[i] : kOOB);
     }
   }

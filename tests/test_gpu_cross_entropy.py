@@ -87,7 +87,7 @@ def test_large_tiles(gpu_lib, rows, vocab, k, w_kn):
 @pytest.mark.parametrize("w_kn", [False, True])
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 def test_several_pieces(gpu_lib, w_kn, kind):
-    """So many rows that the vocabulary is taken in pieces (of 1024 entries here), the last of them ragged: the pieces'
+    """So many rows that the vocabulary is taken in pieces (of 1792 entries here), the last of them ragged: the pieces'
     sums against the same in 64 bits, for some rows and entries, and for all in one against the other layout."""
     t, rows, vocab, k = TYPES[kind], 270000, 2500, 16
     x, w = _mat(rows, k, t, 1), _weight(vocab, k, t, 2, w_kn)
