@@ -1098,10 +1098,12 @@ class AdamW:
             row.param, row.mantissa, row.count, row.param_dtype = p.data_ptr(), low, n, code
             row.m, row.v, row.m_scale, row.v_scale = at["m"], at["v"], at["m_scale"], at["v_scale"]
             row.lr_mul, row.wd_mul, row.state_bits = lr_mul[i], wd_mul[i], bits[i]
+        self._plan = None
         self.bind(grads)
 
     def bind(self, grads):
-        """Takes the gradients from other tensors from the next step on."""
+        """Takes the gradients from other tensors from the next step on, a captured step's replays too.  It
+        writes the plan on the current stream: steps on other streams have to be ordered with it."""
         torch = _module()
         grads = list(grads)
         if len(grads) != len(self.params):
@@ -1118,8 +1120,13 @@ class AdamW:
         self.plan_bytes = int(lib.anvil_adamw_plan_bytes(table, count))
         host = (ctypes.c_int64 * max(1, self.plan_bytes // 8))()
         _check("anvil_adamw_plan", lib.anvil_adamw_plan(table, count, ctypes.cast(host, _vp), self.plan_bytes))
-        # the copy from pageable memory has ended when this returns, whatever stream a step runs on
-        self._plan = torch.frombuffer(host, dtype=torch.int64).to(f"cuda:{self.device}") if count else None
+        # the copy from pageable memory has ended when this returns, whatever stream a step runs on; a plan
+        # stays where it is, so that a captured step follows
+        words = torch.frombuffer(host, dtype=torch.int64)
+        if self._plan is None:
+            self._plan = words.to(f"cuda:{self.device}") if count else None
+        else:
+            self._plan.copy_(words)
 
     def _arguments(self, grad_scale, stream):
         """(plan, its bytes, tensors), the grad_scale pointer and the stream's handle of a step."""

@@ -317,6 +317,23 @@ def test_replayed_graph(gpu_lib):
         assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
 
 
+def test_captured_step_follows_its_gradients(gpu_lib):
+    """bind() after a capture: the replay reads the new gradients, wherever the old ones went."""
+    s = _state(5000, "fp32", "bf16", 32, 1)
+    plan, again = _plan(gpu_lib, [s]), _plan(gpu_lib, [s])
+    gpu_lib.anvil_adamw(plan, 0.0, 1)      # outside capture first
+    for a, b in ((plan.m, again.m), (plan.v, again.v), (plan.params, again.params)):
+        a[0].copy_(b[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gpu_lib.anvil_adamw(plan, 1e-3, 1, betas=BETAS, eps=EPS, weight_decay=0.1)
+    other = dict(s, grad=_state(5000, "fp32", "fp16", 32, 2)["grad"])
+    plan.bind([other["grad"].cuda()])
+    graph.replay()
+    _compare(plan, [A.step32(other, 0, 1e-3, 0.1, BETAS, EPS, 1, None, 1)])
+
+
 def test_other_stream(gpu_lib):
     s = _state(100000, "fp32", "fp32", 8, 1)
     plan, side = _plan(gpu_lib, [s]), torch.cuda.Stream()
