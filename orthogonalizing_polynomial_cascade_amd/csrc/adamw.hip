@@ -43,22 +43,24 @@ using eight = T __attribute__((ext_vector_type(8), aligned(sizeof(T))));
 template <bool FULL, typename T>
 __device__ __forceinline__ eight<T> load8(const void* base, int64_t at, int n) {
   const global_ptr<const T> p = (global_ptr<const T>)base + at;
-  if constexpr (FULL) {
-    return *(global_ptr<const eight<T>>)p;
-  } else {
-    eight<T> v;
+  if (FULL || n >= kPer) return *(global_ptr<const eight<T>>)p;
+  eight<T> v;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] = e < n ? p[e] : T(0);
-    return v;
+  for (int e = 0; e < kPer; ++e) v[e] = T(0);
+  if (n > 0) {   // the tensor's last lane
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (e < n) v[e] = p[e];
   }
+  return v;
 }
 
 template <bool FULL, typename T>
 __device__ __forceinline__ void store8(void* base, int64_t at, int n, eight<T> v) {
   const global_ptr<T> p = (global_ptr<T>)base + at;
-  if constexpr (FULL) {
+  if (FULL || n >= kPer) {
     *(global_ptr<eight<T>>)p = v;
-  } else {
+  } else if (n > 0) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
       if (e < n) p[e] = v[e];

@@ -22,33 +22,28 @@ namespace {
 
 int64_t ceil8(int64_t v) { return (v + 7) / 8 * 8; }
 
-// to [rows][pitch] = from [rows][width] at ld, zeros from width to pitch.  16-bit elements.
-__global__ __launch_bounds__(256) void head_pack_kernel(const uint16_t* from, int64_t ld,
-                                                        int64_t rows, int64_t width, uint16_t* to,
-                                                        int64_t pitch) {
-  const int64_t pieces = pitch / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pieces;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / pieces, c = i % pieces * 8;
-    const uint16_t* at = from + r * ld + c;
-    uint16_t v[8];
-    if (c + 8 <= width) {
-      __builtin_memcpy(v, at, 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = c + e < width ? at[e] : (uint16_t)0;
-    }
-    __builtin_memcpy(to + r * pitch + c, v, 16);
-  }
-}
+// What a call has to prepare, in one launch: copies [rows][width] -> [rows][pitch] of 16-bit elements
+// with zeros from width to pitch, and the scale of P.
+struct PackedCopy {
+  const uint16_t* from;
+  int64_t ld, rows, width;
+  uint16_t* to;          // null: nothing to copy
+  int64_t pitch;         // a multiple of 8
+};
+struct HeadReady {
+  PackedCopy copy[2];
+  const float* dloss;
+  int64_t rows;
+  float* scale;          // {S, 1 / S}, or null
+};
+constexpr int kReadyThreads = 1024;
 
-// scale = {S, 1 / S}: S the power of two that takes the largest finite |dloss| to [2^14, 2^15).
-__global__ __launch_bounds__(1024) void head_scale_kernel(const float* dloss, int64_t rows,
-                                                          float* scale) {
-  __shared__ float wave_top[16];
+// S the power of two that takes the largest finite |dloss| to [2^14, 2^15).
+__device__ __forceinline__ void find_scale(const HeadReady& p) {
+  __shared__ float wave_top[kReadyThreads / 64];
   float top = 0.0f;
-  for (int64_t r = threadIdx.x; r < rows; r += 1024) {
-    const float v = fabsf(dloss[r]);
+  for (int64_t r = threadIdx.x; r < p.rows; r += kReadyThreads) {
+    const float v = fabsf(p.dloss[r]);
     if (v > top && v < INFINITY) top = v;
   }
 #pragma unroll
@@ -56,14 +51,39 @@ __global__ __launch_bounds__(1024) void head_scale_kernel(const float* dloss, in
   if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, wave_top[i]);
+    for (int i = 1; i < kReadyThreads / 64; ++i) top = fmaxf(top, wave_top[i]);
     int power = 0;
     if (top > 0.0f) {
       frexpf(top, &power);                       // top in [2^(power - 1), 2^power)
       power = min(max(15 - power, -120), 120);   // S and 1 / S stay normal numbers
     }
-    scale[0] = ldexpf(1.0f, power);
-    scale[1] = ldexpf(1.0f, -power);
+    p.scale[0] = ldexpf(1.0f, power);
+    p.scale[1] = ldexpf(1.0f, -power);
+  }
+}
+
+// Workgroup 0 finds the scale where there is one; the others copy.
+__global__ __launch_bounds__(kReadyThreads) void head_ready_kernel(HeadReady p) {
+  const int first = p.scale ? 1 : 0;
+  if ((int)blockIdx.x < first) return find_scale(p);
+  const int64_t me = (int64_t)(blockIdx.x - first) * kReadyThreads + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - first) * kReadyThreads;
+  for (int k = 0; k < 2; ++k) {
+    const PackedCopy& c = p.copy[k];
+    if (!c.to) continue;
+    const int64_t pieces = c.pitch / 8;
+    for (int64_t i = me; i < c.rows * pieces; i += step) {
+      const int64_t r = i / pieces, at = i % pieces * 8;
+      const uint16_t* from = c.from + r * c.ld + at;
+      uint16_t v[8];
+      if (at + 8 <= c.width) {
+        __builtin_memcpy(v, from, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = at + e < c.width ? from[e] : (uint16_t)0;
+      }
+      __builtin_memcpy(c.to + r * c.pitch + at, v, 16);
+    }
   }
 }
 
@@ -179,6 +199,7 @@ __global__ __launch_bounds__(256) void input_planes_kernel(InputGrad p) {
        u += (int64_t)gridDim.x * 256) {
     float v[8];
     load_vec<float, 8>(p.planes + u * 8, v);
+#pragma unroll 8
     for (int s = 1; s < p.splits; ++s) {
       float more[8];
       load_vec<float, 8>(p.planes + s * plane + u * 8, more);
@@ -281,6 +302,7 @@ __global__ __launch_bounds__(256) void head_planes_kernel(WeightGrad p) {
        u += (int64_t)gridDim.x * 256) {
     float v[8];
     load_vec<float, 8>(p.planes + u * 8, v);
+#pragma unroll 8
     for (int s = 1; s < p.splits; ++s) {
       float more[8];
       load_vec<float, 8>(p.planes + s * plane + u * 8, more);
@@ -402,16 +424,7 @@ int64_t piece_of(int64_t rows, int64_t vocab, int64_t depth) {
 // dx of 16384 rows, 16384 deep 484 us, 457 with a line more.
 int64_t p_pitch(int64_t cols) { return ceil8(cols) + (ceil8(cols) % 512 == 0 ? 64 : 0); }
 
-hipError_t pack(const void* from, int64_t ld, int64_t rows, int64_t width, void* to, int64_t pitch,
-                hipStream_t stream) {
-  const int64_t pieces = rows * (pitch / 8);
-  if (pieces == 0) return hipSuccess;
-  head_pack_kernel<<<dim3((unsigned)std::min<int64_t>(ceil64(pieces, 256), 16384)), 256, 0, stream>>>(
-      static_cast<const uint16_t*>(from), ld, rows, width, static_cast<uint16_t*>(to), pitch);
-  return hipGetLastError();
-}
-
-// The call's operands as the tiles read them, packed where that is needed.
+// The call's operands as the tiles read them, packed where that is needed, and P's scale.
 hipError_t ready(const HeadCall& a, const HeadPlan& plan, char* ws, HeadProduct* p,
                  hipStream_t stream) {
   *p = HeadProduct{};
@@ -420,20 +433,33 @@ hipError_t ready(const HeadCall& a, const HeadPlan& plan, char* ws, HeadProduct*
   p->w_kn = a.w_kn; p->f16 = a.f16;
   p->rows = a.rows; p->depth = a.depth; p->vocab = a.vocab;
   p->targets = a.targets; p->wide = a.wide;
+  HeadReady r{};
+  int64_t pieces = 0;
   if (plan.x >= 0) {
-    const hipError_t e = pack(a.x, a.ldx, a.rows, a.depth, ws + plan.x, plan.ldx, stream);
-    if (e != hipSuccess) return e;
-    p->x = ws + plan.x;
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws + plan.x);
+    r.copy[0] = {static_cast<const uint16_t*>(a.x), a.ldx, a.rows, a.depth, to, plan.ldx};
+    p->x = to;
     p->ldx = plan.ldx;
+    pieces += a.rows * (plan.ldx / 8);
   }
   if (plan.w >= 0) {
-    const hipError_t e = pack(a.w, p->ldw, a.w_kn ? a.depth : a.vocab, p->ldw, ws + plan.w, plan.ldw,
-                              stream);
-    if (e != hipSuccess) return e;
-    p->w = ws + plan.w;
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws + plan.w);
+    r.copy[1] = {static_cast<const uint16_t*>(a.w), p->ldw, a.w_kn ? a.depth : a.vocab, p->ldw, to,
+                 plan.ldw};
+    p->w = to;
     p->ldw = plan.ldw;
+    pieces += r.copy[1].rows * (plan.ldw / 8);
   }
-  return hipSuccess;
+  if (plan.scale >= 0) {
+    r.dloss = a.dloss;
+    r.rows = a.rows;
+    r.scale = reinterpret_cast<float*>(ws + plan.scale);
+    p->scale = r.scale;
+  }
+  const int64_t grid = std::min<int64_t>(ceil64(pieces, kReadyThreads), 4096) + (r.scale ? 1 : 0);
+  if (grid == 0) return hipSuccess;
+  head_ready_kernel<<<dim3((unsigned)grid), kReadyThreads, 0, stream>>>(r);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -444,13 +470,6 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
   p.lse = a.lse;
   p.dloss = a.dloss;
   p.p = ws + plan.p;
-  if (plan.scale >= 0) {
-    float* scale = reinterpret_cast<float*>(ws + plan.scale);
-    head_scale_kernel<<<1, 1024, 0, stream>>>(a.dloss, a.rows, scale);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    p.scale = scale;
-  }
   for (int64_t v = 0; v < a.vocab; v += plan.piece) {
     const int64_t cols = std::min(plan.piece, a.vocab - v);
     p.first = v;
