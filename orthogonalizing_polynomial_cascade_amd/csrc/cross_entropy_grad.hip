@@ -87,6 +87,23 @@ __global__ __launch_bounds__(kReadyThreads) void head_ready_kernel(HeadReady p) 
   }
 }
 
+// v = the sum over the planes of their eight words at `from`, in order; four planes' loads at a time (one
+// after the other they took 0.34 us each, 11 of a call of five rows).
+__device__ __forceinline__ void sum_planes(const float* from, int64_t plane, int splits, float v[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  for (int s = 0; s < splits; s += 4) {
+    float t[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_vec<float, 8>(from + min(s + k, splits - 1) * plane, t[k]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += s + k < splits ? t[k][e] : 0.0f;
+  }
+}
+
 // One piece's part of dx.
 struct InputGrad {
   const void* p;         // [rows][ldp], columns up to `depth`
@@ -198,14 +215,7 @@ __global__ __launch_bounds__(256) void input_planes_kernel(InputGrad p) {
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < p.rows * pieces;
        u += (int64_t)gridDim.x * 256) {
     float v[8];
-    load_vec<float, 8>(p.planes + u * 8, v);
-#pragma unroll 8
-    for (int s = 1; s < p.splits; ++s) {
-      float more[8];
-      load_vec<float, 8>(p.planes + s * plane + u * 8, more);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += more[e];
-    }
+    sum_planes(p.planes + u * 8, plane, p.splits, v);
     input_out<T>(p, u / pieces, (int)(u % pieces) * 8, back, v);
   }
 }
@@ -301,14 +311,7 @@ __global__ __launch_bounds__(256) void head_planes_kernel(WeightGrad p) {
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < p.ni * pieces;
        u += (int64_t)gridDim.x * 256) {
     float v[8];
-    load_vec<float, 8>(p.planes + u * 8, v);
-#pragma unroll 8
-    for (int s = 1; s < p.splits; ++s) {
-      float more[8];
-      load_vec<float, 8>(p.planes + s * plane + u * 8, more);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += more[e];
-    }
+    sum_planes(p.planes + u * 8, plane, p.splits, v);
     weight_out<T>(p, u / pieces, (int)(u % pieces) * 8, back, v);
   }
 }
