@@ -193,6 +193,57 @@ def test_ignored_rows_hold_anything(gpu_lib):
         assert torch.equal(dw, want[1])
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """More than 2^32 logits, several pieces of more than 2^28 probabilities: the last rows' loss and dx, and dw of rows at
+    both ends of the batch (the others have no target)."""
+    t, rows, vocab, k = torch.bfloat16, 150000, 33000, 64
+    x, w = _mat(rows, k, t, 1), _weight(vocab, k, t, 2, True)
+    targets = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    some = torch.cat([torch.arange(40), torch.arange(rows - 40, rows)]).cuda()
+    targets[some] = _targets(80, vocab, 3, torch.int32)
+    loss, lse = gpu_lib.anvil_cross_entropy(x, w, targets, w_kn=True)
+    dloss = torch.full((rows,), 1 / 80, device="cuda")
+    dx, dw = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, dloss, w_kn=True, out_dtype=torch.float32)
+    xs, ts = x[some].cpu(), targets[some]
+    (lw, el), (sw, es) = C.forward(xs, w.cpu(), ts, True)
+    H.assert_within(loss[some], lw, el, "loss")
+    H.assert_within(lse[some], sw, es, "lse")
+    (xw, ex), (ww, ew) = C.gradients(xs, w.cpu(), ts, lse[some], dloss[some], True, t)
+    H.assert_within(dx[some], xw, ex + H.half_step(xw, t), "dx")
+    H.assert_within(dw, ww, ew + H.half_step(ww, torch.float32), "dw")
+    assert not loss[40:-40].any() and not dx[40:-40].any()
+
+
+def test_no_targets(gpu_lib):
+    """Every row ignored: no loss and no gradient, and none of them NaN."""
+    for t in TYPES.values():
+        x, w = _mat(70, 40, t, 1), _weight(300, 40, t, 2, False)
+        targets = torch.full((70,), -100, device="cuda")
+        loss, lse = gpu_lib.anvil_cross_entropy(x, w, targets)
+        dx, dw = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, torch.zeros(70, device="cuda"))
+        assert torch.isfinite(lse).all() and not loss.any() and not dx.any() and not dw.any()
+        assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+def test_a_single_row_of_any_pitch(gpu_lib):
+    t, far = torch.bfloat16, (1 << 22) + 8
+    for k in (64, 45):
+        _check(gpu_lib, _mat(2, k, t, 1, pitch=far)[1:], _weight(900, k, t, 2, False), _targets(1, 900, 3), False, t)
+
+
+def test_infinite_logits(gpu_lib):
+    """An infinity or NaN in a row makes that row's loss NaN or infinite, no other's."""
+    t = torch.bfloat16
+    x, w, targets = _mat(300, 64, t, 1), _weight(900, 64, t, 2, False), _targets(300, 900, 3, ignored=False)
+    clean, _ = gpu_lib.anvil_cross_entropy(x, w, targets)
+    x[5, 1], x[200, 0], x[299, 63] = float("inf"), float("nan"), -float("inf")
+    loss, lse = gpu_lib.anvil_cross_entropy(x, w, targets)
+    rest = torch.ones(300, dtype=torch.bool, device="cuda")
+    rest[[5, 200, 299]] = False
+    assert torch.equal(loss[rest], clean[rest]) and not torch.isfinite(loss[~rest]).any()
+    assert not torch.isfinite(lse[~rest]).any()
+
+
 def test_empty(gpu_lib):
     t = torch.bfloat16
     w = _weight(50, 16, t, 1, False)

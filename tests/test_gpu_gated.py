@@ -140,6 +140,32 @@ def test_experts(gpu_lib, n, k, w_kn, offsets):
             H.assert_within(dz[s], want, err + H.half_step(want, t), f"dz {i}")
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """z and dz of more than 2^32 elements: their last rows, by the tiles and by the kernels of any width."""
+    t, rows = torch.bfloat16, 800000
+    for n, k in ((2816, 64), (2817, 33)):
+        x, w, down = _mat(rows, k, t, 1), _weight(2 * n, k, t, 2, False), _weight(k, n, t, 3, False)
+        assert rows * 2 * n > 1 << 32
+        y, z = gpu_lib.anvil_gated_linear(x, w, keep_preact=True)
+        dz = gpu_lib.anvil_gated_grad_input(x, down, z)
+        part = slice(rows - 70, rows)
+        h, eh, zw, ez = G.forward(x[part].cpu(), w.cpu(), None, "silu", False)
+        H.assert_within(y[part], h, eh + H.half_step(h, t), "y")
+        H.assert_within(z[part], zw, ez + H.half_step(zw, t), "z")
+        want, err = G.grad(x[part].cpu(), down.cpu(), z[part].cpu(), "silu", False)
+        H.assert_within(dz[part], want, err + H.half_step(want, t), "dz")
+        del x, w, y, z, dz
+
+
+def test_a_single_row_of_any_pitch(gpu_lib):
+    """The last row of a tensor whose rows lie further apart than a pitch may be."""
+    t, far = torch.bfloat16, (1 << 22) + 8
+    x = _mat(2, 72, t, 1, pitch=far)[1:]
+    w, down = _weight(2 * 40, 72, t, 2, False), _weight(72, 40, t, 3, False)
+    _check_forward(gpu_lib, x, w, None, "silu", False, True, t)
+    _check_grad(gpu_lib, x, down, _mat(2, 80, t, 4, pitch=far)[1:], "silu", False, t)
+
+
 def test_empty(gpu_lib):
     t = torch.bfloat16
     for rows, n, k in ((0, 16, 8), (3, 0, 8)):
