@@ -26,13 +26,12 @@ struct HeadProduct {
   // target's logit
   float2* part;
   float* loss;
-  // probabilities: p [rows][ldp] = (softmax - onehot) * dloss * (scale ? scale[0] : 1), zeros from cols to
-  // ldp; rows without a target zeros
+  // probabilities: p = (softmax - onehot) * dloss * (scale ? scale[0] : 1), rows without a target zeros,
+  // in blocks of 64 columns, [ceil(cols / 64)][rows][64], zeros from cols to the next multiple of 8
   const float* lse;
   const float* dloss;
   const float* scale;
   void* p;
-  int64_t ldp;
 };
 
 // The same for a caller's operands of any width, pitch and alignment: what of the workspace a call takes.

@@ -206,8 +206,8 @@ void head_kernel(HeadProduct p, int tiles_n) {
     if (kg > 0 || idle) return;
     char* stage = pipe.spare() + wave * S::kBytes;
     const int64_t c = c0 + S::col(lane), first = r0 + S::row(0, lane);
-    const int inside = c < p.ldp ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
-    T* out = static_cast<T*>(p.p) + first * p.ldp + c;
+    const int inside = c < p.cols ? (int)min(p.rows - first, (int64_t)C::kWTM) : 0;
+    T* out = static_cast<T*>(p.p) + (c / 64 * p.rows + first) * 64 + c % 64;
     if (c0 + C::kWTN > p.cols) mask_columns(acc, (int)(p.cols - c0) - 4 * (lane >> 5));
 #pragma unroll
     for (int fm = 0; fm < C::kFM; ++fm) {
@@ -227,7 +227,7 @@ void head_kernel(HeadProduct p, int tiles_n) {
           w = pack8<T>(v);
         }
         if (r < inside)
-          *reinterpret_cast<u32x4_t*>(out + r * p.ldp) =
+          *reinterpret_cast<u32x4_t*>(out + r * 64) =
               counts >> S::row(i, lane) & 1 ? w : u32x4_t{};
       }
     }

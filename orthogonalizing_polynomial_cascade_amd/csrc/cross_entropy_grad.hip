@@ -4,7 +4,8 @@
 // vocabulary at a time (cross_entropy.hip), rounded to the operands' type as the matrix cores take it, and
 // both products read it: dW of the piece is complete, dx is summed over the pieces in fp32.  An fp16 P is
 // scaled by a power of two so that the largest |dloss| comes to 2^14 (a mean over 16384 rows alone would push
-// probabilities below 2^-10 under fp16's range); the products are scaled back in fp32, exactly.  The
+// probabilities below 2^-10 under fp16's range); the products are scaled back in fp32, exactly.  P lies in
+// blocks of 64 columns, so that the slabs of both products are contiguous.  The
 // rounding of P is each element's own, at most half a step of its type: it adds to a sum of many of them
 // what the roundings of the inputs already did.
 //
@@ -106,8 +107,7 @@ __device__ __forceinline__ void sum_planes(const float* from, int64_t plane, int
 
 // One piece's part of dx.
 struct InputGrad {
-  const void* p;         // [rows][ldp], columns up to `depth`
-  int64_t ldp;
+  const void* p;         // [ceil(depth / 64)][rows][64]
   const void* w;         // of the piece's first entry
   int64_t ldw;
   int64_t rows;
@@ -178,8 +178,10 @@ void head_input_kernel(InputGrad p, int tiles_m, int tiles_n) {
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   float none;
   Pipe<T, false, QT, BM, BN, WM, WN, KS> pipe(smem, wave);
-  pipe.begin(static_cast<const uint16_t*>(p.p) + row0 * p.ldp + k0, p.ldp, p.rows - row0, w, p.ldw,
-             p.cols - j0, k1 - k0, kg);
+  const uint16_t* block0 = static_cast<const uint16_t*>(p.p);
+  pipe.begin(block0, 64, 0, w, p.ldw, p.cols - j0, k1 - k0, kg);
+  pipe.sp.init_blocks(block0 + ((k0 / 64 + (KS > 1 ? kg * pipe.KT : 0)) * p.rows + row0) * 64,
+                      p.rows * 64, p.rows - row0, wave, lane);
   const int wm = wave / WN, wn = wave % WN;
   const bool idle = row0 + wm * C::kWTM >= p.rows;
   if (idle) pipe.attend();
@@ -220,12 +222,12 @@ __global__ __launch_bounds__(256) void input_planes_kernel(InputGrad p) {
   }
 }
 
-// dW of one piece: out[i][j] = sum_r p[r][i] q[r][j], one of the two P and the other x.
+// dW of one piece: out[i][j] = the sum over the rows of P(r, i) x(r, j), or of x(r, i) P(r, j).
 struct WeightGrad {
-  const void* p;
-  int64_t ldp;
-  const void* q;
-  int64_t ldq;
+  const void* p;         // [ceil(entries / 64)][rows][64]
+  const void* x;
+  int64_t ldx;
+  bool p_second;         // P(r, j)
   int64_t rows;
   int ni, nj;
   int splits;            // parts of the rows; with several, sums go to planes [splits][ni][ceil8(nj)]
@@ -280,8 +282,13 @@ void head_weight_kernel(WeightGrad p, int tiles_i, int tiles_j) {
     for (int fn = 0; fn < C::kFN; ++fn) acc[fm][fn] = f32x16_t{};
   float none;
   Pipe<T, true, true, BM, BN, WM, WN, 1> pipe(smem, wave);
-  pipe.begin(static_cast<const uint16_t*>(p.p) + k0 * p.ldp + i0, p.ldp, p.ni - i0,
-             static_cast<const uint16_t*>(p.q) + k0 * p.ldq + j0, p.ldq, p.nj - j0, k1 - k0, 0);
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + k0 * p.ldx;
+  const uint16_t* blocks = static_cast<const uint16_t*>(p.p);
+  const int64_t block = p.rows * 64;
+  pipe.begin(x + i0, p.ldx, p.ni - i0, x + j0, p.ldx, p.nj - j0, k1 - k0, 0);
+  // (tiles begin at multiples of 64)
+  if (p.p_second) pipe.sq[0].init_blocks(blocks + j0 / 64 * block + k0 * 64, block, p.nj - j0, wave, lane);
+  else pipe.sp.init_blocks(blocks + i0 / 64 * block + k0 * 64, block, p.ni - i0, wave, lane);
   pipe.template run<false>(acc, 0, none);
   const int wm = wave / WN, wn = wave % WN;
   char* stage = pipe.spare() + wave * S::kBytes;
@@ -423,10 +430,6 @@ int64_t piece_of(int64_t rows, int64_t vocab, int64_t depth) {
   return most;
 }
 
-// Elements from one row of P to the next.  Rows a multiple of 1 KB apart would share the memory channels:
-// dx of 16384 rows, 16384 deep 484 us, 457 with a line more.
-int64_t p_pitch(int64_t cols) { return ceil8(cols) + (ceil8(cols) % 512 == 0 ? 64 : 0); }
-
 // The call's operands as the tiles read them, packed where that is needed, and P's scale.
 hipError_t ready(const HeadCall& a, const HeadPlan& plan, char* ws, HeadProduct* p,
                  hipStream_t stream) {
@@ -477,12 +480,11 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
     const int64_t cols = std::min(plan.piece, a.vocab - v);
     p.first = v;
     p.cols = cols;
-    p.ldp = p_pitch(cols);
     e = launch_head_probabilities(p, stream);
     if (e != hipSuccess) return e;
     if (a.dx) {
       InputGrad g{};
-      g.p = p.p; g.ldp = p.ldp;
+      g.p = p.p;
       g.w = static_cast<const uint16_t*>(p.w) + (a.w_kn ? v : v * p.ldw);
       g.ldw = p.ldw;
       g.rows = a.rows; g.cols = a.depth; g.depth = (int)cols;
@@ -502,13 +504,11 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
       WeightGrad g{};
       const WeightPlan tiles = plan_of(a.rows, cols, a.depth, a.w_kn);
       const int64_t at = a.w_kn ? v : v * a.depth;
-      if (a.w_kn) {
-        g.p = p.x; g.ldp = p.ldx; g.ni = a.depth;
-        g.q = p.p; g.ldq = p.ldp; g.nj = (int)cols;
-      } else {
-        g.p = p.p; g.ldp = p.ldp; g.ni = (int)cols;
-        g.q = p.x; g.ldq = p.ldx; g.nj = a.depth;
-      }
+      g.p = p.p;
+      g.x = p.x; g.ldx = p.ldx;
+      g.p_second = a.w_kn;
+      g.ni = a.w_kn ? a.depth : (int)cols;
+      g.nj = a.w_kn ? (int)cols : a.depth;
       g.rows = a.rows;
       g.splits = tiles.splits;
       g.planes = plan.planes >= 0 ? reinterpret_cast<float*>(ws + plan.planes) : nullptr;
@@ -542,7 +542,7 @@ HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f1
   }
   plan.piece = piece_of(rows, vocab, depth);
   if (f16) plan.scale = take(8);
-  plan.p = take(rows * (plan.piece + 64) * 2);
+  plan.p = take(rows * ceil64(plan.piece, 64) * 128);
   if (want_dx && plan.piece < vocab) plan.dx = take(rows * ceil8(depth) * 4);
   if (want_dx) {
     int splits = 1;

@@ -17,7 +17,7 @@ int check_head(int dtype, int w_kn, int target_bits, int64_t rows, int64_t vocab
     return anvil::elem_known(dtype) ? ANVIL_ERR_UNSUPPORTED : ANVIL_ERR_INVALID_ARG;
   if ((w_kn != 0 && w_kn != 1) || (target_bits != 32 && target_bits != 64)) return ANVIL_ERR_INVALID_ARG;
   if (rows < 0 || vocab < 1 || k < 0) return ANVIL_ERR_INVALID_ARG;
-  if (rows > (int64_t(1) << 24) || vocab > anvil::kMaxWidth || k > anvil::kMaxWidth ||
+  if (rows > (int64_t(1) << 22) || vocab > anvil::kMaxWidth || k > anvil::kMaxWidth ||
       vocab * k > (int64_t(1) << 30) || rows * vocab > (int64_t(1) << 37) ||
       rows * k > (int64_t(1) << 37))
     return ANVIL_ERR_UNSUPPORTED;

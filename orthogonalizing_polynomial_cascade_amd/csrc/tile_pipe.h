@@ -70,6 +70,22 @@ struct SlabStream {
     }
   }
 
+  // The same for a matrix in blocks of 64 columns, [columns / 64][matrix rows][64] with `block` elements
+  // from one to the next, so that a slab is contiguous.  origin: in the block of the tile's first column
+  // (K-contiguous: of its first k), the tile's first row (K-major: the first k).
+  __device__ __forceinline__ void init_blocks(const uint16_t* origin, int64_t block, int64_t rows,
+                                              int wave, int lane) {
+    init(origin, 64, rows, wave, lane);
+    if constexpr (!KMAJOR) {
+      step = (uint64_t)block * 2;
+    } else {
+      int row, c;
+      piece(0, wave, lane, &row, &c);
+      if (off[0] != kOOB)
+        off[0] = ((uint32_t)row * 64u + (uint32_t)(c / 8) * (uint32_t)block + (uint32_t)(c % 8) * 8u) * 2u;
+    }
+  }
+
   // Instruction i of the slab at `base` into LDS address dst; left: depth from its first k on, at
   // most kBK (no branch, so that the copies can stand among the multiplies).
   __device__ __forceinline__ void issue(int i, uint32_t dst, int left, int wave) const {

@@ -28,9 +28,9 @@ def test_forward_refusals(lib):
     for bad in ({"rows": -1}, {"vocab": 0}, {"vocab": -5}, {"k": -1}, {"x": None}, {"w": None}, {"t": None}, {"loss": None},
                 {"lse": None}, {"ws": None}, {"kn": 2}, {"bits": 16}, {"dt": 9}):
         assert _forward(lib, **bad) == INVALID, bad
-    for bad in ({"dt": F32}, {"ldx": 63}, {"ldx": (1 << 22) + 1}, {"rows": (1 << 24) + 1}, {"vocab": (1 << 22) + 1},
-                {"vocab": 1 << 20, "k": 1 << 11, "ldx": 1 << 11}, {"rows": 1 << 24, "vocab": (1 << 13) + 1, "k": 8},
-                {"rows": 1 << 24, "k": (1 << 13) + 1, "ldx": 1 << 14}):
+    for bad in ({"dt": F32}, {"ldx": 63}, {"ldx": (1 << 22) + 1}, {"rows": (1 << 22) + 1}, {"vocab": (1 << 22) + 1},
+                {"vocab": 1 << 20, "k": 1 << 11, "ldx": 1 << 11}, {"rows": 1 << 22, "vocab": (1 << 15) + 1, "k": 8},
+                {"rows": 1 << 22, "k": (1 << 15) + 1, "ldx": 1 << 16, "vocab": 16}):
         assert _forward(lib, **bad) == UNSUPPORTED, bad
     for bad in ({"x": X + 1}, {"w": W + 1}, {"t": T + 4}, {"loss": L + 2}, {"lse": E + 1}, {"ws": S + 64}):
         assert _forward(lib, **bad) == MISALIGNED, bad
@@ -43,7 +43,7 @@ def test_grad_refusals(lib):
     for bad in ({"rows": -1}, {"vocab": 0}, {"k": -1}, {"x": None}, {"w": None}, {"t": None}, {"lse": None}, {"dl": None},
                 {"ws": None}, {"kn": -1}, {"bits": 8}, {"wt": F16}):
         assert _grad(lib, **bad) == INVALID, bad
-    for bad in ({"dt": F32}, {"ldx": 63}, {"lddx": 63}, {"rows": (1 << 24) + 1}):
+    for bad in ({"dt": F32}, {"ldx": 63}, {"lddx": 63}, {"rows": (1 << 22) + 1}):
         assert _grad(lib, **bad) == UNSUPPORTED, bad
     for bad in ({"dx": DX + 1}, {"dw": DW + 2}, {"dl": D + 2}, {"ws": S + 128}):
         assert _grad(lib, **bad) == MISALIGNED, bad
