@@ -154,7 +154,8 @@ __global__ __launch_bounds__(WM * WN * KS * 64)
 __attribute__((amdgpu_waves_per_eu(OCC)))
 void head_input_kernel(InputGrad p, int tiles_m, int tiles_n) {
   using C = Tile<BM, BN, WM, WN, KS>;
-  using S = OutStage<C::kWTN>;
+  constexpr int kSide = C::kFN % 2 ? 1 : 2;   // fragments that leave side by side
+  using S = OutStage<kSide * 32>;
   static_assert(C::kWaves * S::kBytes <= C::kStage, "the outgoing rows fit one buffer");
   extern __shared__ __attribute__((aligned(1024))) char smem_all[];
   const int lane = threadIdx.x & 63;
@@ -192,19 +193,25 @@ void head_input_kernel(InputGrad p, int tiles_m, int tiles_n) {
   }
   if (idle) return;
   char* stage = pipe.spare() + wave * S::kBytes;
-  const int c = j0 + wn * C::kWTN + S::col(lane);
   const float back = p.scale ? p.scale[1] : 1.0f;
 #pragma unroll
-  for (int fm = 0; fm < C::kFM; ++fm) {
-    S::put(stage, acc[fm], lane);
+  for (int fn = 0; fn < C::kFN; fn += kSide) {
+    const int c = j0 + wn * C::kWTN + fn * 32 + S::col(lane);
 #pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) {
-      const int64_t r = row0 + wm * C::kWTM + fm * 32 + S::row(i, lane);
-      float v[8];
-      S::get(stage, i, lane, v);
-      if (r >= p.rows || c >= p.cols) continue;
-      if (p.splits > 1) store_vec<float, 8>(p.planes + (s * p.rows + r) * p.ldsum + c, v);
-      else input_out<T>(p, r, c, back, v);
+    for (int fm = 0; fm < C::kFM; ++fm) {
+      f32x16_t leaving[kSide];
+#pragma unroll
+      for (int f = 0; f < kSide; ++f) leaving[f] = acc[fm][fn + f];
+      S::put(stage, leaving, lane);
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) {
+        const int64_t r = row0 + wm * C::kWTM + fm * 32 + S::row(i, lane);
+        float v[8];
+        S::get(stage, i, lane, v);
+        if (r >= p.rows || c >= p.cols) continue;
+        if (p.splits > 1) store_vec<float, 8>(p.planes + (s * p.rows + r) * p.ldsum + c, v);
+        else input_out<T>(p, r, c, back, v);
+      }
     }
   }
 }
@@ -344,9 +351,39 @@ hipError_t input_tiles(const InputGrad& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Tile and splits of dx's product: the least of the tiles' time, by the linear layers' fits, and the
-// join's, which writes and reads each split's sums.  The depth is a piece of the vocabulary, so few rows
-// leave most CUs idle for long without splits.
+// Time in microseconds of a product of `groups` workgroups with `slabs` 64-deep slabs each, for depths of
+// hundreds of slabs: a fixed part (first slab, outgoing rows) and one for each slab, which grows with the
+// share of the CUs that multiply (256x256: 1.05 us with a few workgroups, 1.34 with 96, 1.6 with 192, 1.7
+// with all).  The last, partial round counts with its own share.
+double deep_cost(RowsTile tile, double groups, double slabs) {
+  double slots = 256, fixed = 10.0, slab = 1.05, more = 0.65;   // 256x256
+  switch (tile) {
+    case kRows32: return rounds(groups, 256) * (4.5 + 0.7 * std::ceil(slabs / 8));
+    case kRows32x128: return rounds(groups, 512) * (4.5 + 0.6 * std::ceil(slabs / 2));
+    case kRows64: fixed = 2.2; slab = 0.22; more = 0.08; break;
+    case kRows128: slots = 512; fixed = 4.0; slab = 0.6; more = 0.5; break;
+    case kRows128x192: slots = 512; fixed = 5.0; slab = 0.75; more = 0.7; break;
+    default: break;
+  }
+  const double whole = std::floor(groups / slots), rest = groups - whole * slots;
+  return whole * (fixed + (slab + more) * slabs) +
+         (rest > 0 ? fixed + (slab + more * rest / slots) * slabs : 0.0);
+}
+
+// Adding up `splits` planes of `bytes`: read in the join, written in the product, half of it hidden there.
+double join_cost(int splits, double bytes) {
+  return splits > 1 ? 5.0 + 1.5 * splits * bytes / 5.4e6 : 0.0;
+}
+
+// Tile and splits of dx's product: the least of these.  The depth is a piece of the vocabulary, so few rows
+// leave most CUs idle for long without splits.  Us by tile/splits with the join, the choice first (rows x
+// width, depth):
+//    256 x  768, 16384   128/16        21   64/4  24   256/16 32   128/1 159   256/1  278
+//    512 x  768, 50304   128/16        54   64/8  88   256/16 73   128/1 487   256/1  829
+//   2048 x  768, 50304   128x192/8    165   128/4 196  256/8  183  128/1 565   256/1  943
+//   8192 x 1024, 32768   256/2        450   128/1 556  128x192/4 584           256/1  760
+//  16384 x  768, 21760   128x192/1    487   256/4 521  128/2  611  128/1 682   256/1  543
+//  16384 x 1536, 16384   256/2        704   128x192/1 725          128/1 801   256/1  800
 struct InputPlan {
   RowsTile tile;
   int splits;
@@ -357,19 +394,13 @@ InputPlan input_plan(int64_t rows, int64_t cols, int64_t depth) {
   const double bytes = 4.0 * (double)rows * (double)cols;
   InputPlan best{kRows256, 1};
   double least = 0;
-  for (RowsTile t : {kRows256, kRows128, kRows64, kRows32x128, kRows32}) {
+  for (RowsTile t : {kRows256, kRows128x192, kRows128, kRows64, kRows32x128, kRows32}) {
     const double tiles = (double)ceil64(rows, kTileRows[t]) * (double)ceil64(cols, kTileCols[t]);
     if (t != kRows256 && tiles > kMaxTileGrid) continue;
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       const double each = std::ceil(slabs / splits), groups = tiles * splits;
       if (splits > 1 && (each < 8 || groups > kMaxTileGrid || splits * bytes > 2.7e8)) break;
-      double cost = 0;
-      switch (t) {
-        case kRows32: cost = rounds(groups, 256) * (4.5 + 0.7 * std::ceil(each / 8)); break;
-        case kRows32x128: cost = rounds(groups, 512) * (4.5 + 0.6 * std::ceil(each / 2)); break;
-        default: cost = tile_cost(kTileRows[t], groups, each, false); break;
-      }
-      if (splits > 1) cost += 5.0 + (2 * splits + 1) * bytes / 5e6;
+      const double cost = deep_cost(t, groups, each) + join_cost(splits, bytes);
       if ((t == kRows256 && splits == 1) || cost < least) {
         best = {t, splits};
         least = cost;
@@ -386,6 +417,7 @@ hipError_t input_variant(const InputGrad& a, RowsTile tile, hipStream_t stream) 
     case kRows32x128: return input_tiles<T, QT, 32, 128, 1, 4, 2, 4>(a, stream);
     case kRows64: return input_tiles<T, QT, 64, 64, 2, 2, 4, 4>(a, stream);
     case kRows128: return input_tiles<T, QT, 128, 128, 2, 2, 1, 2>(a, stream);
+    case kRows128x192: return input_tiles<T, QT, 128, 192, 2, 2, 1, 2>(a, stream);
     default: return input_tiles<T, QT, 256, 256, 2, 4, 1, 2>(a, stream);
   }
 }
@@ -405,14 +437,30 @@ hipError_t weight_side(const WeightGrad& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The splits and tiles of a weight gradient of the same size.
-WeightPlan plan_of(int64_t rows, int64_t vocab, int64_t depth, bool w_kn) {
-  WeightProduct a{};
-  a.rows = rows;
-  a.pi = (int)(w_kn ? depth : vocab);
-  a.qj = (int)(w_kn ? vocab : depth);
-  a.groups = Groups{nullptr, false, 1};
-  return weight_plan(a);
+// The same for dW, whose depth is the rows (at least 256 a split).
+struct HeadWeightPlan {
+  int side, splits;
+};
+
+HeadWeightPlan head_weight_plan(int64_t rows, int64_t entries, int64_t depth) {
+  const double slabs = (double)std::max<int64_t>(1, ceil64(rows, kBK));
+  const double bytes = 4.0 * (double)entries * (double)depth;
+  HeadWeightPlan best{256, 1};
+  double least = 0;
+  for (RowsTile t : {kRows256, kRows128}) {
+    const int side = kTileRows[t];
+    const double tiles = (double)ceil64(entries, side) * (double)ceil64(depth, side);
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      const double each = std::ceil(slabs / splits);
+      if (splits > 1 && (each < 4 || splits * bytes > 1.1e9)) break;
+      const double cost = deep_cost(t, tiles * splits, each) + join_cost(splits, bytes);
+      if ((t == kRows256 && splits == 1) || cost < least) {
+        best = {side, splits};
+        least = cost;
+      }
+    }
+  }
+  return best;
 }
 
 // Columns of the vocabulary at a time: as many as give dW whole rounds of 256x256 tiles on the CUs, with
@@ -502,7 +550,7 @@ hipError_t gradients(const HeadCall& a, const HeadPlan& plan, char* ws, hipStrea
     }
     if (a.dw) {
       WeightGrad g{};
-      const WeightPlan tiles = plan_of(a.rows, cols, a.depth, a.w_kn);
+      const HeadWeightPlan tiles = head_weight_plan(a.rows, cols, a.depth);
       const int64_t at = a.w_kn ? v : v * a.depth;
       g.p = p.p;
       g.x = p.x; g.ldx = p.ldx;
@@ -554,7 +602,7 @@ HeadPlan head_plan(bool gradient, bool want_dx, bool want_dw, bool w_kn, bool f1
     int64_t words = 0;
     for (int64_t cols : {std::min(plan.piece, vocab), vocab % plan.piece}) {   // and the last piece
       if (cols == 0) continue;
-      const WeightPlan t = plan_of(rows, cols, depth, w_kn);
+      const HeadWeightPlan t = head_weight_plan(rows, cols, depth);
       if (t.splits > 1)
         words = std::max(words, t.splits * (w_kn ? depth * ceil8(cols) : cols * ceil8(depth)));
     }

@@ -40,13 +40,16 @@ struct KContig {
 // [BK][ROWS] bf16: a k-row is ROWS*2 bytes = ROWS/8 slots.  A transposing read takes 32 bytes of
 // each of four consecutive k-rows: the swizzle puts those at four distinct 64-byte quarters of the
 // 256 bytes that the banks span.  From 128 rows up, logical slot c of k-row kr sits at slot
-// c ^ (4 * (kr & 3)); at 64 rows two k-rows share the 256 bytes and every second pair swaps its
+// c ^ (4 * (kr & 3)); at 192 rows every second k-row begins at the upper half of the 256 bytes by itself
+// and every second pair swaps 64-byte quarters; at 64 rows two k-rows share the 256 bytes and every second pair swaps its
 // halves; at 32 rows four k-rows fill the 256 bytes by themselves.
 template <int ROWS>
 struct KMajor {
-  static_assert(ROWS >= 32 && (ROWS & (ROWS - 1)) == 0, "K-major slab rows: a power of two");
+  static_assert(ROWS == 192 || (ROWS >= 32 && (ROWS & (ROWS - 1)) == 0),
+                "K-major slab rows: a power of two, or 192");
   static constexpr int kPer256 = ROWS >= 128 ? 1 : 128 / ROWS;
   __device__ static __forceinline__ int swz(int kr) {
+    if constexpr (ROWS == 192) return ((kr >> 1) & 1) << 2;
     return ((kr / kPer256) & (4 / kPer256 - 1)) << 2;
   }
   __device__ static __forceinline__ int offset(int kr, int c) {

@@ -31,11 +31,12 @@ struct SlabStream {
   // K-contiguous one, which exchanges the halves of the slab's k.
   static constexpr int kStep = KMAJOR ? NW * (512 / ROWS) : NW * (512 / kBK);
   static constexpr bool kHalf = !KMAJOR && kStep == 8;
-  static_assert(kInsts == 1 || kHalf || kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
   // K-major instructions differ by a uniform offset (soff); K-contiguous ones by rows that have to
-  // be checked against the edge one by one
-  uint32_t off[KMAJOR ? 1 : kInsts];
-  int kin;                 // the lane's k within the slab (of its first instruction)
+  // be checked against the edge one by one; K-major ones of 192 rows begin anywhere in a k-row
+  static constexpr bool kAny = KMAJOR && 512 % ROWS != 0;
+  static_assert(kInsts == 1 || kHalf || kAny || kStep % (KMAJOR ? 4 : 16) == 0, "slot swizzle period");
+  uint32_t off[KMAJOR && !kAny ? 1 : kInsts];
+  int kin[kAny ? kInsts : 1];   // the lane's k within the slab (of its first instruction)
   uint32_t soff;           // K-major: bytes from one instruction to the next
   uint64_t base, step;
 
@@ -45,6 +46,10 @@ struct SlabStream {
       constexpr int kSlots = kBK / 8;
       *row = (64 / kSlots) * u + lane / kSlots;
       *c = (lane % kSlots) ^ KContig<ROWS, kBK>::swz(*row);
+    } else if constexpr (kAny) {
+      constexpr int kSlots = ROWS / 8;
+      *row = (u * 64 + lane) / kSlots;
+      *c = ((u * 64 + lane) % kSlots) ^ KMajor<ROWS>::swz(*row);
     } else {
       constexpr int kSlots = ROWS / 8;
       *row = u * (512 / ROWS) + lane / kSlots;
@@ -57,13 +62,14 @@ struct SlabStream {
                                        int lane) {
     base = reinterpret_cast<uint64_t>(origin);
     step = KMAJOR ? (uint64_t)ld * (2 * kBK) : 2 * kBK;
-    soff = KMAJOR ? (uint32_t)ld * (2 * kStep) : 0;
+    soff = KMAJOR && !kAny ? (uint32_t)ld * (2 * kStep) : 0;
     int row, c;
     piece(0, wave, lane, &row, &c);
-    kin = KMAJOR ? row : c * 8;
+    kin[0] = KMAJOR ? row : c * 8;
 #pragma unroll
-    for (int i = 0; i < (KMAJOR ? 1 : kInsts); ++i) {
+    for (int i = 0; i < (KMAJOR && !kAny ? 1 : kInsts); ++i) {
       piece(i, wave, lane, &row, &c);
+      if constexpr (kAny) kin[i] = row;
       off[i] = (KMAJOR ? c * 8 : row) < rows
                    ? ((uint32_t)row * (uint32_t)ld + (uint32_t)c * 8) * 2u
                    : kOOB;
@@ -75,6 +81,7 @@ struct SlabStream {
   // (K-contiguous: of its first k), the tile's first row (K-major: the first k).
   __device__ __forceinline__ void init_blocks(const uint16_t* origin, int64_t block, int64_t rows,
                                               int wave, int lane) {
+    static_assert(!kAny, "blocks for power-of-two rows");
     init(origin, 64, rows, wave, lane);
     if constexpr (!KMAJOR) {
       step = (uint64_t)block * 2;
@@ -91,11 +98,13 @@ struct SlabStream {
   __device__ __forceinline__ void issue(int i, uint32_t dst, int left, int wave) const {
     const i32x4_t rsrc = make_rsrc(reinterpret_cast<const uint16_t*>(base), 0x80000000u);
     const uint32_t to = dst + (uint32_t)(wave + i * NW) * 1024u;
-    if constexpr (KMAJOR) {
-      dma16(rsrc, to, kin < left - i * kStep ? off[0] : kOOB,
+    if constexpr (kAny) {
+      dma16(rsrc, to, kin[i] < left ? off[i] : kOOB);
+    } else if constexpr (KMAJOR) {
+      dma16(rsrc, to, kin[0] < left - i * kStep ? off[0] : kOOB,
             (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)i * soff)));
     } else {
-      const int k = kHalf && (i & 1) ? kin ^ (kBK / 2) : kin;
+      const int k = kHalf && (i & 1) ? kin[0] ^ (kBK / 2) : kin[0];
       dma16(rsrc, to, k < left ? off[i] : kOOB);
     }
   }
@@ -584,10 +593,10 @@ hipError_t launch_lds(K kern, std::atomic<uint64_t>& configured, int64_t grid, i
 
 // Tile shapes of the rows product: 32x32 with eight sets of one wave, 32x128 with two sets of four
 // (two workgroups a CU), 64x64 with four sets of four, 128x128 of four waves (two workgroups a CU),
-// 256x256 of eight.
-enum RowsTile { kRows32, kRows32x128, kRows64, kRows128, kRows256 };
-constexpr int kTileRows[] = {32, 32, 64, 128, 256};
-constexpr int kTileCols[] = {32, 128, 64, 128, 256};
+// 256x256 of eight.  (128x192 of four waves, two workgroups a CU, is not among rows_tile's choices.)
+enum RowsTile { kRows32, kRows32x128, kRows64, kRows128, kRows256, kRows128x192 };
+constexpr int kTileRows[] = {32, 32, 64, 128, 256, 128};
+constexpr int kTileCols[] = {32, 128, 64, 128, 256, 192};
 
 inline int64_t row_tiles(const RowsProduct& a, int side) {
   return ceil64(a.rows, side) + (a.groups.offsets ? a.groups.count + 1 : 0);
