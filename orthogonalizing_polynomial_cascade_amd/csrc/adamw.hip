@@ -16,6 +16,9 @@
 // gradient, 14.06 with 8-bit ones.  A workgroup takes 2048 elements of one tensor, eight consecutive ones a
 // lane, so that 32 lanes hold a block and its maxima are five exchanges within half a wave; the tensors are
 // found through a table of the pieces in device memory, which makes any number of them one launch.
+// 77.3M weights as two halves with a bf16 gradient: 368 us with 32-bit states (5.5 TB/s), 210-217 with 8-bit
+// ones (5.0-5.2 TB/s; about 90 vector operations an element, which bounds weights of 16 bits alone: 80M in 190
+// us, 4.2 TB/s).  96 vectors of 256 to 2816 elements: 4.7 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

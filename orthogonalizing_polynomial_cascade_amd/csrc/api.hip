@@ -352,7 +352,7 @@ const char* anvil_status_string(int status) {
 
 int anvil_last_hip_error(void) { return t_last_hip; }
 
-int anvil_version(void) { return 200; }
+int anvil_version(void) { return 300; }
 
 size_t anvil_workspace_bytes(int64_t g, int64_t m, int64_t n) {
   Shape sh;

@@ -236,7 +236,8 @@ void head_kernel(HeadProduct p, int tiles_n) {
 
 // The statistics of large products: 256 workgroups that walk over the 256x256 tiles, the next tile's
 // slabs on their way while a tile is finished (Pipe::walk); the waves' statistics lie beside the two
-// buffers.  16384 x 50304, depth 768: 1146 us (1100 TFLOP/s), 1320 with a workgroup for each tile.  The
+// buffers.  16384 x 50304, depth 768: 1482 us with a workgroup for each tile, 1208 in the walk, 1146 (1100
+// TFLOP/s) with an epilogue whose rare parts are behind ballots.  The
 // probabilities do not gain: vector memory operations end in order, so a walk's copies wait for the
 // last tile's 128 KB of stores, which a workgroup of its own leaves behind when it ends (16384 x 16384: 560 us,
 // 483 with a workgroup for each tile, 484 in a walk whose stores are left out).
