@@ -1033,6 +1033,15 @@ class AdamwTensor(ctypes.Structure):
                 ("grad_dtype", _i), ("lr_mul", _f), ("wd_mul", _f), ("state_bits", _i)]
 
 
+def _member(t, name, i, dtype, device, shape):
+    """Pointer of entry i of a list of contiguous tensors (_dense with its name put together only for an
+    error: a plan checks several tensors for each parameter)."""
+    if (isinstance(t, _torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_cuda
+            and t.get_device() == device and t.is_contiguous()):
+        return t.data_ptr()
+    return _dense(t, f"{name}[{i}]", dtype, device, tuple(shape))
+
+
 class AdamW:
     """The tensors of an AdamW step, their states and the plan of the launch that updates them all.
 
@@ -1061,42 +1070,41 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32")
         self.mantissas = each(mantissas, "mantissas", None)
         lr_mul, wd_mul = each(lr_mul, "lr_mul", 1.0), each(wd_mul, "wd_mul", 1.0)
-        given = [each(s, name, None) for s, name in ((m, "m"), (v, "v"), (m_scale, "m_scale"), (v_scale, "v_scale"))]
-        self.m, self.v, self.m_scale, self.v_scale = [], [], [], []
+        self.m, self.v = each(m, "m", None), each(v, "v", None)
+        self.m_scale, self.v_scale = each(m_scale, "m_scale", None), each(v_scale, "v_scale", None)
         self._table = (AdamwTensor * max(1, count))()
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else 0
+        self.device = device = torch.cuda.current_device() if torch.cuda.is_available() else 0
+
+        def state(states, name, i, dtype, shape):
+            """Pointer of tensor i's state, made of zeros (of which the bytes are zeros in either type) where
+            there is none."""
+            if states[i] is None:
+                states[i] = _empty(shape, dtype, self.params[i].device, None)
+                states[i].view(-1).view(torch.uint8).zero_()
+            return _member(states[i], name, i, dtype, device, shape)
+
         for i, p in enumerate(self.params):
-            self.device = device = _device(p, f"params[{i}]")
-            code = _code(p, f"params[{i}]", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
-            shape, n = tuple(p.shape), p.numel()
+            if not isinstance(p, torch.Tensor) or not p.is_cuda or p.get_device() != device:
+                _device(p, f"params[{i}]")
+            code = _codes.get(p.dtype)
+            if code is None:
+                raise TypeError(f"params[{i}] has an unsupported dtype ({p.dtype})")
+            shape, n, row = p.shape, p.numel(), self._table[i]
+            row.param, row.count, row.param_dtype = _member(p, "params", i, p.dtype, device, shape), n, code
             low = self.mantissas[i]
             if low is not None:
                 if code != ANVIL_BF16:
                     raise TypeError(f"params[{i}] must be bfloat16 to have a mantissa")
                 if not isinstance(low, torch.Tensor) or low.dtype not in (torch.int16, torch.uint16):
                     raise TypeError(f"mantissas[{i}] must be a 16-bit integer tensor")
-                low = _dense(low, f"mantissas[{i}]", low.dtype, device, shape)
-            at = {}
-            blocks = -(-n // 256)
-            for name, value, own in zip(("m", "v", "m_scale", "v_scale"), given, (self.m, self.v, self.m_scale, self.v_scale)):
-                scale = name.endswith("scale")
-                if scale and bits[i] == 32:
-                    own.append(None)
-                    at[name] = None
-                    continue
-                dtype = torch.float32 if scale or bits[i] == 32 else torch.float8_e4m3fn
-                want = (blocks,) if scale else shape
-                t = value[i]
-                if t is None:
-                    # as bytes: those of zero are zeros in either type
-                    t = _empty(want, dtype, p.device, None)
-                    t.view(torch.uint8).zero_()
-                at[name] = _dense(t, f"{name}[{i}]", dtype, device, want)
-                own.append(t)
-            _dense(p, f"params[{i}]", p.dtype, device, shape)
-            row = self._table[i]
-            row.param, row.mantissa, row.count, row.param_dtype = p.data_ptr(), low, n, code
-            row.m, row.v, row.m_scale, row.v_scale = at["m"], at["v"], at["m_scale"], at["v_scale"]
+                row.mantissa = _member(low, "mantissas", i, low.dtype, device, shape)
+            kept = torch.float32 if bits[i] == 32 else torch.float8_e4m3fn
+            row.m = state(self.m, "m", i, kept, shape)
+            row.v = state(self.v, "v", i, kept, shape)
+            if bits[i] == 8:
+                blocks = torch.Size((-(-n // 256),))
+                row.m_scale = state(self.m_scale, "m_scale", i, torch.float32, blocks)
+                row.v_scale = state(self.v_scale, "v_scale", i, torch.float32, blocks)
             row.lr_mul, row.wd_mul, row.state_bits = lr_mul[i], wd_mul[i], bits[i]
         self._plan = None
         self.bind(grads)
@@ -1111,9 +1119,11 @@ class AdamW:
         for i, (g, p) in enumerate(zip(grads, self.params)):
             if not isinstance(g, torch.Tensor):
                 raise TypeError(f"grads[{i}] must be a torch.Tensor")
-            code = _code(g, f"grads[{i}]", (ANVIL_F32, ANVIL_BF16, ANVIL_F16))
-            self._table[i].grad = _dense(g, f"grads[{i}]", g.dtype, self.device, tuple(p.shape))
-            self._table[i].grad_dtype = code
+            code = _codes.get(g.dtype)
+            if code is None:
+                raise TypeError(f"grads[{i}] has an unsupported dtype ({g.dtype})")
+            row = self._table[i]
+            row.grad, row.grad_dtype = _member(g, "grads", i, g.dtype, self.device, p.shape), code
         self.grads = grads
         lib, count = load(), len(self.params)
         table = ctypes.cast(self._table, _vp)

@@ -45,17 +45,15 @@ struct RowData {
   int target[FM];      // -1: ignored
   float ref[FM];       // -lse log2(e)
   float weight[FM];    // dloss times the scale
-  bool in[FM];
   template <bool STATS>
   __device__ __forceinline__ void load(const HeadProduct& p, int64_t r0, int lane) {
     const float scale = !STATS && p.scale ? p.scale[0] : 1.0f;
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
       const int64_t r = r0 + fm * 32 + (lane & 31);
-      in[fm] = r < p.rows;
       target[fm] = -1;
       ref[fm] = weight[fm] = 0.0f;
-      if (!in[fm]) continue;
+      if (r >= p.rows) continue;
       target[fm] = (int)target_of(p, r);
       if (!STATS) {
         ref[fm] = -p.lse[r] * kLog2e;

@@ -247,6 +247,27 @@ def test_empty(gpu_lib):
     gpu_lib.anvil_adamw(gpu_lib.AdamW([none], [none.clone()], state_bits=8), 1e-3, 1)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_of_its_own(gpu_lib, bits):
+    """States that are not given begin at zero, for matrices and for a single number."""
+    g = torch.Generator().manual_seed(3)
+    shapes = [(), (3, 5, 70), (1,), (256,)]
+    params, grads = ([torch.randn(s, generator=g) for s in shapes] for _ in range(2))
+    plan = gpu_lib.AdamW([p.cuda() for p in params], [v.cuda() for v in grads], state_bits=bits)
+    for i, p in enumerate(params):
+        assert plan.m[i].shape == plan.v[i].shape == p.shape and not plan.m[i].float().any() and not plan.v[i].float().any()
+    gpu_lib.anvil_adamw(plan, 1e-2, 1, betas=BETAS, eps=EPS, weight_decay=0.1)
+    for i, (p, v) in enumerate(zip(params, grads)):
+        n = p.numel()
+        s = {"param": p.view(-1), "mantissa": None, "grad": v.view(-1), "lr_mul": 1.0, "wd_mul": 1.0}
+        zero = torch.zeros(n, dtype=torch.uint8).view(torch.float8_e4m3fn) if bits == 8 else torch.zeros(n)
+        s |= {"m": zero, "v": zero, "m_scale": torch.zeros(-(-n // 256)), "v_scale": torch.zeros(-(-n // 256))}
+        want = A.step32(s, i, 1e-2, 0.1, BETAS, EPS, 1, None, 1)
+        _same_bits(plan.params[i].view(-1), want["param"], f"param {i}")
+        _same_bits(plan.m[i].view(-1), want["m"], f"m {i}")
+        _same_bits(plan.v[i].view(-1), want["v"], f"v {i}")
+
+
 def test_gradients_elsewhere(gpu_lib):
     """bind() takes the gradients from other tensors, of another type too."""
     s = _state(3000, "fp32", "bf16", 32, 1)

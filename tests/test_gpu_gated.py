@@ -173,6 +173,13 @@ def test_empty(gpu_lib):
         assert y.shape == (rows, n) and z.shape == (rows, 2 * n)
         dz = gpu_lib.anvil_gated_grad_input(_mat(rows, k, t, 1), _weight(k, n, t, 2, False), _mat(rows, 2 * n, t, 3))
         assert dz.shape == (rows, 2 * n)
+    # no experts: no row has one
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, z = gpu_lib.anvil_expert_gated_linear(_mat(5, 8, t, 1), torch.empty(0, 32, 8, dtype=t, device="cuda"), off,
+                                             preact=_nan(5, 32, t=t), out=_nan(5, 16, t=t))
+    dz = gpu_lib.anvil_expert_gated_grad_input(_mat(5, 8, t, 1), torch.empty(0, 8, 16, dtype=t, device="cuda"), off, z,
+                                               out=_nan(5, 32, t=t))
+    assert not y.any() and not z.any() and not dz.any()
     # no inputs: z is the bias alone; no outputs: nothing reaches z
     bias = torch.randn(32, generator=torch.Generator().manual_seed(1)).cuda()
     y, z = gpu_lib.anvil_gated_linear(_mat(4, 0, t, 1), torch.empty(32, 0, dtype=t, device="cuda"), bias, act="relu", keep_preact=True)
