@@ -8,6 +8,13 @@
 
 namespace anvil {
 
+// Row r's target as a column of the whole vocabulary, -1 where it is outside (the row is ignored).
+__device__ __forceinline__ int64_t target_of(const void* targets, bool wide, int64_t vocab, int64_t r) {
+  const int64_t t = wide ? static_cast<const int64_t*>(targets)[r]
+                         : (int64_t)static_cast<const int32_t*>(targets)[r];
+  return t >= 0 && t < vocab ? t : -1;
+}
+
 // One product over columns [first, first + cols) of the vocabulary.  x [rows][depth] at pitch ldx and w
 // ([vocab][depth], or [depth][vocab] where w_kn) at pitch ldw are ready for the copies: 16-byte aligned,
 // pitches multiples of 8, the pieces of eight that reach past the depth zero.

@@ -23,13 +23,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The row's target as a column of the whole vocabulary, -1 where it is outside (the row is ignored).
-__device__ __forceinline__ int64_t target_of(const HeadProduct& p, int64_t r) {
-  const int64_t t = p.wide ? static_cast<const int64_t*>(p.targets)[r]
-                           : (int64_t)static_cast<const int32_t*>(p.targets)[r];
-  return t >= 0 && t < p.vocab ? t : -1;
-}
-
 // (m, s) and (m2, s2) as one: s e^m + s2 e^m2 with the larger m.  Without columns m is -inf and s 0.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = m2 > m ? m2 : m;
@@ -54,7 +47,7 @@ struct RowData {
       target[fm] = -1;
       ref[fm] = weight[fm] = 0.0f;
       if (r >= p.rows) continue;
-      target[fm] = (int)target_of(p, r);
+      target[fm] = (int)target_of(p.targets, p.wide, p.vocab, r);
       if (!STATS) {
         ref[fm] = -p.lse[r] * kLog2e;
         weight[fm] = p.dloss[r] * scale;
@@ -301,7 +294,7 @@ __global__ __launch_bounds__(256) void head_join_kernel(HeadProduct p, int tiles
   if (lane == 0) {
     const float l = m + logf(s);
     lse[r] = l;
-    p.loss[r] = target_of(p, r) >= 0 ? l - p.loss[r] : 0.0f;
+    p.loss[r] = target_of(p.targets, p.wide, p.vocab, r) >= 0 ? l - p.loss[r] : 0.0f;
   }
 }
 

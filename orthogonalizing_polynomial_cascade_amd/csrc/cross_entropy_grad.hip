@@ -3,7 +3,7 @@
 // With P = (softmax(x W^T) - onehot) dloss:  dx = P W,  dW = P^T x.  P is formed for a piece of the
 // vocabulary at a time (cross_entropy.hip), rounded to the operands' type as the matrix cores take it, and
 // both products read it: dW of the piece is complete, dx is summed over the pieces in fp32.  An fp16 P is
-// scaled by a power of two so that the largest |dloss| comes to 2^14 (a mean over 16384 rows alone would push
+// scaled by a power of two so that the largest |dloss| of a row with a target comes to 2^14 (a mean over 16384 rows alone would push
 // probabilities below 2^-10 under fp16's range); the products are scaled back in fp32, exactly.  P lies in
 // blocks of 64 columns, so that the slabs of both products are contiguous.  The
 // rounding of P is each element's own, at most half a step of its type: it adds to a sum of many of them
@@ -41,18 +41,21 @@ struct PackedCopy {
 struct HeadReady {
   PackedCopy copy[2];
   const float* dloss;
-  int64_t rows;
+  const void* targets;
+  bool wide;
+  int64_t vocab, rows;
   float* scale;          // {S, 1 / S}, or null
 };
 constexpr int kReadyThreads = 1024;
 
-// S the power of two that takes the largest finite |dloss| to [2^14, 2^15).
+// S the power of two that takes the largest finite |dloss| to [2^14, 2^15).  Rows without a target do not
+// count: they may hold anything.
 __device__ __forceinline__ void find_scale(const HeadReady& p) {
   __shared__ float wave_top[kReadyThreads / 64];
   float top = 0.0f;
   for (int64_t r = threadIdx.x; r < p.rows; r += kReadyThreads) {
     const float v = fabsf(p.dloss[r]);
-    if (v > top && v < INFINITY) top = v;
+    if (v > top && v < INFINITY && target_of(p.targets, p.wide, p.vocab, r) >= 0) top = v;
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
@@ -513,6 +516,7 @@ hipError_t ready(const HeadCall& a, const HeadPlan& plan, char* ws, HeadProduct*
   }
   if (plan.scale >= 0) {
     r.dloss = a.dloss;
+    r.targets = a.targets; r.wide = a.wide; r.vocab = a.vocab;
     r.rows = a.rows;
     r.scale = reinterpret_cast<float*>(ws + plan.scale);
     p->scale = r.scale;

@@ -193,6 +193,21 @@ def test_ignored_rows_hold_anything(gpu_lib):
         assert torch.equal(dw, want[1])
 
 
+@pytest.mark.parametrize("bits", [torch.int32, torch.int64])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_large_dloss_of_ignored_rows(gpu_lib, kind, bits):
+    """A finite dloss of a row without a target, however large, does not take part in an fp16 P's scale."""
+    t = TYPES[kind]
+    x, w, targets = _mat(150, 64, t, 1), _weight(900, 64, t, 2, False), _targets(150, 900, 3, bits)
+    ignored = ~C.counts_of(targets, 900).cuda()
+    dloss = torch.full((150,), 1 / 150, device="cuda")
+    _, lse = gpu_lib.anvil_cross_entropy(x, w, targets)
+    want = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, dloss)
+    dloss[ignored] = 1e30
+    got = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, dloss)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_offsets_past_32_bits(gpu_lib):
     """More than 2^32 logits, several pieces of more than 2^28 probabilities: the last rows' loss and dx, and dw of rows at
     both ends of the batch (the others have no target)."""
