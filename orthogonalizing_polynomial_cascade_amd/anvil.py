@@ -1111,8 +1111,11 @@ class AdamW:
 
     def bind(self, grads):
         """Takes the gradients from other tensors from the next step on, a captured step's replays too.  It
-        writes the plan on the current stream: steps on other streams have to be ordered with it."""
+        writes the plan on the current stream (not while that is captured): steps on other streams have to be
+        ordered with it.  A refused call leaves the plan and its gradients as they were."""
         torch = _module()
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a plan is written from host memory, which a graph cannot capture")
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"grads must have one entry for each of {len(self.params)} parameters")
@@ -1124,7 +1127,6 @@ class AdamW:
                 raise TypeError(f"grads[{i}] has an unsupported dtype ({g.dtype})")
             row = self._table[i]
             row.grad, row.grad_dtype = _member(g, "grads", i, g.dtype, self.device, p.shape), code
-        self.grads = grads
         lib, count = load(), len(self.params)
         table = ctypes.cast(self._table, _vp)
         self.plan_bytes = int(lib.anvil_adamw_plan_bytes(table, count))
@@ -1137,6 +1139,7 @@ class AdamW:
             self._plan = words.to(f"cuda:{self.device}") if count else None
         else:
             self._plan.copy_(words)
+        self.grads = grads   # last: until here the plan in memory names the gradients before
 
     def _arguments(self, grad_scale, stream):
         """(plan, its bytes, tensors), the grad_scale pointer and the stream's handle of a step."""

@@ -282,6 +282,26 @@ def test_gradients_elsewhere(gpu_lib):
         plan.bind([torch.zeros(7, device="cuda")])
 
 
+def test_a_refused_bind_changes_nothing(gpu_lib):
+    """The plan goes on with the gradients that it has, and keeps them alive."""
+    s = _state(3000, "fp32", "fp32", 32, 1)
+    plan = _plan(gpu_lib, [s])
+    had = plan.grads[0].data_ptr()
+    with pytest.raises(gpu_lib.AnvilError):
+        plan.bind([plan.params[0]])               # shares memory with what a step writes
+    for bad in ([torch.zeros(7, device="cuda")], [plan.grads[0].double()], []):
+        with pytest.raises((ValueError, TypeError)):
+            plan.bind(bad)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gpu_lib.anvil_adamw(plan, 1e-3, 1, betas=BETAS, eps=EPS, weight_decay=0.1)
+        with pytest.raises(RuntimeError, match="capture"):
+            plan.bind([torch.zeros(3000, device="cuda")])
+    assert plan.grads[0].data_ptr() == had
+    graph.replay()
+    _compare(plan, [A.step32(s, 0, 1e-3, 0.1, BETAS, EPS, 1, None, 1)])
+
+
 def test_refusals(gpu_lib):
     p, g = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
     for kw in ({"state_bits": 16}, {"mantissas": [None, None]}, {"lr_mul": [1.0, 2.0]}, {"m": [torch.zeros(3, device="cuda")]},
