@@ -99,45 +99,52 @@ struct AnySlab {
 // acc (the wave's fragments, C transposed: register r of lane l is row l%32, column
 // 8(r/4) + 4(l/32) + r%4 of a fragment) of the tile's k range [k0, k1).  `sum`: 1 the wave also adds
 // up its P fragments over k into `sums`, 2 its Q fragments (see add8).
-template <typename T, bool PT, bool QT, int SIDE>
+// PAIR: SIDE rows by the same 64 columns of two Qs, `second` elements apart; a wave has 32 columns, acc[m][0] of
+// the first and acc[m][1] of the second, and no sums.
+template <typename T, bool PT, bool QT, int SIDE, bool PAIR = false>
 __device__ __forceinline__ void any_accumulate(const T* P, int64_t ldp, int64_t i0, int64_t ni,
                                                const T* Q, int64_t ldq, int64_t j0, int64_t nj,
                                                int64_t k0, int64_t k1,
-                                               f32x16_t (&acc)[SIDE / 64][SIDE / 64], int sum,
-                                               float (&sums)[SIDE / 64]) {
+                                               f32x16_t (&acc)[SIDE / 64][PAIR ? 2 : SIDE / 64], int sum,
+                                               float (&sums)[SIDE / 64], int64_t second = 0) {
+  constexpr int kQs = PAIR ? 2 : 1, kCols = PAIR ? 64 : SIDE;   // Qs, columns of each
   __shared__ __attribute__((aligned(16))) T lp[SIDE][kAnyPitch];
-  __shared__ __attribute__((aligned(16))) T lq[SIDE][kAnyPitch];
+  __shared__ __attribute__((aligned(16))) T lq[kQs * kCols][kAnyPitch];
   typedef typename Mfma<T>::vec vec;
-  constexpr int F = SIDE / 64;
+  constexpr int F = SIDE / 64, FN = PAIR ? 2 : F;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   AnySlab<T, PT, SIDE> sp;
-  AnySlab<T, QT, SIDE> sq;
-  if (k0 < k1) {
-    sp.load(P, ldp, i0, ni, k0, k1);
-    sq.load(Q, ldq, j0, nj, k0, k1);
-  }
+  AnySlab<T, QT, kCols> sq[kQs];
+  auto load = [&](int64_t k) {
+    sp.load(P, ldp, i0, ni, k, k1);
+#pragma unroll
+    for (int q = 0; q < kQs; ++q) sq[q].load(Q + q * second, ldq, j0, nj, k, k1);
+  };
+  if (k0 < k1) load(k0);
   for (int64_t k = k0; k < k1; k += kAnyDepth) {
     __syncthreads();   // the previous slab's reads are done
     sp.store(lp);
-    sq.store(lq);
+#pragma unroll
+    for (int q = 0; q < kQs; ++q) sq[q].store(lq + q * kCols);
     __syncthreads();
-    if (k + kAnyDepth < k1) {
-      sp.load(P, ldp, i0, ni, k + kAnyDepth, k1);
-      sq.load(Q, ldq, j0, nj, k + kAnyDepth, k1);
-    }
+    if (k + kAnyDepth < k1) load(k + kAnyDepth);
 #pragma unroll
     for (int ks = 0; ks < kAnyDepth / 16; ++ks) {
       const int kk = ks * 16 + 8 * (lane >> 5);
-      vec fp[F], fq[F];
+      vec fp[F], fq[FN];
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
+      for (int f = 0; f < F; ++f)
         fp[f] = *reinterpret_cast<const vec*>(&lp[((wave >> 1) * F + f) * 32 + (lane & 31)][kk]);
-        fq[f] = *reinterpret_cast<const vec*>(&lq[((wave & 1) * F + f) * 32 + (lane & 31)][kk]);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        const int row = PAIR ? f * kCols + (wave & 1) * 32 : ((wave & 1) * F + f) * 32;
+        fq[f] = *reinterpret_cast<const vec*>(&lq[row + (lane & 31)][kk]);
       }
 #pragma unroll
       for (int m = 0; m < F; ++m)
 #pragma unroll
-        for (int n = 0; n < F; ++n) acc[m][n] = Mfma<T>::run(fq[n], fp[m], acc[m][n]);
+        for (int n = 0; n < FN; ++n) acc[m][n] = Mfma<T>::run(fq[n], fp[m], acc[m][n]);
+      if constexpr (PAIR) continue;
       if (sum) {   // one branch for the waves that have none
         if (sum == 1) {
 #pragma unroll

@@ -268,12 +268,14 @@ void gated_grad_kernel(RowsProduct p, int tiles_n) {
   }
 }
 
-// Any width, pitch and alignment: 64x64 or 128x128 tiles through registers, the two projections one
-// after the other into accumulators of their own.
+// Any width, pitch and alignment: tiles of 64 or 128 rows through registers, the forward pass's by 64 columns
+// of either projection, which meet in one lane as in the tiles above.  (In two passes over the depth, one for
+// each projection, 128x128 tiles spilled 126 registers and 64x64 ones waited twice as long.)
 template <typename T, bool QT, int SIDE, bool GRADIENT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void any_gated_kernel(RowsProduct p, int tiles_n) {
   constexpr int F = SIDE / 64;
+  constexpr int kCols = GRADIENT ? SIDE : 64, FN = kCols / 64;   // columns of a tile, a wave's fragments of them
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t wide = GRADIENT ? p.cols : 2 * (int64_t)p.cols;   // columns of b
   RowTiles<SIDE> tiles(p.groups, p.rows);
@@ -281,28 +283,23 @@ void any_gated_kernel(RowsProduct p, int tiles_n) {
     int64_t row0, end;
     int group;
     tiles.find((int)(tile / tiles_n), &row0, &end, &group);
-    const int64_t j0 = (tile % tiles_n) * SIDE;
+    const int64_t j0 = (tile % tiles_n) * kCols;
     const T* b = static_cast<const T*>(p.b) + (int64_t)(group < 0 ? 0 : group) * wide * p.depth;
-    f32x16_t acc[F][F] = {}, up[F][F] = {};
+    f32x16_t acc[F][GRADIENT ? FN : 2] = {};
     float none[F] = {};
-    any_accumulate<T, false, QT, SIDE>(static_cast<const T*>(p.a), p.lda, row0, end, b,
-                                       QT ? wide : p.depth, j0, p.cols, 0, group < 0 ? 0 : p.depth,
-                                       acc, 0, none);
-    if constexpr (!GRADIENT)
-      any_accumulate<T, false, QT, SIDE>(static_cast<const T*>(p.a), p.lda, row0, end,
-                                         b + (QT ? (int64_t)p.cols : (int64_t)p.cols * p.depth),
-                                         QT ? wide : p.depth, j0, p.cols, 0,
-                                         group < 0 ? 0 : p.depth, up, 0, none);
+    any_accumulate<T, false, QT, SIDE, !GRADIENT>(
+        static_cast<const T*>(p.a), p.lda, row0, end, b, QT ? wide : p.depth, j0, p.cols, 0,
+        group < 0 ? 0 : p.depth, acc, 0, none, QT ? (int64_t)p.cols : (int64_t)p.cols * p.depth);
 #pragma unroll
     for (int m = 0; m < F; ++m) {
       const int64_t r = row0 + ((wave >> 1) * F + m) * 32 + (lane & 31);
       if (r >= end) continue;
 #pragma unroll
-      for (int n = 0; n < F; ++n) {
+      for (int n = 0; n < FN; ++n) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int64_t c =
-              j0 + ((wave & 1) * F + n) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+              j0 + ((wave & 1) * FN + n) * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
           if (c >= p.cols) continue;
           T* out = static_cast<T*>(p.out) + r * p.ldout + c;
           if constexpr (GRADIENT) {
@@ -313,7 +310,7 @@ void any_gated_kernel(RowsProduct p, int tiles_n) {
             out[0] = from_f32<T>(group < 0 ? 0.0f : dg);
             out[p.cols] = from_f32<T>(group < 0 ? 0.0f : du);
           } else {
-            float zg = acc[m][n][i], zu = up[m][n][i];
+            float zg = acc[m][0][i], zu = acc[m][1][i];
             if (p.bias && group >= 0) {
               const int64_t at = (int64_t)group * wide + c;
               const float* f = static_cast<const float*>(p.bias);
@@ -417,7 +414,7 @@ hipError_t gated_grad_variant(const RowsProduct& a, hipStream_t stream) {
 template <typename T, int SIDE, bool GRADIENT>
 hipError_t any_gated_side(const RowsProduct& a, hipStream_t stream) {
   const int64_t tiles_m = ceil64(a.rows, SIDE) + (a.groups.offsets ? a.groups.count + 1 : 0);
-  const int tiles_n = (int)ceil64(a.cols, SIDE);
+  const int tiles_n = (int)ceil64(a.cols, GRADIENT ? SIDE : 64);
   if (a.b_kmajor)
     any_gated_kernel<T, true, SIDE, GRADIENT>
         <<<grid_for(tiles_m * tiles_n), 256, 0, stream>>>(a, tiles_n);
@@ -429,7 +426,7 @@ hipError_t any_gated_side(const RowsProduct& a, hipStream_t stream) {
 
 template <typename T, bool GRADIENT>
 hipError_t any_gated(const RowsProduct& a, hipStream_t stream) {
-  return any_wide_tiles(a) ? any_gated_side<T, 128, GRADIENT>(a, stream)
+  return any_wide_tiles(as_rows(a, GRADIENT)) ? any_gated_side<T, 128, GRADIENT>(a, stream)
                            : any_gated_side<T, 64, GRADIENT>(a, stream);
 }
 
