@@ -140,6 +140,29 @@ def test_experts(gpu_lib, n, k, w_kn, offsets):
             H.assert_within(dz[s], want, err + H.half_step(want, t), f"dz {i}")
 
 
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("act", ["relu2", "gelu"])
+def test_experts_of_large_odd_widths(gpu_lib, w_kn, act):
+    """Enough odd rows and columns for the larger tiles of the kernels of any width, in both directions."""
+    t, rows, n, k, offsets = torch.float16, 4500, 1003, 45, [3, 1700, 1700, 4400]
+    off = torch.tensor(offsets, device="cuda")
+    x, dy, z = _mat(rows, k, t, 1, pitch=k + 2, shift=1), _mat(rows, k, t, 2, 0.1), _mat(rows, 2 * n, t, 3, pitch=2 * n + 1)
+    w, down = _weight(2 * n, k, t, 4, w_kn, (3,)), _weight(k, n, t, 5, w_kn, (3,))
+    bias = torch.randn(3, 2 * n, generator=torch.Generator().manual_seed(6)).to(t).cuda()
+    y, zz = gpu_lib.anvil_expert_gated_linear(x, w, off, bias, act=act, w_kn=w_kn, preact=_nan(rows, 2 * n, t=t),
+                                              out=_nan(rows, n, t=t))
+    dz = gpu_lib.anvil_expert_gated_grad_input(dy, down, off, z, act=act, w_kn=w_kn, out=_nan(rows, 2 * n, t=t))
+    for part in (y, zz, dz):
+        assert not part[:3].any() and not part[4400:].any()
+    for i in (0, 2):
+        s = slice(offsets[i], offsets[i + 1])
+        h, eh, zw, ez = G.forward(x[s].cpu(), w[i].cpu(), bias[i].cpu(), act, w_kn)
+        H.assert_within(y[s], h, eh + H.half_step(h, t), f"y {i}")
+        H.assert_within(zz[s], zw, ez + H.half_step(zw, t), f"z {i}")
+        want, err = G.grad(dy[s].cpu(), down[i].cpu(), z[s].cpu(), act, w_kn)
+        H.assert_within(dz[s], want, err + H.half_step(want, t), f"dz {i}")
+
+
 def test_offsets_past_32_bits(gpu_lib):
     """z and dz of more than 2^32 elements: their last rows, by the tiles and by the kernels of any width."""
     t, rows = torch.bfloat16, 800000
