@@ -579,13 +579,19 @@ def _parameter(t, name, code, like, device, shape):
     return _dense(t, name, t.dtype, device, shape), own
 
 
+def _stream_object(handle, stream):
+    """The torch stream of a handle that `stream` (None: the current one) has."""
+    torch = _module()
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)
+
+
 def _other_stream(stream):
     """`stream` as a torch stream where it is not the current one, else None."""
     torch = _module()
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == torch.cuda.current_stream().cuda_stream:
-        return None
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)
+    return None if handle == torch.cuda.current_stream().cuda_stream else _stream_object(handle, stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -1049,9 +1055,11 @@ class AdamW:
     `mantissas` a bf16 parameter may have an int16 or uint16 tensor (None for others): the low half of an
     fp32 master whose high half it is, as in anvil_bank_update.  state_bits is 32 (m and v in fp32) or 8 (m
     and sqrt(v) as float8_e4m3fn with an fp32 scale for each 256 elements), one for all or one each; states
-    that are not given start at zero.  lr_mul and wd_mul multiply a step's lr and weight decay, one for each
-    tensor.  The plan holds the tensors' addresses (and references to them): gradients that move to other
-    tensors are given to bind()."""
+    that are not given are zeros when the constructor returns.  lr_mul and wd_mul multiply a step's lr and weight
+    decay, one for each tensor.  The plan holds the tensors' addresses (and references to them): gradients that
+    move to other tensors are given to bind().  A step on another stream than the constructor's has it recorded as
+    a user of all of them, so that the object may be dropped while the step is queued; a graph that holds a
+    captured step needs the object for as long as it is replayed."""
 
     def __init__(self, params, grads, mantissas=None, state_bits=32, m=None, v=None, m_scale=None,
                  v_scale=None, lr_mul=None, wd_mul=None):
@@ -1107,6 +1115,7 @@ class AdamW:
                 row.v_scale = state(self.v_scale, "v_scale", i, torch.float32, blocks)
             row.lr_mul, row.wd_mul, row.state_bits = lr_mul[i], wd_mul[i], bits[i]
         self._plan = None
+        self._home, self._users = None, {}   # handle of the constructor's stream; other streams that steps ran on
         self.bind(grads)
 
     def bind(self, grads):
@@ -1136,10 +1145,23 @@ class AdamW:
         # stays where it is, so that a captured step follows
         words = torch.frombuffer(host, dtype=torch.int64)
         if self._plan is None:
-            self._plan = words.to(f"cuda:{self.device}") if count else None
+            if count:
+                self._plan, self._home = words.to(f"cuda:{self.device}"), _raw_stream(None, self.device)
         else:
             self._plan.copy_(words)
+        for user in self._users.values():
+            for g in grads:
+                g.record_stream(user)
         self.grads = grads   # last: until here the plan in memory names the gradients before
+
+    def _used_by(self, handle, stream):
+        """Takes note of another stream than the constructor's: the memory of what a plan holds is that one's, or
+        its owner's, and is not handed out again before what is queued on this stream has ended."""
+        user = self._users[handle] = _stream_object(handle, stream)
+        for tensors in (self.params, self.mantissas, self.grads, self.m, self.v, self.m_scale, self.v_scale, [self._plan]):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(user)
 
     def _arguments(self, grad_scale, stream):
         """(plan, its bytes, tensors), the grad_scale pointer and the stream's handle of a step."""
@@ -1153,12 +1175,12 @@ class AdamW:
             if grad_scale.numel() != 1:
                 raise ValueError("grad_scale must hold one value")
             scale = grad_scale.data_ptr()
-        if stream is not None and self._plan is not None:
-            other = _other_stream(stream)
-            if other is not None:
-                self._plan.record_stream(other)
-        plan = self._plan.data_ptr() if self._plan is not None else None
-        return (plan, self.plan_bytes, len(self.params)), scale, _raw_stream(stream, self.device)
+        handle = _raw_stream(stream, self.device)
+        if self._plan is None:
+            return (None, self.plan_bytes, len(self.params)), scale, handle
+        if handle != self._home and handle not in self._users:
+            self._used_by(handle, stream)
+        return (self._plan.data_ptr(), self.plan_bytes, len(self.params)), scale, handle
 
 
 def anvil_adamw(plan, lr, step, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, grad_scale=None, seed=None,

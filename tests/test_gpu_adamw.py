@@ -382,3 +382,34 @@ def test_other_stream(gpu_lib):
     gpu_lib.anvil_adamw(plan, 1e-3, 1, betas=BETAS, eps=EPS, weight_decay=0.1, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     _compare(plan, [A.step32(s, 0, 1e-3, 0.1, BETAS, EPS, 1, None, 1)])
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_dropped_with_a_step_queued_on_another_stream(gpu_lib, bits, given):
+    """The memory of the object's own states and plan is not handed out before the step has run, whether the stream is
+    given or the current one."""
+    n = 3 << 20
+    side = torch.cuda.Stream()
+    p, g = torch.ones(n, device="cuda"), torch.ones(n, device="cuda")
+    plan = gpu_lib.AdamW([p], [g], state_bits=bits)
+    held = [t for t in (plan.m[0], plan.v[0], plan.m_scale[0], plan.v_scale[0], plan._plan) if t is not None]
+    sizes, was = [t.numel() * t.element_size() for t in held], {t.data_ptr() for t in held}
+    del held
+    a = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(a)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(100):          # about a millisecond each
+            torch.mm(a, a, out=out)
+        if not given:
+            gpu_lib.anvil_adamw(plan, 1e-2, 1, betas=BETAS, eps=EPS)
+    if given:
+        gpu_lib.anvil_adamw(plan, 1e-2, 1, betas=BETAS, eps=EPS, stream=side)
+    del plan
+    fresh = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in sizes for _ in range(4)]
+    again = was & {t.data_ptr() for t in fresh}
+    assert side.query() or not again
+    torch.cuda.synchronize()
+    # m = 0.1, v = 0.05: the update is lr * 1 / (1 + eps)
+    assert ((p - (1 - 1e-2)).abs() < 1e-6).all()
