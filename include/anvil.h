@@ -455,8 +455,8 @@ size_t anvil_cross_entropy_grad_workspace(int want_dx, int want_dw, int w_kn, in
  * Per element in fp32, every operation rounded on its own:
  *   g = grad * grad_scale;  m = m beta1 + g (1 - beta1);  v = v beta2 + (g g) (1 - beta2);
  *   p = p (1 - lr wd) - lr ((m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps))
- * with lr * lr_mul and weight_decay * wd_mul of the tensor as lr and wd (both corrections are formed in
- * double and applied as fp32 factors).
+ * with lr * lr_mul and weight_decay * wd_mul of the tensor as lr and wd.  The corrections are applied as fp32
+ * factors, 1 / (1 - beta1^t) and 1 / sqrt(1 - beta2^t), which anvil_adamw forms in double and rounds once.
  * ------------------------------------------------------------------------------------------ */
 typedef struct anvil_adamw_tensor {
   void* param;          /* [count] of param_dtype: rounded to it once, to nearest even, ... */
@@ -490,7 +490,9 @@ int anvil_adamw(const void* plan, size_t plan_bytes, int64_t tensors, float lr, 
                 const float* grad_scale, void* stream);
 
 /* The same with the per-step values read from the device when the kernel runs (graph-capturable): fp32
- * scalars[5] = lr, weight_decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24). */
+ * scalars[5] = lr, weight_decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24).  The
+ * corrections' factors are the fp32 reciprocals of these fp32 numbers, rounded twice where anvil_adamw rounds once:
+ * m, v and scales are the same bits as its, weights may differ by 2^-20 of the update ahead of their rounding. */
 int anvil_adamw_dev(const void* plan, size_t plan_bytes, int64_t tensors, const float* scalars,
                     double beta1, double beta2, double eps, const float* grad_scale, void* stream);
 

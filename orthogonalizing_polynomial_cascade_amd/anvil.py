@@ -1198,7 +1198,9 @@ def anvil_adamw(plan, lr, step, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, g
 
 def anvil_adamw_dev(plan, scalars, betas=(0.9, 0.95), eps=1e-8, grad_scale=None, stream=None):
     """anvil_adamw with the step's values read from the device when it runs (for a captured graph): scalars
-    fp32 [5] = lr, weight decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24)."""
+    fp32 [5] = lr, weight decay, 1 - beta1^t, sqrt(1 - beta2^t), seed (a whole number below 2^24).  The corrections'
+    reciprocals are formed from these fp32 numbers: weights may differ from anvil_adamw's (ahead of their rounding by 2^-20
+    of the update), states do not."""
     head, scale, handle = plan._arguments(grad_scale, stream)
     _same(scalars, "scalars", _torch.float32, plan.device)
     if scalars.numel() < 5 or not scalars.is_contiguous():

@@ -413,3 +413,70 @@ def test_dropped_with_a_step_queued_on_another_stream(gpu_lib, bits, given):
     torch.cuda.synchronize()
     # m = 0.1, v = 0.05: the update is lr * 1 / (1 + eps)
     assert ((p - (1 - 1e-2)).abs() < 1e-6).all()
+
+
+def _dev_step32(s, i, scalars, clip):
+    """A.step32 with the corrections as the device forms them: fp32 reciprocals of the scalars."""
+    lr, wd, one1, root2, seed = (np.float32(v) for v in scalars)
+
+    def weights(p, m, root, lr, wd, betas, eps, step):
+        fix1, fix2 = np.float32(1) / one1, np.float32(1) / root2
+        with np.errstate(all="ignore"):
+            return A._t(A._f(p) * (A._f(1.0) - lr * wd) - lr * ((A._f(m) * fix1) / (A._f(root) * fix2 + A._f(eps))))
+
+    with pytest.MonkeyPatch.context() as patch:
+        patch.setattr(A, "weights", weights)
+        return A.step32(s, i, lr, wd, BETAS, EPS, None, clip, int(seed))
+
+
+SCALARS = (3e-3, 0.1, 1 - BETAS[0] ** 7, math.sqrt(1 - BETAS[1] ** 7), 12345)
+# each of them changed alone (lr, weight decay, both corrections, seed), and the extremes of the seed
+CHANGES = [{}, {0: 5e-4}, {1: 0.0}, {1: 0.5}, {2: 1 - BETAS[0]}, {3: 1.0}, {4: 0}, {4: (1 << 24) - 1}]
+
+
+def _dev_states():
+    kinds = [("split", "bf16", 8), ("fp32", "fp32", 32), ("fp16", "fp16", 8), ("split", "bf16", 32), ("fp32", "bf16", 8)]
+    return [_state(n, *kinds[i % 5], 7 * i, 1 + 0.5 * (i % 3), 0.5 + i % 2) for i, n in enumerate((5000, 2049, 300, 257, 40000))]
+
+
+def test_scalar_changes_show_in_the_oracle():
+    """What the next test compares depends on every scalar: each change gives other weights, or other codes."""
+    states = _dev_states()
+    base = [_dev_step32(s, i, SCALARS, 0.3) for i, s in enumerate(states)]
+    for change in CHANGES[1:]:
+        other = [_dev_step32(s, i, [change.get(k, v) for k, v in enumerate(SCALARS)], 0.3) for i, s in enumerate(states)]
+        for a, b, s in zip(base, other, states):
+            if 4 in change:
+                assert torch.equal(a["param"], b["param"])
+                assert s["m_scale"] is None or not torch.equal(a["m"].view(torch.uint8), b["m"].view(torch.uint8))
+            else:
+                low = "param" if a["mantissa"] is None else "mantissa"
+                assert not torch.equal(a[low], b[low]), change
+
+
+@pytest.mark.parametrize("change", CHANGES, ids=str)
+def test_device_scalars_bit_for_bit(gpu_lib, change):
+    """Every scalar, read from the device, against the same operations on the CPU: weights, low halves, states, scales."""
+    scalars = [change.get(k, v) for k, v in enumerate(SCALARS)]
+    states = _dev_states()
+    plan = _plan(gpu_lib, states)
+    gpu_lib.anvil_adamw_dev(plan, torch.tensor(scalars, dtype=torch.float32, device="cuda"), betas=BETAS, eps=EPS,
+                            grad_scale=torch.tensor([0.3], device="cuda"))
+    _compare(plan, [_dev_step32(s, i, scalars, 0.3) for i, s in enumerate(states)])
+
+
+def test_device_corrections_differ_from_the_hosts_by_their_roundings(gpu_lib):
+    """The factor 1 / (1 - beta1^t) is off by at most 2^-24 of itself from the host and by 2 * 2^-24 + 2^-48 from the
+    device (its divisor is a number of 32 bits, and so is the quotient), the root's likewise: the quotients of an
+    update are apart by at most 6 * 2^-24 and, with four roundings more in either, 14 * 2^-24 of the update, and the
+    weights by that and their own last rounding."""
+    u = 2.0 ** -24
+    s = _state(100000, "fp32", "bf16", 32, 3)
+    for step in (1, 7, 1000):
+        host, dev = _plan(gpu_lib, [s]), _plan(gpu_lib, [s])
+        gpu_lib.anvil_adamw(host, 1e-2, step, betas=BETAS, eps=EPS)
+        gpu_lib.anvil_adamw_dev(dev, torch.tensor([1e-2, 0, 1 - BETAS[0] ** step, math.sqrt(1 - BETAS[1] ** step), 0],
+                                                  device="cuda"), betas=BETAS, eps=EPS)
+        a, b, was = (t.double().cpu() for t in (host.params[0], dev.params[0], s["param"]))
+        assert ((a - b).abs() <= 14 * u * (a - was).abs() * (1 + 1e-3) + 2 * u * (a.abs() + was.abs())).all()
+        assert torch.equal(host.m[0], dev.m[0]) and torch.equal(host.v[0], dev.v[0])
