@@ -338,3 +338,29 @@ def test_other_stream(gpu_lib):
     torch.cuda.current_stream().wait_stream(side)
     for a, b in ((loss, loss2), (lse, lse2), (dx, dx2), (dw, dw2)):
         assert torch.equal(a, b)
+
+
+# pieces of 1792 entries and a ragged rest; and so many rows that the least piece, 1024 entries, is taken
+@pytest.mark.parametrize("rows,vocab,k,w_kn,kind", [(270000, 2500, 16, False, "bf16"), (270000, 2500, 16, True, "bf16"),
+                                                    (270000, 2500, 16, False, "fp16"), (270000, 2500, 16, True, "fp16"),
+                                                    ((1 << 20) + 5, 1100, 8, False, "bf16")])
+def test_several_pieces_of_every_row(gpu_lib, monkeypatch, rows, vocab, k, w_kn, kind):
+    """A gradient at every row's loss: loss, log-sum-exp, dx and dw of all rows and entries against 64 bits, which are
+    formed on the GPU (the plain forms fetch nothing here)."""
+    t = TYPES[kind]
+    x, w = _mat(rows, k, t, 1), _weight(vocab, k, t, 2, w_kn)
+    targets = _targets(rows, vocab, 3, torch.int32)
+    dloss = (torch.randn(rows, generator=torch.Generator().manual_seed(4)) / rows).cuda()
+    loss, lse = gpu_lib.anvil_cross_entropy(x, w, targets, w_kn=w_kn)
+    dx, dw = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, dloss, w_kn=w_kn, out=_nan(rows, k, t=t),
+                                              dw_out=_nan(*w.shape, t=torch.float32))
+    torch.cuda.synchronize()
+    with monkeypatch.context() as patch:
+        patch.setattr(torch.Tensor, "cpu", lambda self: self)
+        (lw, el), (sw, es) = C.forward(x, w, targets, w_kn)
+        (xw, ex), (ww, ew) = C.gradients(x, w, targets, lse, dloss, w_kn, t)
+    assert int(C.counts_of(targets, vocab).sum()) > 0.8 * rows and (ww.abs() > ew).double().mean() > 0.9   # bounds that say something
+    H.assert_within(loss, lw, el, "loss")
+    H.assert_within(lse, sw, es, "lse")
+    H.assert_within(dx, xw, ex + H.half_step(xw, t), "dx")
+    H.assert_within(dw, ww, ew + H.half_step(ww, torch.float32), "dw")
