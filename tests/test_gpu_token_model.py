@@ -66,3 +66,43 @@ def test_training_runs(gpu_lib, state_bits):
         assert torch.isfinite(now.float()).all() and not torch.equal(now, old), name
     losses = M.train(steps=2, rows=128, vocab=200, width=64, hidden=64, blocks=1, state_bits=state_bits)
     assert len(losses) == 2 and all(v == v and abs(v) < float("inf") for v in losses)
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_updates_are_the_operators(gpu_lib, state_bits):
+    """Two steps: every parameter goes against its gradient in the first, the bank's as a bank update of a copy with the
+    same gradients and settings and the others' as the AdamW formula on the CPU, bit for bit."""
+    from orthogonalizing_polynomial_cascade_amd import token_model as M
+    from tests import adamw_helpers as A
+    model = M.TokenModel(300, 64, 128, 2, seed=1, state_bits=state_bits)
+    names, dloss = ("embedding", "head", "norms"), torch.full((256,), 1 / 256, device="cuda")
+    flat = lambda t: None if t is None else t.detach().cpu().reshape(-1).clone()  # noqa: E731
+    for step in range(2):
+        tokens = M.sequence(256, 300, step)
+        _, kept = model.loss(tokens[:-1], tokens[1:])
+        grads = {name: g.clone() for name, g in model.gradients(dloss, kept).items()}
+        before = {name: getattr(model, name).clone() for name in names + ("bank",)}
+        adam, states = model.adam, []
+        for i, name in enumerate(names):
+            s = {k: flat(v[i]) for k, v in (("param", adam.params), ("mantissa", adam.mantissas), ("grad", adam.grads), ("m", adam.m),
+                                            ("v", adam.v), ("m_scale", adam.m_scale), ("v_scale", adam.v_scale))}
+            assert torch.equal(s["grad"], flat(grads[name]))
+            states.append(s | {"lr_mul": 1.0, "wd_mul": 0.0 if name == "norms" else 1.0})
+        bank = [t.clone() for t in (model.velocity, model.energy, model.bank, model.mantissa)]
+        model.update(step)
+        # the clipping coefficient as a model's user would have it: a norm over all that AdamW takes
+        norm = torch.stack([grads[name].float().norm() for name in names]).norm()
+        clip = float(torch.clamp(M.CLIP / (norm + 1e-6), max=1.0))
+        for i, name in enumerate(names):
+            want = A.step32(states[i], i, model.adam_lr, 0.01, (0.9, 0.95), 1e-8, step + 1, clip, step + 1)
+            for key, have in (("param", adam.params), ("mantissa", adam.mantissas), ("m", adam.m), ("v", adam.v)):
+                if want[key] is not None:
+                    kind = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[want[key].element_size()]
+                    assert torch.equal(flat(have[i]).view(kind), want[key].view(kind)), (step, name, key)
+        velocity, energy, weights, mantissa = bank
+        gpu_lib.anvil_bank_update(grads["bank"], velocity, *gpu_lib.rail_scalars(step), energy, 0.95, weights, mantissa, 0.0,
+                                  model.eff_lr)
+        assert torch.equal(weights.view(torch.int16), model.bank.view(torch.int16)) and torch.equal(mantissa, model.mantissa)
+        if step == 0:   # no state yet that could point elsewhere
+            for name, old in before.items():
+                assert float(((getattr(model, name).double() - old.double()) * grads[name].double()).sum()) < 0, name
