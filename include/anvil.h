@@ -439,6 +439,7 @@ size_t anvil_cross_entropy_workspace(int w_kn, int in_place, int64_t rows, int64
  *   dloss      fp32 [rows]: the gradient that reaches each row's loss (1 / rows for their mean)
  *   dx         dtype [rows][k], dw of dw_dtype (ANVIL_F32 or dtype) as w; each may be NULL
  *   workspace  anvil_cross_entropy_grad_workspace bytes (want_dx, want_dw: whether dx, dw are given)
+ *              of which P takes up to 1 GiB, or 2 KiB a row from 2^19 rows on
  * P is formed by pieces of the vocabulary and rounded to dtype (fp16: scaled by a power of two first) for
  * the two products, whose sums are fp32: dw in fp32 holds the sums of the rounded P.  dw is zeros when
  * there are no rows. */

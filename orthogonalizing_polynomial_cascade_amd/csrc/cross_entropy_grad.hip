@@ -474,7 +474,8 @@ HeadWeightPlan head_weight_plan(int64_t rows, int64_t entries, int64_t depth) {
 }
 
 // Columns of the vocabulary at a time: as many as give dW whole rounds of 256x256 tiles on the CUs, with
-// up to 2^29 elements of P.  Loss and gradients of 16384 rows, 768 x 50304, dx on 256x256 tiles: 5610 us by
+// up to 2^29 elements of P (1 GiB), but no fewer than 1024, since every piece reads and writes dx's sums: from 2^19
+// rows on P has 1024 columns, 8 GiB at the most rows that a call takes.  Loss and gradients of 16384 rows, 768 x 50304, dx on 256x256 tiles: 5610 us by
 // 21760 columns (255 tiles of dW), 5690 by 16384 (192), 5790 by 25344 (297).
 int64_t piece_of(int64_t rows, int64_t vocab, int64_t depth) {
   const int64_t most =

@@ -79,3 +79,14 @@ def test_binding_refuses_before_the_library():
         anvil.anvil_cross_entropy_grad(cpu, cpu, t, t.float(), t.float())
     with pytest.raises(TypeError):
         anvil.anvil_cross_entropy([1.0], cpu, t)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 1 << 22), (16384, 50304), (1 << 18, 1 << 19), ((1 << 19) - 1, 100000),
+                                        (1 << 20, 1 << 17), (1 << 22, 1 << 15)])
+def test_what_the_probabilities_take(lib, rows, vocab):
+    """P takes up to 1 GiB, or 2 KiB a row; beside it dx's sums (one for each of 8 columns here) and planes of partial sums,
+    of which dx's end at 2.7e8 bytes and dw's at 1.1e9."""
+    for want in ((1, 0), (0, 1), (1, 1)):
+        need = lib.anvil_cross_entropy_grad_workspace(*want, 0, 3, BF16, rows, vocab, 8)
+        p = max(1 << 30, 2048 * rows)
+        assert 0 < need <= p + want[0] * (rows * 32 + 270_000_000) + want[1] * 1_100_000_000 + 4096
