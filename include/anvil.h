@@ -425,7 +425,7 @@ int anvil_expert_gated_grad_input(const void* dy, int64_t lddy, const void* w, i
  *              aligned and ldx (k for a single row) a multiple of 8, plus ANVIL_W_IN_PLACE where w is
  *              16-byte aligned.  What is not, or has a row of another length than a multiple of 8, is
  *              copied there first, and it is larger.
- * rows <= 2^22, 1 <= vocab <= 2^22, vocab * k <= 2^30, rows * vocab and rows * k <= 2^37. */
+ * rows <= 2^22, 1 <= vocab <= 2^22, k <= 2^22, vocab * k < 2^31, rows * vocab and rows * k <= 2^37. */
 enum anvil_in_place { ANVIL_X_IN_PLACE = 1, ANVIL_W_IN_PLACE = 2 };
 int anvil_cross_entropy(const void* x, int64_t ldx, const void* w, int w_kn, const void* targets,
                         int target_bits, float* loss, float* lse, int dtype, int64_t rows,

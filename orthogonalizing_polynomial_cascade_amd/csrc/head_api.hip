@@ -17,8 +17,10 @@ int check_head(int dtype, int w_kn, int target_bits, int64_t rows, int64_t vocab
     return anvil::elem_known(dtype) ? ANVIL_ERR_UNSUPPORTED : ANVIL_ERR_INVALID_ARG;
   if ((w_kn != 0 && w_kn != 1) || (target_bits != 32 && target_bits != 64)) return ANVIL_ERR_INVALID_ARG;
   if (rows < 0 || vocab < 1 || k < 0) return ANVIL_ERR_INVALID_ARG;
+  // Offsets within a tile depend on widths and pitches alone and addresses are 64-bit: the bounds on the products
+  // keep their tiles within a launch's grid (2^31 weights: 2^17 tiles of dw) and the workspace within memory.
   if (rows > (int64_t(1) << 22) || vocab > anvil::kMaxWidth || k > anvil::kMaxWidth ||
-      vocab * k > (int64_t(1) << 30) || rows * vocab > (int64_t(1) << 37) ||
+      vocab * k >= (int64_t(1) << 31) || rows * vocab > (int64_t(1) << 37) ||
       rows * k > (int64_t(1) << 37))
     return ANVIL_ERR_UNSUPPORTED;
   return ANVIL_OK;

@@ -364,3 +364,27 @@ def test_several_pieces_of_every_row(gpu_lib, monkeypatch, rows, vocab, k, w_kn,
     H.assert_within(lse, sw, es, "lse")
     H.assert_within(dx, xw, ex + H.half_step(xw, t), "dx")
     H.assert_within(dw, ww, ew + H.half_step(ww, torch.float32), "dw")
+
+
+@pytest.mark.parametrize("w_kn", [False, True])
+def test_more_than_2_30_weights(gpu_lib, monkeypatch, w_kn):
+    """A head whose gradient's last entries lie past 2^30 elements and 2^32 bytes: everything against 64 bits on the GPU."""
+    t, rows, vocab, k = torch.bfloat16, 70, 152064, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, k, generator=g, device="cuda").to(t)
+    w = torch.empty((k, vocab) if w_kn else (vocab, k), dtype=t, device="cuda").normal_(0, 2 * k ** -0.5, generator=g)
+    targets = _targets(rows, vocab, 3)
+    dloss = (torch.randn(rows, generator=torch.Generator().manual_seed(4)) / rows).cuda()
+    loss, lse = gpu_lib.anvil_cross_entropy(x, w, targets, w_kn=w_kn)
+    dx, dw = gpu_lib.anvil_cross_entropy_grad(x, w, targets, lse, dloss, w_kn=w_kn, out=_nan(rows, k, t=t),
+                                              dw_out=_nan(*w.shape, t=torch.float32))
+    torch.cuda.synchronize()
+    with monkeypatch.context() as patch:
+        patch.setattr(torch.Tensor, "cpu", lambda self: self)
+        (lw, el), (sw, es) = C.forward(x, w, targets, w_kn)
+        (xw, ex), (ww, ew) = C.gradients(x, w, targets, lse, dloss, w_kn, t)
+        H.assert_within(loss, lw, el, "loss")
+        H.assert_within(lse, sw, es, "lse")
+        H.assert_within(dx, xw, ex + H.half_step(xw, t), "dx")
+        ew += H.half_step(ww, torch.float32)
+        H.assert_within(dw, ww, ew, "dw")

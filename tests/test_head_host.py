@@ -90,3 +90,14 @@ def test_what_the_probabilities_take(lib, rows, vocab):
         need = lib.anvil_cross_entropy_grad_workspace(*want, 0, 3, BF16, rows, vocab, 8)
         p = max(1 << 30, 2048 * rows)
         assert 0 < need <= p + want[0] * (rows * 32 + 270_000_000) + want[1] * 1_100_000_000 + 4096
+
+
+def test_heads_of_more_than_2_30_weights(lib):
+    """A vocabulary of 152064 entries at a width of 8192 is taken; 2^31 weights are not."""
+    for kn in (0, 1):
+        for vocab, k in ((152064, 8192), (1 << 22, 511), (511, 1 << 22), ((1 << 20) - 1, 1 << 11)):
+            assert lib.anvil_cross_entropy_workspace(kn, 3, 10, vocab, k) > 0, (vocab, k)
+            assert lib.anvil_cross_entropy_grad_workspace(1, 1, kn, 3, BF16, 10, vocab, k) > 0, (vocab, k)
+        for vocab, k in ((1 << 20, 1 << 11), (1 << 22, 512)):
+            assert lib.anvil_cross_entropy_workspace(kn, 3, 10, vocab, k) == 0
+            assert lib.anvil_cross_entropy_grad_workspace(1, 1, kn, 3, BF16, 10, vocab, k) == 0
