@@ -1121,7 +1121,9 @@ class AdamW:
     def bind(self, grads):
         """Takes the gradients from other tensors from the next step on, a captured step's replays too.  It
         writes the plan on the current stream (not while that is captured): steps on other streams have to be
-        ordered with it.  A refused call leaves the plan and its gradients as they were."""
+        ordered with it.  A refused call leaves the plan and its gradients as they were.  All tensors are checked
+        and the whole plan is made again on the host, so gradients are better written to the same tensors step after
+        step."""
         torch = _module()
         if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("a plan is written from host memory, which a graph cannot capture")

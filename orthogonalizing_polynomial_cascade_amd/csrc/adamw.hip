@@ -126,8 +126,9 @@ __device__ __forceinline__ void store_weights(const AdamwTensor& t, int64_t at, 
   }
 }
 
-// Square roots, correctly rounded, of values that are not negative.  The hardware's is within a step; the
-// neighbour is right if the product with it lies on the other side.  Below 2^-96 those products lose
+// Square roots, correctly rounded, of values that are not negative, by Tuckerman's test (Agarwal and others, IBM J.
+// Res. Dev. 30, 1986): the hardware's root is within a step, and its neighbour is right if the product with it
+// lies on the other side of the value.  Below 2^-96 those products lose
 // bits: a wave that has such a value takes the compiler's root, which scales.
 __device__ __forceinline__ void roots(const float v[kPer], float r[kPer]) {
   uint32_t least = ~0u;   // of bits - 1: zeros, infinities and NaN are far up

@@ -96,8 +96,10 @@ struct AnySlab {
   }
 };
 
-// A second slab on its way in tiles of 64 rows gained nothing (517 rows, 2002 x 513: 14.1 us as it is, 16.3 with it; its
-// input gradient 35.6 and 36.8).
+// A slab with an edge is what odd widths wait for: edge() shifts a piece right behind its load and in a branch of its
+// own, so the compiler waits for each such load before it issues the next, two an operand and slab in tiles of 64
+// rows and four in those of 128.  A second slab on its way in tiles of 64 rows gained nothing while that is so (517
+// rows, 2002 x 513: 14.1 us as it is, 16.3 with it; its input gradient 35.6 and 36.8).
 //
 // acc (the wave's fragments, C transposed: register r of lane l is row l%32, column
 // 8(r/4) + 4(l/32) + r%4 of a fragment) of the tile's k range [k0, k1).  `sum`: 1 the wave also adds

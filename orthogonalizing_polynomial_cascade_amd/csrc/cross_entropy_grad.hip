@@ -386,7 +386,8 @@ double join_cost(int splits, double bytes) {
 }
 
 // Tile and splits of dx's product: the least of these.  The depth is a piece of the vocabulary, so few rows
-// leave most CUs idle for long without splits.  Us by tile/splits with the join, the choice first (rows x
+// leave most CUs idle for long without splits.  The planes of a split take at most 2.7e8 bytes, which bounds the
+// workspace; the sweep went no further.  Us by tile/splits with the join, the choice first (rows x
 // width, depth):
 //    256 x  768, 16384   128/16        21   64/4  24   256/16 32   128/1 159   256/1  278
 //    512 x  768, 50304   128/16        54   64/8  88   256/16 73   128/1 487   256/1  829
@@ -447,7 +448,8 @@ hipError_t weight_side(const WeightGrad& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The same for dW, whose depth is the rows (at least 256 a split).
+// The same for dW, whose depth is the rows (at least 256 a split).  Its planes take at most 1.1e9 bytes, about what P
+// does.
 struct HeadWeightPlan {
   int side, splits;
 };

@@ -441,7 +441,9 @@ __global__ __launch_bounds__(256) void gated_activation_kernel(RowsProduct p) {
   }
 }
 
-// The product's shape as the tile choice sees it: a gated product has twice the output's columns.
+// The product's shape as the tile choice sees it: a gated product has twice the output's columns.  The choice is
+// the linear layers' fitted cost, which no sweep of the gated products' own tiles has been taken for; 32768 rows,
+// 768 -> 2 x 2816 on either side of it stand at the head of this file.
 RowsProduct as_rows(const RowsProduct& a, bool gradient) {
   RowsProduct r = a;
   r.cols = gradient ? a.cols : 2 * a.cols;
